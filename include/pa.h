@@ -14,6 +14,11 @@
  *                    table; decode rows, chunked-prefill/extend rows, prefix
  *                    hits and the shared-prefix (cascade) route;
  *   pa_zero_blocks   device: clear newly allocated cache blocks (§4, §5.1.1);
+ *   pa_rotary        device: rotate query / key rows by their positions;
+ *   pa_append_kv     device: the cache write with the rotation on the way, into
+ *                    every cache type (block-scaled 8-bit caches included);
+ *   pa_attention_scaled
+ *                    device: attention over block-scaled 8-bit caches;
  *   pa_attention_with_kv_update
  *                    device: the cache write and attention as one call (§6.1,
  *                    fused dispatch).
@@ -38,7 +43,7 @@
  * at absolute position num_computed_tokens[r] + i and attends to keys
  * 0..position (bottom-right causal alignment).
  *
- * Supported: head_dim 64 or 128 (128 only with FP8 caches), block_size 16,
+ * Supported: head_dim 64 or 128 (128 only with PA_KV_FP8_E4M3 caches), block_size 16,
  * Hq % Hkv == 0 with the group size G = Hq/Hkv at most 128 (groups of more
  * than 16 query heads run every row on the tensor-core tiles), num_blocks *
  * 16 < 2^31.  Other shapes return PA_ERR_UNSUPPORTED.
@@ -117,9 +122,10 @@ typedef struct {
                                             selects the cascade route              */
     float softmax_scale;           /* scores are softmax_scale * <q, k>; must be > 0   */
     int32_t num_sms;               /* SMs to plan for; 0 = query the current device    */
-    int32_t kv_cache_dtype;        /* PA_KV_BF16 or PA_KV_FP8_E4M3                      */
-    float k_scale;                 /* FP8 caches: a key reads code_value * k_scale     */
-    float v_scale;                 /* FP8 caches: a value reads code_value * v_scale   */
+    int32_t kv_cache_dtype;        /* one of PA_KV_*                                    */
+    float k_scale;                 /* PA_KV_FP8_E4M3: a key reads code_value * k_scale */
+    float v_scale;                 /* PA_KV_FP8_E4M3: a value, code_value * v_scale
+                                      (the other cache types ignore both)              */
 } pa_batch_desc;
 
 /* Element type of the K/V caches ("vLLM 推理流程分析" §6.3: kv_cache_dtype, FP8
@@ -128,6 +134,17 @@ typedef struct {
  * 448, S.1111.111 = NaN) in the same [num_blocks][16][Hkv][D] layout. */
 #define PA_KV_BF16 0
 #define PA_KV_FP8_E4M3 1
+
+/* Block-scaled caches: one 8-bit code per element in the same layout, and for
+ * each of K and V a float array scales [num_blocks][Hkv]: element (block b,
+ * row, kv head h, d) reads code_value * scales[b][h].  Codes are E4M3 (as
+ * above) or signed 8-bit integers (-127 .. 127 as pa_append_kv writes them;
+ * -128 reads as -128).  head_dim 64 or 128.  Plans of these types go with
+ * pa_attention_scaled / pa_attention_scaled_launch alone: the attention calls
+ * without scales refuse them (PA_ERR_INVALID_ARGUMENT), pa_graph_create does
+ * too (PA_ERR_UNSUPPORTED). */
+#define PA_KV_FP8_E4M3_BLOCK 2
+#define PA_KV_INT8_BLOCK 3
 
 /* Work decomposition of a plan (for tests, benchmarks and launch counts). */
 typedef struct {
@@ -141,7 +158,7 @@ typedef struct {
     int32_t num_partial_slots;     /* (token, partition) partial results              */
     int32_t num_merge_rows;        /* tokens whose output is merged from partials     */
     int32_t kernels_per_call;      /* kernel launches one pa_attention call makes     */
-    int32_t num_dequant_blocks;    /* FP8: cache blocks the tensor-core tiles read,
+    int32_t num_dequant_blocks;    /* 8-bit caches: blocks the tensor-core tiles read,
                                       expanded to bf16 in the workspace each call   */
     int64_t decode_kv_bytes;       /* K+V bytes the decode kernel's rows must read    */
     int64_t prefix_kv_bytes;       /* K+V bytes of the shared prefix (read once)      */
@@ -444,7 +461,8 @@ pa_status pa_attention_with_kv_update_launch_staged(const pa_plan_t *plan, const
  *                    non-NULL)
  *   key_cache,
  *   value_cache      DEVICE, 16-byte aligned, [num_blocks][16][Hkv][D] of
- *                    kv_cache_dtype (PA_KV_BF16 or PA_KV_FP8_E4M3)
+ *                    kv_cache_dtype (any PA_KV_*; code 0 of a block-scaled
+ *                    cache reads 0 under every scale, so scales stay)
  * Returns PA_ERR_INVALID_ARGUMENT for a negative count or size, a NULL or
  * misaligned pointer, or an unknown kv_cache_dtype; PA_ERR_CUDA on a launch
  * failure.  Enqueue before the step's pa_write_kv.
@@ -452,6 +470,163 @@ pa_status pa_attention_with_kv_update_launch_staged(const pa_plan_t *plan, const
 pa_status pa_zero_blocks(const int32_t *block_ids, int32_t num_ids, int32_t num_blocks, int32_t num_heads_kv,
                          int32_t head_dim, int32_t kv_cache_dtype, void *key_cache, void *value_cache,
                          int32_t *device_error_word, void *stream);
+
+/*
+ * Rotary positions.  A row's pair i (of rotary_dim / 2) at position p turns by
+ * the angle a = p * f_i:
+ *   (x, y) -> m * (x cos a - y sin a, y cos a + x sin a),
+ * f_i = base^(-2 i / rotary_dim), m = 1, changed for long contexts by `scaling`
+ * with s = factor, L = original_max_position:
+ *   NONE        f_i
+ *   LINEAR      f_i / s                       (positions interpolated)
+ *   WAVELENGTH  f_i (u + (1 - u) / s), u = (L f_i / 2 pi - low) / (high - low)
+ *               clamped to [0, 1]: pairs of at most `low` turns over the
+ *               original context are interpolated, those of `high` or more kept
+ *   YARN        f_i (r / s + 1 - r), r = (i - i_lo) / (i_hi - i_lo) clamped to
+ *               [0, 1], i_lo = floor(at(high)) >= 0, i_hi = ceil(at(low)) <=
+ *               rotary_dim - 1, at(t) = rotary_dim ln(L / 2 pi t) / (2 ln base);
+ *               m = 0.1 ln s + 1      ("YaRN: Efficient Context Window Extension
+ *               of Large Language Models", low = beta_slow, high = beta_fast)
+ * attention_factor > 0 replaces m (0: as above).  Elements from rotary_dim on
+ * pass through unchanged.  The inverse rotation, and the gradient of the
+ * rotation, is the rotation by negated positions (times m as well).
+ */
+#define PA_ROPE_HALF 0          /* pair i is elements i and i + rotary_dim / 2 */
+#define PA_ROPE_INTERLEAVED 1   /* pair i is elements 2 i and 2 i + 1          */
+#define PA_ROPE_SCALE_NONE 0
+#define PA_ROPE_SCALE_LINEAR 1
+#define PA_ROPE_SCALE_WAVELENGTH 2
+#define PA_ROPE_SCALE_YARN 3
+
+typedef struct {
+    int32_t rotary_dim;            /* > 0, a multiple of 8, at most 256                  */
+    int32_t layout;                /* PA_ROPE_HALF or PA_ROPE_INTERLEAVED                */
+    int32_t scaling;               /* PA_ROPE_SCALE_*                                    */
+    int32_t original_max_position; /* L > 0 (WAVELENGTH, YARN)                           */
+    double base;                   /* > 0 (YARN: > 1)                                    */
+    double factor;                 /* s > 0 (all but NONE)                               */
+    double low, high;              /* 0 < low < high, turns (WAVELENGTH, YARN)           */
+    double attention_factor;       /* m, or 0 for the scaling's own                      */
+} pa_rope_desc;
+
+typedef struct pa_rope_s pa_rope_t;
+
+/*
+ * Build a rotation (host memory only, no CUDA call; owned by the library until
+ * pa_rope_destroy; immutable, so any number of threads, streams, devices and
+ * captured graphs may use it: calls copy what the kernels need).
+ * Errors: PA_ERR_INVALID_ARGUMENT for a NULL pointer or a field outside the
+ * ranges above, PA_ERR_UNSUPPORTED for an even rotary_dim that is not a multiple
+ * of 8 or above 256.
+ * pa_rope_frequencies: the angles f_i (HOST double [rotary_dim / 2]) and m
+ * (either may be NULL, not both).
+ */
+pa_status pa_rope_create(const pa_rope_desc *desc, pa_rope_t **out);
+void pa_rope_destroy(pa_rope_t *rope);   /* NULL is ignored */
+pa_status pa_rope_frequencies(const pa_rope_t *rope, double *frequencies, double *magnitude);
+
+/*
+ * out[t][h] = row x[t][h] rotated by positions[t], for t < num_tokens and
+ * h < num_heads: products and sums in binary32, angles exact to 2^-32 of a
+ * turn at every int32 position, one rounding to bf16 (elements that pass through
+ * are bit copies up to the quieting of NaNs).
+ *   x, out      DEVICE bf16, 16-byte aligned; heads head_dim apart, tokens
+ *               x_stride / out_stride elements apart (>= num_heads * head_dim, a
+ *               multiple of 8), so views of a packed projection output work,
+ *               and query and key heads that lie side by side are one call.
+ *               out == x with equal strides rotates in place; other overlaps
+ *               are invalid
+ *   positions   DEVICE int32 [num_tokens], negative ones too
+ *   head_dim    a multiple of 8, rotary_dim .. 256
+ * Errors: PA_ERR_INVALID_ARGUMENT (negative counts, NULL or misaligned pointers,
+ * strides, rotary_dim > head_dim), PA_ERR_UNSUPPORTED (head_dim), PA_ERR_CUDA.
+ * Capturable.  The current device must be the pointers' and the stream's.
+ */
+pa_status pa_rotary(const pa_rope_t *rope, const void *x, int64_t x_stride, const int32_t *positions,
+                    int32_t num_tokens, int32_t num_heads, int32_t head_dim, void *out, int64_t out_stride,
+                    void *stream);
+
+/*
+ * The step's cache write with the rotation on the way, one launch: token i of
+ * request r at position p = num_computed[r] + i goes to slot p % 16 of block
+ * block_table[r][p / 16] (pa_slot_mapping's slot), its key rotated by p, its
+ * value as it is; optionally its query rotated into q_out.  The metadata is read
+ * on the device, so a launch may be captured and replayed.
+ *   PA_KV_BF16      the rotated key, in binary32 arithmetic, rounded once; the
+ *                   caches end up as pa_rotary + pa_write_kv leave them
+ *   PA_KV_FP8_E4M3  codes as pa_write_kv_fp8 makes them, of the rotated key in
+ *                   binary32 (not rounded to bf16 in between)
+ *   block-scaled    per kv head and cache block that gets tokens, K and V
+ *                   each: with A the largest magnitude among the call's new
+ *                   finite values and Q the largest code value (448, 127),
+ *                   P = the smallest power of two >= 2^-64 with A <= P Q.  When
+ *                   the first new token is the block's first (slot 0), the
+ *                   scale becomes P; otherwise the larger of P and the block's
+ *                   scale, and when that grows, the codes of the earlier
+ *                   slots are re-coded: code * old scale / new scale, rounded to
+ *                   nearest, ties to even.  New codes are the values over the
+ *                   scale, rounded the same way; infinities saturate.  A NaN
+ *                   is E4M3's NaN; int8 has none, so there the block's scale
+ *                   of that head becomes NaN until the block starts anew.
+ *                   Slots behind the new tokens keep their codes.
+ * rope NULL: keys are written as they are (then q must be NULL).
+ * A cache block gets tokens of one request only (others are invalid input).
+ * Tokens from query_start_loc[num_reqs] on (a launch sized for a capacity) are
+ * neither read nor written, q_out rows included.  A token whose block id is
+ * outside [0, num_blocks), or whose block lies past max_blocks_per_req, is not
+ * stored and sets PA_DEVERR_BLOCK_RANGE in *device_error_word (its query is still
+ * rotated).
+ */
+typedef struct {
+    int32_t num_reqs, num_tokens;         /* R; T, or a capacity >= query_start_loc[R]  */
+    int32_t num_heads_q, num_heads_kv;    /* num_heads_q: 0 without q                   */
+    int32_t head_dim, block_size;         /* 64 or 128; 16                              */
+    int32_t num_blocks, max_blocks_per_req;
+    int32_t kv_cache_dtype;               /* PA_KV_*                                    */
+    float k_scale, v_scale;               /* PA_KV_FP8_E4M3: finite, > 0                */
+    const int32_t *query_start_loc;       /* DEVICE [R+1]                               */
+    const int32_t *num_computed_tokens;   /* DEVICE [R]                                 */
+    const int32_t *block_table;           /* DEVICE [R][max_blocks_per_req]; only the
+                                             entries of blocks that get tokens are read */
+    const void *key, *value;              /* DEVICE bf16 rows [T][Hkv][D], 16-byte
+                                             aligned, tokens *_stride elements apart
+                                             (>= Hkv * D, a multiple of 8)              */
+    int64_t key_stride, value_stride;
+    const void *q;                        /* optional, DEVICE bf16 rows [T][Hq][D]      */
+    void *q_out;                          /* with q; may be q itself (equal strides)    */
+    int64_t q_stride, q_out_stride;
+    void *key_cache, *value_cache;        /* DEVICE, 16-byte aligned                    */
+    float *key_scales, *value_scales;     /* block-scaled: DEVICE [num_blocks][Hkv]     */
+    int32_t *device_error_word;           /* optional, DEVICE                           */
+} pa_append_args;
+
+/* Errors: PA_ERR_INVALID_ARGUMENT (negative counts, NULL or misaligned pointers,
+ * strides, scales, an unknown kv_cache_dtype, rotary_dim > head_dim, q without a
+ * rope), PA_ERR_UNSUPPORTED (block_size, head_dim, num_blocks * 16 >= 2^31),
+ * PA_ERR_CUDA.  Enqueue before the step's attention on the same stream. */
+pa_status pa_append_kv(const pa_rope_t *rope, const pa_append_args *args, void *stream);
+
+/*
+ * pa_attention and pa_attention_launch for plans of block-scaled caches
+ * (PA_KV_FP8_E4M3_BLOCK, PA_KV_INT8_BLOCK; others are PA_ERR_INVALID_ARGUMENT):
+ * every kind of row that pa_attention takes, cascade and fixed shapes included.
+ *   key_scales,
+ *   value_scales   DEVICE float [num_blocks][Hkv], finite and > 0 (a scale
+ *                  below 2^-100 is read as 2^-100); a NaN scale makes the
+ *                  outputs that read the block NaN.  Only scales of blocks that
+ *                  are read are looked at
+ * Rows on the tensor-core tiles read bf16 copies of the dequantised blocks, made
+ * on the way: exact for scales that are powers of two (as pa_append_kv writes
+ * them), rounded once to bf16 for others.  Other rows read the codes.  All other
+ * arguments, errors and ordering as for pa_attention / pa_attention_launch.
+ */
+pa_status pa_attention_scaled(const pa_plan_t *plan, const void *q, const void *key_cache, const void *value_cache,
+                              const float *key_scales, const float *value_scales, const int32_t *block_table,
+                              void *out, void *workspace, size_t workspace_bytes, void *stream);
+pa_status pa_attention_scaled_launch(const pa_plan_t *plan, const void *q, const void *key_cache,
+                                     const void *value_cache, const float *key_scales, const float *value_scales,
+                                     const int32_t *block_table, void *out, void *workspace, size_t workspace_bytes,
+                                     void *stream);
 
 /*
  * Read and clear the device error word (the first 4 bytes of a workspace, or
@@ -579,6 +754,7 @@ typedef struct {
  * device buffers are not read during this call.
  * Errors: as pa_plan_fixed; PA_ERR_INVALID_ARGUMENT for a NULL or misaligned
  * buffer, host I/O given in part, or a host buffer that is not page-locked;
+ * PA_ERR_UNSUPPORTED for block-scaled caches;
  * PA_ERR_CUDA when an allocation, the capture or the instantiation fails.
  */
 pa_status pa_graph_create(const pa_batch_desc *desc, const pa_fixed_shape *shape, const pa_graph_buffers *bufs,

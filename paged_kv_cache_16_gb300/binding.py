@@ -25,6 +25,15 @@ PA_ERR_CAPACITY = 6
 
 PA_KV_BF16 = 0
 PA_KV_FP8_E4M3 = 1
+PA_KV_FP8_E4M3_BLOCK = 2
+PA_KV_INT8_BLOCK = 3
+
+PA_ROPE_HALF = 0
+PA_ROPE_INTERLEAVED = 1
+PA_ROPE_SCALE_NONE = 0
+PA_ROPE_SCALE_LINEAR = 1
+PA_ROPE_SCALE_WAVELENGTH = 2
+PA_ROPE_SCALE_YARN = 3
 
 PA_DEVERR_SLOT_RANGE = 0x1
 PA_DEVERR_BLOCK_RANGE = 0x2
@@ -38,7 +47,8 @@ EXPORTED = ("pa_plan", "pa_plan_destroy", "pa_plan_get_info", "pa_slot_mapping",
             "pa_attention_with_kv_update", "pa_attention_with_kv_update_launch", "pa_plan_metadata_bytes",
             "pa_plan_copy_metadata", "pa_upload_metadata_from", "pa_graph_create", "pa_graph_step",
             "pa_graph_turn", "pa_graph_wait", "pa_graph_workspace", "pa_graph_slot_mapping", "pa_graph_destroy",
-            "pa_attention_with_kv_update_launch_staged")
+            "pa_attention_with_kv_update_launch_staged", "pa_rope_create", "pa_rope_destroy", "pa_rope_frequencies",
+            "pa_rotary", "pa_append_kv", "pa_attention_scaled", "pa_attention_scaled_launch")
 
 
 class PaError(RuntimeError):
@@ -129,6 +139,52 @@ class GraphBuffers(ctypes.Structure):
     ]
 
 
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("rotary_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("scaling", ctypes.c_int32),
+        ("original_max_position", ctypes.c_int32),
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+        ("attention_factor", ctypes.c_double),
+    ]
+
+
+class AppendArgs(ctypes.Structure):
+    _fields_ = [
+        ("num_reqs", ctypes.c_int32),
+        ("num_tokens", ctypes.c_int32),
+        ("num_heads_q", ctypes.c_int32),
+        ("num_heads_kv", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("block_size", ctypes.c_int32),
+        ("num_blocks", ctypes.c_int32),
+        ("max_blocks_per_req", ctypes.c_int32),
+        ("kv_cache_dtype", ctypes.c_int32),
+        ("k_scale", ctypes.c_float),
+        ("v_scale", ctypes.c_float),
+        ("query_start_loc", ctypes.c_void_p),
+        ("num_computed_tokens", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p),
+        ("key", ctypes.c_void_p),
+        ("value", ctypes.c_void_p),
+        ("key_stride", ctypes.c_int64),
+        ("value_stride", ctypes.c_int64),
+        ("q", ctypes.c_void_p),
+        ("q_out", ctypes.c_void_p),
+        ("q_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64),
+        ("key_cache", ctypes.c_void_p),
+        ("value_cache", ctypes.c_void_p),
+        ("key_scales", ctypes.c_void_p),
+        ("value_scales", ctypes.c_void_p),
+        ("device_error_word", ctypes.c_void_p),
+    ]
+
+
 def library_path() -> str:
     return _build.LIBRARY
 
@@ -206,6 +262,20 @@ def load(path: str | None = None, build_if_missing: bool = False) -> ctypes.CDLL
     lib.pa_plan_enable_timing.argtypes = [vp, i32]
     lib.pa_plan_kernel_times.restype = ctypes.c_int
     lib.pa_plan_kernel_times.argtypes = [vp, ctypes.POINTER(ctypes.c_double), i32p]
+    lib.pa_rope_create.restype = ctypes.c_int
+    lib.pa_rope_create.argtypes = [ctypes.POINTER(RopeDesc), ctypes.POINTER(vp)]
+    lib.pa_rope_destroy.restype = None
+    lib.pa_rope_destroy.argtypes = [vp]
+    lib.pa_rope_frequencies.restype = ctypes.c_int
+    lib.pa_rope_frequencies.argtypes = [vp, vp, vp]
+    lib.pa_rotary.restype = ctypes.c_int
+    lib.pa_rotary.argtypes = [vp, vp, i64, vp, i32, i32, i32, vp, i64, vp]
+    lib.pa_append_kv.restype = ctypes.c_int
+    lib.pa_append_kv.argtypes = [vp, ctypes.POINTER(AppendArgs), vp]
+    lib.pa_attention_scaled.restype = ctypes.c_int
+    lib.pa_attention_scaled.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.pa_attention_scaled_launch.restype = ctypes.c_int
+    lib.pa_attention_scaled_launch.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     if path is None:
         _LIB = lib
     return lib
@@ -466,6 +536,158 @@ def pa_attention_no_alloc(plan: Plan, q, key_cache, value_cache, block_table, ou
     _check(load().pa_attention_no_alloc(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache),
                                         _ptr(block_table), _ptr(out), _ptr(device_error_word), _stream(stream)),
            "pa_attention_no_alloc")
+
+
+@dataclass
+class Rope:
+    """pa_rope_t: a rotation by position (see pa.h); immutable, used by any
+    number of calls, streams and captured graphs."""
+    handle: int
+    rotary_dim: int
+
+    def frequencies(self):
+        """(angles per position [rotary_dim / 2] as float64, factor on cos and sin)"""
+        f = np.empty(self.rotary_dim // 2, dtype=np.float64)
+        m = ctypes.c_double()
+        _check(load().pa_rope_frequencies(self.handle, f.ctypes.data, ctypes.addressof(m)), "pa_rope_frequencies")
+        return f, m.value
+
+    def destroy(self):
+        if self.handle:
+            load().pa_rope_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.destroy()
+        except Exception:  # noqa: BLE001 -- interpreter shutdown
+            pass
+
+
+def _rope_desc(rotary_dim, layout, base, scaling, factor, original_max_position, low, high, attention_factor):
+    return RopeDesc(int(rotary_dim), int(layout), int(scaling), int(original_max_position), float(base), float(factor),
+                    float(low), float(high), float(attention_factor))
+
+
+def pa_rope_create(*, rotary_dim, layout=PA_ROPE_HALF, base=10000.0, scaling=PA_ROPE_SCALE_NONE, factor=1.0,
+                   original_max_position=0, low=1.0, high=4.0, attention_factor=0.0) -> Rope:
+    """Build a rotation (host only, see pa.h)."""
+    d = _rope_desc(rotary_dim, layout, base, scaling, factor, original_max_position, low, high, attention_factor)
+    h = ctypes.c_void_p()
+    _check(load().pa_rope_create(ctypes.byref(d), ctypes.byref(h)), "pa_rope_create")
+    return Rope(h.value, int(rotary_dim))
+
+
+def pa_rope_status(*, rotary_dim, layout=PA_ROPE_HALF, base=10000.0, scaling=PA_ROPE_SCALE_NONE, factor=1.0,
+                   original_max_position=0, low=1.0, high=4.0, attention_factor=0.0) -> int:
+    """Status code pa_rope_create returns (rotation discarded)."""
+    d = _rope_desc(rotary_dim, layout, base, scaling, factor, original_max_position, low, high, attention_factor)
+    h = ctypes.c_void_p()
+    st = load().pa_rope_create(ctypes.byref(d), ctypes.byref(h))
+    if st == PA_OK:
+        load().pa_rope_destroy(h.value)
+    return st
+
+
+def _rows(t, name: str) -> int:
+    """Token stride of bf16 rows [T, heads, D] whose heads are dense (views of
+    a packed projection output are)."""
+    if t.dim() != 3 or t.element_size() != 2 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
+        raise ValueError(f"{name}: bf16 rows [tokens, heads, head_dim] with dense heads wanted")
+    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), t.shape[1] * t.shape[2])
+
+
+def _same_rows(a, b, what: str):
+    if tuple(a.shape) != tuple(b.shape):
+        raise ValueError(f"{what}: shapes {tuple(a.shape)} and {tuple(b.shape)} differ")
+
+
+def _dense(t, dtype: str, shape, name: str):
+    """A contiguous tensor of this dtype (and shape, unless None)."""
+    if str(t.dtype) != "torch." + dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{name}: a contiguous {dtype} tensor{'' if shape is None else f' of shape {tuple(shape)}'} wanted")
+
+
+def pa_rotary(rope: Rope, x, positions, out, stream=None):
+    """out = x (bf16 [T, H, D], token stride free) rotated by positions (int32
+    [T]); out may be x."""
+    xs, os_ = _rows(x, "x"), _rows(out, "out")
+    _same_rows(x, out, "x and out")
+    T, H, D = x.shape
+    _dense(positions, "int32", (T,), "positions")
+    _check(load().pa_rotary(rope.handle, _ptr(x), xs, _ptr(positions), T, H, D, _ptr(out), os_, _stream(stream)),
+           "pa_rotary")
+
+
+def _cache_dtype(cache, scales) -> int:
+    """PA_KV_* of a cache tensor: bf16, uint8 (E4M3 codes, block-scaled when
+    there are scales) or int8 (block-scaled)."""
+    kind = {"torch.bfloat16": PA_KV_BF16, "torch.uint8": PA_KV_FP8_E4M3 if scales is None else PA_KV_FP8_E4M3_BLOCK,
+            "torch.int8": PA_KV_INT8_BLOCK}.get(str(cache.dtype))
+    if kind is None or (kind in (PA_KV_BF16,) and scales is not None) or (kind == PA_KV_INT8_BLOCK and scales is None):
+        raise ValueError(f"a cache of {cache.dtype} {'with' if scales is not None else 'without'} block scales is none of PA_KV_*")
+    return kind
+
+
+def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, block_table, key_cache, value_cache, *,
+                 key_scales=None, value_scales=None, k_scale: float = 1.0, v_scale: float = 1.0, q=None, q_out=None,
+                 device_error_word=None, stream=None):
+    """The cache write with the rotation of key (and q into q_out) on the way
+    (see pa.h).  The cache's type follows from the tensors: bf16; uint8 E4M3
+    codes with k_scale / v_scale; uint8 or int8 codes with key_scales and
+    value_scales (float [num_blocks, Hkv])."""
+    T, hkv, d = key.shape
+    _same_rows(key, value, "key and value")
+    nb, bs = key_cache.shape[:2]
+    kind = _cache_dtype(key_cache, key_scales)
+    for c, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
+        _dense(c, str(key_cache.dtype)[6:], (nb, bs, hkv, d), name)
+    if (key_scales is None) != (value_scales is None):
+        raise ValueError("key_scales and value_scales come together")
+    if key_scales is not None:
+        _dense(key_scales, "float32", (nb, hkv), "key_scales")
+        _dense(value_scales, "float32", (nb, hkv), "value_scales")
+    R = int(num_computed.numel())
+    _dense(num_computed, "int32", (R,), "num_computed")
+    _dense(query_start_loc, "int32", (R + 1,), "query_start_loc")
+    _dense(block_table, "int32", (R, block_table.shape[-1]), "block_table")
+    a = AppendArgs()
+    a.num_reqs, a.num_tokens, a.num_heads_kv, a.head_dim, a.block_size = R, T, hkv, d, bs
+    a.num_blocks, a.max_blocks_per_req, a.kv_cache_dtype = nb, int(block_table.shape[1]), kind
+    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
+    a.query_start_loc, a.num_computed_tokens, a.block_table = _ptr(query_start_loc), _ptr(num_computed), _ptr(block_table)
+    a.key, a.key_stride, a.value, a.value_stride = _ptr(key), _rows(key, "key"), _ptr(value), _rows(value, "value")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out come together")
+    if q is not None:
+        _same_rows(q, q_out, "q and q_out")
+        if q.shape[0] != T or q.shape[2] != d:
+            raise ValueError("q: rows of key's tokens and head_dim wanted")
+        a.num_heads_q = q.shape[1]
+        a.q, a.q_stride, a.q_out, a.q_out_stride = _ptr(q), _rows(q, "q"), _ptr(q_out), _rows(q_out, "q_out")
+    a.key_cache, a.value_cache = _ptr(key_cache), _ptr(value_cache)
+    a.key_scales, a.value_scales = _ptr(key_scales), _ptr(value_scales)
+    a.device_error_word = _ptr(device_error_word)
+    _check(load().pa_append_kv(rope.handle if rope is not None else None, ctypes.byref(a), _stream(stream)),
+           "pa_append_kv")
+
+
+def pa_attention_scaled(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace,
+                        stream=None):
+    """Attention over block-scaled 8-bit caches (see pa.h)."""
+    nbytes = workspace.numel() * workspace.element_size()
+    _check(load().pa_attention_scaled(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(key_scales),
+                                      _ptr(value_scales), _ptr(block_table), _ptr(out), _ptr(workspace), nbytes,
+                                      _stream(stream)), "pa_attention_scaled")
+
+
+def pa_attention_scaled_launch(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out,
+                               workspace, stream=None):
+    """Its kernels alone, after pa_upload_metadata (capturable in a CUDA graph)."""
+    nbytes = workspace.numel() * workspace.element_size()
+    _check(load().pa_attention_scaled_launch(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(key_scales),
+                                             _ptr(value_scales), _ptr(block_table), _ptr(out), _ptr(workspace), nbytes,
+                                             _stream(stream)), "pa_attention_scaled_launch")
 
 
 NO_ALLOC_SCRATCH_BYTES = 16 << 20

@@ -104,6 +104,77 @@ __device__ __forceinline__ void expand16(const uint4 codes, uint4 *dst) {
     dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
+// Block-scaled caches: the same with each head's scale, code * scale rounded
+// once to bf16 (exact for scales that are powers of two).
+template <bool INT8>
+__device__ __forceinline__ void expand16_scaled(const uint4 codes, float scale, uint4 *dst) {
+    const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x[4];
+        if constexpr (INT8) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = static_cast<float>(static_cast<int8_t>(w[i] >> (8 * k)));
+        } else {
+            uint32_t lo, hi;
+            dev::e4m3x4_to_f16x2x2(w[i], lo, hi);
+            x[0] = dev::f16_lo(lo); x[1] = dev::f16_hi(lo); x[2] = dev::f16_lo(hi); x[3] = dev::f16_hi(hi);
+        }
+        o[2 * i] = dev::pack_bf16x2(x[0] * scale, x[1] * scale);
+        o[2 * i + 1] = dev::pack_bf16x2(x[2] * scale, x[3] * scale);
+    }
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+}
+
+template <bool INT8>
+__global__ void dequant_scaled_kernel(DequantParams p) {
+    dev::grid_launch_dependents();
+    dev::grid_dep_wait();
+    const int32_t n = p.counts[kCountDequant];
+    const int32_t chunks = p.block_elems / 16;
+    for (int32_t i = blockIdx.x; i < n; i += gridDim.x) {
+        const DequantItem it = p.items[i];
+        const int32_t src = p.block_table[static_cast<int64_t>(it.req) * p.max_blocks + it.block];
+        uint4 *kd = reinterpret_cast<uint4 *>(p.key_out + static_cast<int64_t>(it.dst) * p.block_elems);
+        uint4 *vd = reinterpret_cast<uint4 *>(p.value_out + static_cast<int64_t>(it.dst) * p.block_elems);
+        if (src < 0 || src >= p.num_blocks) {
+            if (threadIdx.x == 0) atomicOr(p.err, kErrBlockRange);
+            for (int32_t c = threadIdx.x; c < 2 * chunks; c += blockDim.x) kd[c] = vd[c] = make_uint4(0, 0, 0, 0);
+            continue;
+        }
+        const uint4 *ks = reinterpret_cast<const uint4 *>(p.key_cache + static_cast<int64_t>(src) * p.block_elems);
+        const uint4 *vs = reinterpret_cast<const uint4 *>(p.value_cache + static_cast<int64_t>(src) * p.block_elems);
+        const int64_t scales = static_cast<int64_t>(src) * p.num_heads_kv;
+        // a thread's chunks of the block are all loaded before any is stored
+        constexpr int U = 4;
+        for (int32_t c0 = threadIdx.x; c0 < chunks; c0 += U * blockDim.x) {
+            uint4 kx[U], vx[U];
+            float ksc[U], vsc[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t c = c0 + u * static_cast<int32_t>(blockDim.x);
+                if (c < chunks) {
+                    const int32_t head = 16 * c / p.head_dim % p.num_heads_kv;
+                    kx[u] = __ldg(ks + c);
+                    vx[u] = __ldg(vs + c);
+                    ksc[u] = __ldg(p.key_scales + scales + head);
+                    vsc[u] = __ldg(p.value_scales + scales + head);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int32_t c = c0 + u * static_cast<int32_t>(blockDim.x);
+                if (c < chunks) {
+                    expand16_scaled<INT8>(kx[u], ksc[u], kd + 2 * c);
+                    expand16_scaled<INT8>(vx[u], vsc[u], vd + 2 * c);
+                }
+            }
+        }
+    }
+}
+
 __global__ void dequant_kernel(DequantParams p) {
     dev::grid_launch_dependents();
     dev::grid_dep_wait();
@@ -309,6 +380,9 @@ cudaError_t launch_write_kv_fp8(const void *key, const void *value, const int64_
 
 cudaError_t launch_dequant(int grid, const DequantParams &p, cudaStream_t stream, bool pdl) {
     if (grid <= 0) return cudaSuccess;
+    if (p.key_scales != nullptr)
+        return p.int8 ? launch_ex(dequant_scaled_kernel<true>, dim3(grid), dim3(256), 0, stream, pdl, p)
+                      : launch_ex(dequant_scaled_kernel<false>, dim3(grid), dim3(256), 0, stream, pdl, p);
     return launch_ex(dequant_kernel, dim3(grid), dim3(256), 0, stream, pdl, p);
 }
 

@@ -57,12 +57,14 @@ bool make_map_kv(CUtensorMap *tm, const void *ptr, uint64_t d, uint64_t hkv, uin
     auto fn = encode_fn();
     if (!fn) return false;
     const uint64_t es = u8 ? 1 : 2;
+    const bool narrow = d * es == 64;   // rows of 64 codes: one box of 64 bytes, swizzled as such
     cuuint64_t dims[3] = {d, rows, hkv};
     cuuint64_t strides[2] = {hkv * d * es, d * es};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(kBlockSize), box_heads};
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(narrow ? 64 : 128 / es), static_cast<cuuint32_t>(kBlockSize), box_heads};
     cuuint32_t estr[3] = {1, 1, 1};
     CUresult r = fn(tm, u8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(ptr),
-                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                    dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
                     CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
@@ -187,7 +189,7 @@ pa_status validate(const pa_batch_desc *d) {
             }
         }
     }
-    if (d->kv_cache_dtype != PA_KV_BF16 && d->kv_cache_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARGUMENT;
+    if (d->kv_cache_dtype < PA_KV_BF16 || d->kv_cache_dtype > PA_KV_INT8_BLOCK) return PA_ERR_INVALID_ARGUMENT;
     if (d->kv_cache_dtype == PA_KV_FP8_E4M3 &&
         (!(d->k_scale > 0.f) || !std::isfinite(d->k_scale) || !(d->v_scale > 0.f) || !std::isfinite(d->v_scale)))
         return PA_ERR_INVALID_ARGUMENT;
@@ -229,6 +231,11 @@ constexpr int64_t kItemBytes = 64 * 1024;
 // Shortest cascade prefix tile, in 128-key steps.
 constexpr int kMinPrefixSteps = 8;
 
+int decode_ctas_per_sm(const pa_plan_s *P) {
+    return std::max(1, P->scaled ? scaled_decode_ctas_per_sm(P->D, P->HG)
+                                 : decode_ctas_per_sm_static(P->D, P->HG, P->kv8));
+}
+
 void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector<int32_t> &pieces,
                  std::vector<int32_t> &item_unit, int64_t work_ctas, int64_t fixed_ncta) {
     struct Run { int32_t u, grp, pb, pe; };
@@ -250,7 +257,7 @@ void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector
         if (fixed_ncta > 0) P->cta_begin.assign(static_cast<size_t>(fixed_ncta) + 1, 0);
         return;
     }
-    const int cps = std::max(1, decode_ctas_per_sm_static(P->D, P->HG, P->kv8));
+    const int cps = decode_ctas_per_sm(P);
     const int64_t min_pages = 4;
     const int64_t cap = work_ctas > 0 ? work_ctas : static_cast<int64_t>(P->num_sms) * cps;
     int64_t ncta = std::min<int64_t>(cap, (total + min_pages - 1) / min_pages);
@@ -377,11 +384,14 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
     P->G = P->Hq / P->Hkv;
     P->HG = heads_per_group(P->Hkv);
     P->n_groups = P->Hkv / P->HG;
-    P->kv8 = d->kv_cache_dtype == PA_KV_FP8_E4M3;
-    P->scale_log2 = d->softmax_scale * (P->kv8 ? d->k_scale : 1.f) * 1.4426950408889634f;
-    P->out_scale = P->kv8 ? d->v_scale : 1.f;
-    P->k_scale = P->kv8 ? d->k_scale : 1.f;
-    P->v_scale = P->kv8 ? d->v_scale : 1.f;
+    const bool e4m3 = d->kv_cache_dtype == PA_KV_FP8_E4M3;   // one scale per tensor
+    P->kv8 = d->kv_cache_dtype != PA_KV_BF16;
+    P->scaled = P->kv8 && !e4m3;
+    P->int8 = d->kv_cache_dtype == PA_KV_INT8_BLOCK;
+    P->scale_log2 = d->softmax_scale * (e4m3 ? d->k_scale : 1.f) * 1.4426950408889634f;
+    P->out_scale = e4m3 ? d->v_scale : 1.f;
+    P->k_scale = e4m3 ? d->k_scale : 1.f;
+    P->v_scale = e4m3 ? d->v_scale : 1.f;
     P->num_sms = d->num_sms;
     if (P->num_sms == 0) {
         int dev = 0;
@@ -534,7 +544,7 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
     if (P->decode_prefix > 0)
         for (const DecodeUnit &u : units)
             if (u.t0 + u.n_tok > P->decode_prefix) return PA_ERR_CAPACITY;
-    const int cps = std::max(1, decode_ctas_per_sm_static(P->D, P->HG, P->kv8));
+    const int cps = decode_ctas_per_sm(P);
 
     // ------------------------------------------ tile costs and the SM split
     // cost of a tile: its 128-key steps (as the kernel counts them) plus one
@@ -893,7 +903,9 @@ SideStream *side_stream() {
 
 pa_status prepare_plan(pa_plan_s *P) {
     if (P->prepared) return PA_OK;
-    if (P->ncta > 0 && prepare_decode(P->D, P->HG, P->kv8) != cudaSuccess) return PA_ERR_CUDA;
+    if (P->ncta > 0 && (P->scaled ? prepare_scaled_decode(P->D, P->HG, P->int8) : prepare_decode(P->D, P->HG, P->kv8)) !=
+                           cudaSuccess)
+        return PA_ERR_CUDA;
     if (P->cap_tiles > 0 && prepare_extend(P->D) != cudaSuccess) return PA_ERR_CUDA;
     if (P->fork && side_stream() == nullptr) return PA_ERR_CUDA;
     P->prepared = true;
@@ -902,7 +914,9 @@ pa_status prepare_plan(pa_plan_s *P) {
 
 pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, const void *value_cache,
                             const int32_t *block_table, void *out, uint8_t *ws, cudaStream_t stream, bool timed,
-                            const KvUpdate &update, bool allow_fork) {
+                            const KvUpdate &update, bool allow_fork, const KvScales &scales) {
+    // block-scaled caches come with their scales and without the fused update
+    if (P->scaled != (scales.key != nullptr) || (P->scaled && update.key != nullptr)) return PA_ERR_INVALID_ARGUMENT;
     auto rec = [&](int kind, bool start, cudaStream_t st) { return timed ? record(P, kind, start, st) : cudaSuccess; };
     int32_t *err = reinterpret_cast<int32_t *>(ws);
     const int32_t *counts = reinterpret_cast<const int32_t *>(ws + kHeader);
@@ -998,6 +1012,11 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
             qp.max_blocks = P->max_blocks;
             qp.num_blocks = P->num_blocks;
             qp.block_elems = kBlockSize * P->Hkv * P->D;
+            qp.key_scales = scales.key;
+            qp.value_scales = scales.value;
+            qp.num_heads_kv = P->Hkv;
+            qp.head_dim = P->D;
+            qp.int8 = P->int8 ? 1 : 0;
             if (launch_dequant(std::min(P->cap_dequant, 8 * sms), qp, tile_stream, !fork) != cudaSuccess)
                 return PA_ERR_CUDA;
             const uint64_t srows = static_cast<uint64_t>(std::max(1, P->cap_dequant)) * kBlockSize;
@@ -1064,7 +1083,10 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
         dp.k_scale = P->k_scale;
         dp.v_scale = P->v_scale;
         if (rec(0, true, stream) != cudaSuccess) return PA_ERR_CUDA;
-        if (launch_decode(P->D, P->HG, P->kv8, P->ncta, tm_dk, tm_dv, dp, stream) != cudaSuccess) return PA_ERR_CUDA;
+        if ((P->scaled ? launch_scaled_decode(P->D, P->HG, P->int8, P->ncta, tm_dk, tm_dv,
+                                              ScaledDecodeParams{dp, scales.key, scales.value}, stream)
+                       : launch_decode(P->D, P->HG, P->kv8, P->ncta, tm_dk, tm_dv, dp, stream)) != cudaSuccess)
+            return PA_ERR_CUDA;
         if (rec(0, false, stream) != cudaSuccess) return PA_ERR_CUDA;
     }
     if (fork && cudaStreamWaitEvent(stream, side->join, 0) != cudaSuccess) return PA_ERR_CUDA;
@@ -1132,8 +1154,8 @@ pa_status pa_plan_fixed(const pa_batch_desc *desc, const pa_fixed_shape *shape, 
         return PA_ERR_INVALID_ARGUMENT;
     pa_status st = validate(desc);
     if (st != PA_OK) return st;
-    if (desc->kv_cache_dtype == PA_KV_FP8_E4M3 && shape->max_extend_tiles > 0 && shape->max_dequant_blocks == 0)
-        return PA_ERR_INVALID_ARGUMENT;   // FP8 tiles read bf16 copies: they need room
+    if (desc->kv_cache_dtype != PA_KV_BF16 && shape->max_extend_tiles > 0 && shape->max_dequant_blocks == 0)
+        return PA_ERR_INVALID_ARGUMENT;   // tiles over 8-bit caches read bf16 copies: they need room
     pa_plan_s *P = new (std::nothrow) pa_plan_s();
     if (!P) return PA_ERR_INVALID_ARGUMENT;
     st = build_plan(P, desc, shape);
@@ -1237,7 +1259,7 @@ pa_status upload(pa_plan_s *P, uint8_t *ws, cudaStream_t stream, bool timed) {
 pa_status pa_attention(const pa_plan_t *plan, const void *q, const void *key_cache, const void *value_cache,
                        const int32_t *block_table, void *out, void *workspace, size_t workspace_bytes,
                        void *stream_) {
-    if (!plan) return PA_ERR_INVALID_ARGUMENT;
+    if (!plan || plan->scaled) return PA_ERR_INVALID_ARGUMENT;
     pa_plan_s *P = const_cast<pa_plan_s *>(plan);
     if (P->T == 0 && !P->fixed) return PA_OK;
     pa_status st = check_launch_args(P, q, key_cache, value_cache, block_table, out, workspace, workspace_bytes);
@@ -1293,7 +1315,7 @@ pa_status pa_upload_metadata_from(const void *host_src, size_t bytes, void *work
 pa_status pa_attention_launch(const pa_plan_t *plan, const void *q, const void *key_cache, const void *value_cache,
                               const int32_t *block_table, void *out, void *workspace, size_t workspace_bytes,
                               void *stream_) {
-    if (!plan) return PA_ERR_INVALID_ARGUMENT;
+    if (!plan || plan->scaled) return PA_ERR_INVALID_ARGUMENT;
     pa_plan_s *P = const_cast<pa_plan_s *>(plan);
     if (P->T == 0 && !P->fixed) return PA_OK;
     pa_status st = check_launch_args(P, q, key_cache, value_cache, block_table, out, workspace, workspace_bytes);
@@ -1304,11 +1326,49 @@ pa_status pa_attention_launch(const pa_plan_t *plan, const void *q, const void *
                              static_cast<cudaStream_t>(stream_), false);
 }
 
+namespace {
+
+// Both calls over block-scaled caches; `whole` uploads the metadata first.
+pa_status attention_scaled(const pa_plan_t *plan, const void *q, const void *key_cache, const void *value_cache,
+                           const float *key_scales, const float *value_scales, const int32_t *block_table, void *out,
+                           void *workspace, size_t workspace_bytes, cudaStream_t stream, bool whole) {
+    if (!plan || !plan->scaled) return PA_ERR_INVALID_ARGUMENT;
+    pa_plan_s *P = const_cast<pa_plan_s *>(plan);
+    if (P->T == 0 && !P->fixed) return PA_OK;
+    pa_status st = check_launch_args(P, q, key_cache, value_cache, block_table, out, workspace, workspace_bytes);
+    if (st != PA_OK) return st;
+    if (!key_scales || !value_scales || !aligned(key_scales, 4) || !aligned(value_scales, 4))
+        return PA_ERR_INVALID_ARGUMENT;
+    std::lock_guard<std::mutex> lock(P->mu);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    if ((st = prepare_plan(P)) != PA_OK) return st;
+    if (whole && (st = upload(P, ws, stream, true)) != PA_OK) return st;
+    return enqueue_attention(P, q, key_cache, value_cache, block_table, out, ws, stream, whole, KvUpdate{}, true,
+                             KvScales{key_scales, value_scales});
+}
+
+}  // namespace
+
+pa_status pa_attention_scaled(const pa_plan_t *plan, const void *q, const void *key_cache, const void *value_cache,
+                              const float *key_scales, const float *value_scales, const int32_t *block_table,
+                              void *out, void *workspace, size_t workspace_bytes, void *stream) {
+    return attention_scaled(plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace,
+                            workspace_bytes, static_cast<cudaStream_t>(stream), true);
+}
+
+pa_status pa_attention_scaled_launch(const pa_plan_t *plan, const void *q, const void *key_cache,
+                                     const void *value_cache, const float *key_scales, const float *value_scales,
+                                     const int32_t *block_table, void *out, void *workspace, size_t workspace_bytes,
+                                     void *stream) {
+    return attention_scaled(plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace,
+                            workspace_bytes, static_cast<cudaStream_t>(stream), false);
+}
+
 pa_status pa_attention_with_kv_update(const pa_plan_t *plan, const void *q, const void *key, const void *value,
                                       void *key_cache, void *value_cache, const int32_t *block_table,
                                       int64_t *slot_mapping, void *out, void *workspace, size_t workspace_bytes,
                                       void *stream_) {
-    if (!plan) return PA_ERR_INVALID_ARGUMENT;
+    if (!plan || plan->scaled) return PA_ERR_INVALID_ARGUMENT;
     pa_plan_s *P = const_cast<pa_plan_s *>(plan);
     if (P->T == 0 && !P->fixed) return PA_OK;
     pa_status st = check_launch_args(P, q, key_cache, value_cache, block_table, out, workspace, workspace_bytes);
@@ -1331,7 +1391,7 @@ pa_status pa_attention_with_kv_update_launch(const pa_plan_t *plan, const void *
                                              const void *value, void *key_cache, void *value_cache,
                                              const int32_t *block_table, int64_t *slot_mapping, void *out,
                                              void *workspace, size_t workspace_bytes, void *stream_) {
-    if (!plan) return PA_ERR_INVALID_ARGUMENT;
+    if (!plan || plan->scaled) return PA_ERR_INVALID_ARGUMENT;
     pa_plan_s *P = const_cast<pa_plan_s *>(plan);
     if (P->T == 0 && !P->fixed) return PA_OK;
     pa_status st = check_launch_args(P, q, key_cache, value_cache, block_table, out, workspace, workspace_bytes);
@@ -1353,7 +1413,7 @@ pa_status pa_attention_with_kv_update_launch_staged(const pa_plan_t *plan, const
                                                     const int32_t *block_table, int64_t *slot_mapping, void *out,
                                                     void *workspace, size_t workspace_bytes, void *stream_,
                                                     void *late_rows, void *late_out_ready) {
-    if (!plan || !late_rows || !plan->fixed || plan->decode_prefix <= 0) return PA_ERR_INVALID_ARGUMENT;
+    if (!plan || plan->scaled || !late_rows || !plan->fixed || plan->decode_prefix <= 0) return PA_ERR_INVALID_ARGUMENT;
     pa_plan_s *P = const_cast<pa_plan_s *>(plan);
     pa_status st = check_launch_args(P, q, key_cache, value_cache, block_table, out, workspace, workspace_bytes);
     if (st != PA_OK) return st;
@@ -1375,13 +1435,13 @@ pa_status pa_zero_blocks(const int32_t *block_ids, int32_t num_ids, int32_t num_
                          int32_t head_dim, int32_t kv_cache_dtype, void *key_cache, void *value_cache,
                          int32_t *device_error_word, void *stream) {
     if (num_ids < 0 || num_blocks < 0 || num_heads_kv <= 0 || head_dim <= 0) return PA_ERR_INVALID_ARGUMENT;
-    if (kv_cache_dtype != PA_KV_BF16 && kv_cache_dtype != PA_KV_FP8_E4M3) return PA_ERR_INVALID_ARGUMENT;
+    if (kv_cache_dtype < PA_KV_BF16 || kv_cache_dtype > PA_KV_INT8_BLOCK) return PA_ERR_INVALID_ARGUMENT;
     if (num_ids == 0) return PA_OK;
     if (!block_ids || !key_cache || !value_cache || !aligned(key_cache, 16) || !aligned(value_cache, 16) ||
         !aligned(block_ids, 4))
         return PA_ERR_INVALID_ARGUMENT;
     const int64_t block_bytes =
-        static_cast<int64_t>(kBlockSize) * num_heads_kv * head_dim * (kv_cache_dtype == PA_KV_FP8_E4M3 ? 1 : 2);
+        static_cast<int64_t>(kBlockSize) * num_heads_kv * head_dim * (kv_cache_dtype == PA_KV_BF16 ? 2 : 1);
     if (block_bytes % 16 != 0) return PA_ERR_UNSUPPORTED;
     cudaError_t e = launch_zero_blocks(block_ids, num_ids, num_blocks, block_bytes, key_cache, value_cache,
                                        device_error_word, static_cast<cudaStream_t>(stream));

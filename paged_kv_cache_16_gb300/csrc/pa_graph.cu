@@ -242,6 +242,8 @@ pa_status pa_graph_create(const pa_batch_desc *desc, const pa_fixed_shape *shape
                           pa_graph_t **out) {
     if (out) *out = nullptr;
     if (!desc || !shape || !bufs || !out) return PA_ERR_INVALID_ARGUMENT;
+    if (desc->kv_cache_dtype > PA_KV_FP8_E4M3 && desc->kv_cache_dtype <= PA_KV_INT8_BLOCK)
+        return PA_ERR_UNSUPPORTED;   // the graph's step holds no scales of block-scaled caches
     pa_status st = check_buffers(*bufs);
     if (st != PA_OK) return st;
     pa_graph_s *g = new (std::nothrow) pa_graph_s;

@@ -42,6 +42,19 @@ constexpr int decode_ctas_per_sm_static(int d, int hg, bool kv8) {
                : (2048 / decode_threads(hg));
 }
 
+// Split-KV decode over block-scaled 8-bit caches: the stages of the E4M3
+// kernel, two barriers per stage, and the stage's K and V scales of each head.
+constexpr int scaled_decode_smem_bytes(int d, int hg) {
+    return decode_stages(d, hg, true) * (decode_stage_bytes(d, hg, true) + 2 * 8 + 2 * hg * 4) + 1024;
+}
+// 12 warps per SM: three per scheduler with 168 registers each, which the
+// accumulators of 16 query rows need
+constexpr int scaled_decode_ctas_per_sm(int d, int hg) {
+    return (kSmemPerSm / (scaled_decode_smem_bytes(d, hg) + 1024)) < (12 / (hg + 1))
+               ? (kSmemPerSm / (scaled_decode_smem_bytes(d, hg) + 1024))
+               : (12 / (hg + 1));
+}
+
 // Device error word bits (mirrors PA_DEVERR_* of pa.h).
 constexpr int kErrSlotRange = 0x1;
 constexpr int kErrBlockRange = 0x2;
@@ -122,6 +135,14 @@ struct DecodeParams {
     float k_scale, v_scale;     // E4M3 quantisation scales of the write
 };
 
+// The same over block-scaled 8-bit caches (base.out_scale is 1, the fused
+// update's fields are unused).
+struct ScaledDecodeParams {
+    DecodeParams base;
+    const float *key_scales;    // [num_blocks][Hkv]
+    const float *value_scales;
+};
+
 struct ExtendParams {
     uint16_t *out;
     const int32_t *block_table;
@@ -162,6 +183,10 @@ struct DequantParams {
     int32_t max_blocks;
     int32_t num_blocks;
     int32_t block_elems;        // 16 * Hkv * D
+    // block-scaled caches: the copies hold code * scale, rounded once to bf16
+    const float *key_scales;    // [num_blocks][Hkv]; null: the code values
+    const float *value_scales;
+    int32_t num_heads_kv, head_dim, int8;
 };
 
 struct MergeParams {
@@ -220,6 +245,49 @@ struct WriteParams {
     int32_t part;               // runs to store: 0 all, 1 the early ones, 2 the rest
 };
 
+// A rotation by position as the kernels take it: pair i of a row at position
+// p turns by the fraction (p * step[i] mod 2^64) / 2^64 of a full turn, and
+// cos and sin are multiplied by `mag`.
+constexpr int kMaxRotaryDim = 256;
+struct RopeParams {
+    uint64_t step[kMaxRotaryDim / 2];
+    float mag;
+    int32_t rotary_dim;         // elements rotated (0: none); the rest of a row passes through
+    int32_t interleaved;        // pairs (2i, 2i + 1), else (i, i + rotary_dim / 2)
+};
+
+struct RotaryParams {
+    const uint16_t *x;          // bf16 rows [T][H][D], token stride in elements
+    uint16_t *out;
+    const int32_t *positions;   // [T]
+    int64_t x_stride, out_stride;
+    int32_t num_tokens, num_heads, head_dim;
+    int32_t tokens_per_cta, heads_per_cta;
+};
+
+// Element types of the cache an append writes.
+enum CacheKind : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheE4m3Block = 2, kCacheInt8Block = 3 };
+
+struct AppendParams {
+    const uint16_t *q;          // optional: rotated into q_out
+    uint16_t *q_out;
+    const uint16_t *key;        // bf16 rows [T][Hkv][D]
+    const uint16_t *value;
+    int64_t q_stride, q_out_stride, key_stride, value_stride;   // token strides in elements
+    const int32_t *query_start_loc;
+    const int32_t *num_computed;
+    const int32_t *block_table;
+    void *key_cache;
+    void *value_cache;
+    float *key_scales;          // block-scaled caches: [num_blocks][Hkv]
+    float *value_scales;
+    int32_t *err;               // optional
+    float k_scale, v_scale;     // E4M3 with one scale per tensor
+    int32_t num_reqs, num_tokens, num_heads_q, num_heads_kv;
+    int32_t num_blocks, max_blocks;
+    int32_t q_heads_per_cta;
+};
+
 // Launch with programmatic stream serialisation when `pdl` (the kernel calls
 // grid_dep_wait before touching data of earlier kernels, which is a no-op for
 // a plain launch).  Plain launches follow a wait on another stream's event.
@@ -265,6 +333,8 @@ cudaError_t launch_dequant(int grid, const DequantParams &p, cudaStream_t stream
 // cudaErrorInvalidValue for an unsupported combination.
 cudaError_t launch_decode(int head_dim, int hg, bool kv8, int num_ctas, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const DecodeParams &p, cudaStream_t stream);
+cudaError_t launch_scaled_decode(int head_dim, int hg, bool int8, int num_ctas, const CUtensorMap &tm_k,
+                                 const CUtensorMap &tm_v, const ScaledDecodeParams &p, cudaStream_t stream);
 cudaError_t launch_extend(int head_dim, int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const ExtendParams &p, cudaStream_t stream, bool pdl = true);
 cudaError_t launch_merge(int head_dim, int grid, const MergeParams &p, cudaStream_t stream, bool pdl = true);
@@ -273,12 +343,18 @@ cudaError_t launch_merge(int head_dim, int grid, const MergeParams &p, cudaStrea
 cudaError_t launch_upload(const void *src, void *dst, size_t bytes, cudaStream_t stream);
 // Fused write of extend-row tokens: grid-stride over their 16-element chunks.
 cudaError_t launch_write_runs(int grid, const WriteParams &p, cudaStream_t stream, bool pdl = true);
+// Rotate rows by their positions; append new rows to the paged caches (kind:
+// a CacheKind) with keys and queries rotated on the way (rope.rotary_dim 0:
+// as they are).
+cudaError_t launch_rotary(const RopeParams &rope, const RotaryParams &p, cudaStream_t stream);
+cudaError_t launch_append(int head_dim, int kind, const RopeParams &rope, const AppendParams &p, cudaStream_t stream);
 // Zero the K and V entries of the listed blocks (ids < 0 skipped).
 cudaError_t launch_zero_blocks(const int32_t *ids, int32_t num_ids, int32_t num_blocks, int64_t block_bytes,
                                void *key_cache, void *value_cache, int32_t *err, cudaStream_t stream);
 // One-time per-process kernel attributes (dynamic shared memory sizes) of the
 // kernels a plan launches, so that later launches can be captured.
 cudaError_t prepare_decode(int head_dim, int hg, bool kv8);
+cudaError_t prepare_scaled_decode(int head_dim, int hg, bool int8);
 cudaError_t prepare_extend(int head_dim);
 
 }  // namespace pa

@@ -53,7 +53,7 @@ extern "C" pa_status pa_attention_no_alloc(const pa_plan_t *plan, const void *q,
                                            const void *value_cache, const int32_t *block_table, void *out,
                                            int32_t *device_error_word, void *stream_) {
     using namespace pa;
-    if (!plan) return PA_ERR_INVALID_ARGUMENT;
+    if (!plan || plan->scaled) return PA_ERR_INVALID_ARGUMENT;   // block-scaled caches: no scales here
     pa_plan_s *P = const_cast<pa_plan_s *>(plan);
     if (P->T == 0) {
         // nothing to attend; the error word still receives this call's bits (none)

@@ -15,7 +15,9 @@ struct pa_plan_s {
     int32_t prefix_req = -1;      // block-table row of the shared prefix
     int32_t prefix_splits = 0;
     float scale_log2 = 0.f;     // softmax_scale * k_scale * log2(e)
-    bool kv8 = false;           // E4M3 caches
+    bool kv8 = false;           // 8-bit caches (E4M3, or block-scaled)
+    bool scaled = false;        // block-scaled: the attention calls with scales take it
+    bool int8 = false;          // of those: int8 codes
     float out_scale = 1.f;      // v_scale for E4M3 caches
     float k_scale = 1.f, v_scale = 1.f;   // E4M3 quantisation scales of the fused write
     // work lists
@@ -87,12 +89,19 @@ struct KvUpdate {
     cudaEvent_t late_out_ready = nullptr;   // optional: recorded once out rows from the prefix on are final
 };
 
+// Scales of block-scaled caches ([num_blocks][Hkv]); null for the others.
+struct KvScales {
+    const float *key = nullptr;
+    const float *value = nullptr;
+};
+
 // allow_fork = false keeps every launch on `stream` (a plan whose tiles run
 // side by side with the decode kernel then runs them one after the other,
 // with the same work cut and the same results).
 pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, const void *value_cache,
                             const int32_t *block_table, void *out, uint8_t *ws, cudaStream_t stream, bool timed,
-                            const KvUpdate &update = KvUpdate{}, bool allow_fork = true);
+                            const KvUpdate &update = KvUpdate{}, bool allow_fork = true,
+                            const KvScales &scales = KvScales{});
 
 // The second stream (and its fork / join events) of this host thread on the
 // current device, created on first use; null if creation fails.
