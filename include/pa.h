@@ -615,10 +615,10 @@ pa_status pa_append_kv(const pa_rope_t *rope, const pa_append_args *args, void *
  *                  below 2^-100 is read as 2^-100); a NaN scale makes the
  *                  outputs that read the block NaN.  Only scales of blocks that
  *                  are read are looked at
- * Rows on the tensor-core tiles read bf16 copies of the dequantised blocks, made
- * on the way: exact for scales that are powers of two (as pa_append_kv writes
- * them), rounded once to bf16 for others.  Other rows read the codes.  All other
- * arguments, errors and ordering as for pa_attention / pa_attention_launch.
+ * Codes and scales are used exactly (scales in binary32; softmax weights rounded
+ * to f16), whatever the scales' spread.  Rows on the tensor-core tiles read 16-bit
+ * copies of the codes, made on the way in the workspace.  All other arguments,
+ * errors and ordering as for pa_attention / pa_attention_launch.
  */
 pa_status pa_attention_scaled(const pa_plan_t *plan, const void *q, const void *key_cache, const void *value_cache,
                               const float *key_scales, const float *value_scales, const int32_t *block_table,

@@ -51,29 +51,7 @@ __device__ __forceinline__ uint32_t tile_at(uint32_t row, uint32_t chunk) {
     else return row * 64u + ((chunk ^ ((row >> 1) & 3u)) << 4);
 }
 
-// four codes (one word, lowest byte first) -> two f16x2 words, exact.  int8:
-// the byte plus 128 as the low mantissa bits of 1024 + byte, minus 1152.
-template <bool INT8>
-__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t &lo, uint32_t &hi) {
-    if constexpr (INT8) {
-        const uint32_t u = w ^ 0x80808080u;
-        const uint32_t a = prmt(u, 0x64646464u, 0x4140u), b = prmt(u, 0x64646464u, 0x4342u);
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(lo) : "r"(a), "r"(0x64806480u));
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(hi) : "r"(b), "r"(0x64806480u));
-    } else {
-        e4m3x4_to_f16x2x2(w, lo, hi);
-    }
-}
-
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 __device__ __forceinline__ float lds_f32(uint32_t addr) { return __uint_as_float(lds_u32(addr)); }
-
-// a scale as used: at least 2^-100 (a NaN stays one)
-__device__ __forceinline__ float used_scale(float s) { return s < 0x1p-100f ? 0x1p-100f : s; }
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");

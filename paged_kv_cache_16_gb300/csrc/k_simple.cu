@@ -104,32 +104,26 @@ __device__ __forceinline__ void expand16(const uint4 codes, uint4 *dst) {
     dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
-// Block-scaled caches: the same with each head's scale, code * scale rounded
-// once to bf16 (exact for scales that are powers of two).
+// Block-scaled caches: K codes to bf16, V codes to f16 (both exact), and the
+// three factors of each (block, kv head) that the tiles' softmax applies.
 template <bool INT8>
-__device__ __forceinline__ void expand16_scaled(const uint4 codes, float scale, uint4 *dst) {
+__device__ __forceinline__ void expand16_codes(const uint4 codes, bool value, uint4 *dst) {
     const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
     uint32_t o[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float x[4];
-        if constexpr (INT8) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = static_cast<float>(static_cast<int8_t>(w[i] >> (8 * k)));
-        } else {
-            uint32_t lo, hi;
-            dev::e4m3x4_to_f16x2x2(w[i], lo, hi);
-            x[0] = dev::f16_lo(lo); x[1] = dev::f16_hi(lo); x[2] = dev::f16_lo(hi); x[3] = dev::f16_hi(hi);
+        dev::codes_to_f16<INT8>(w[i], o[2 * i], o[2 * i + 1]);
+        if (!value) {
+            o[2 * i] = dev::pack_bf16x2(dev::f16_lo(o[2 * i]), dev::f16_hi(o[2 * i]));
+            o[2 * i + 1] = dev::pack_bf16x2(dev::f16_lo(o[2 * i + 1]), dev::f16_hi(o[2 * i + 1]));
         }
-        o[2 * i] = dev::pack_bf16x2(x[0] * scale, x[1] * scale);
-        o[2 * i + 1] = dev::pack_bf16x2(x[2] * scale, x[3] * scale);
     }
     dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
     dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
 }
 
 template <bool INT8>
-__global__ void dequant_scaled_kernel(DequantParams p) {
+__global__ void expand_scaled_kernel(DequantParams p) {
     dev::grid_launch_dependents();
     dev::grid_dep_wait();
     const int32_t n = p.counts[kCountDequant];
@@ -139,38 +133,42 @@ __global__ void dequant_scaled_kernel(DequantParams p) {
         const int32_t src = p.block_table[static_cast<int64_t>(it.req) * p.max_blocks + it.block];
         uint4 *kd = reinterpret_cast<uint4 *>(p.key_out + static_cast<int64_t>(it.dst) * p.block_elems);
         uint4 *vd = reinterpret_cast<uint4 *>(p.value_out + static_cast<int64_t>(it.dst) * p.block_elems);
+        float4 *fd = p.factors + it.dst;
         if (src < 0 || src >= p.num_blocks) {
             if (threadIdx.x == 0) atomicOr(p.err, kErrBlockRange);
             for (int32_t c = threadIdx.x; c < 2 * chunks; c += blockDim.x) kd[c] = vd[c] = make_uint4(0, 0, 0, 0);
+            for (int32_t h = threadIdx.x; h < p.num_heads_kv; h += blockDim.x)
+                fd[static_cast<int64_t>(h) * p.n_dst] = make_float4(1.f, 0.f, 1.f, 0.f);
             continue;
         }
         const uint4 *ks = reinterpret_cast<const uint4 *>(p.key_cache + static_cast<int64_t>(src) * p.block_elems);
         const uint4 *vs = reinterpret_cast<const uint4 *>(p.value_cache + static_cast<int64_t>(src) * p.block_elems);
-        const int64_t scales = static_cast<int64_t>(src) * p.num_heads_kv;
-        // a thread's chunks of the block are all loaded before any is stored
+        // a thread's chunks of the block are all loaded before any is
+        // stored: one round trip to memory instead of one per chunk
         constexpr int U = 4;
         for (int32_t c0 = threadIdx.x; c0 < chunks; c0 += U * blockDim.x) {
             uint4 kx[U], vx[U];
-            float ksc[U], vsc[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int32_t c = c0 + u * static_cast<int32_t>(blockDim.x);
                 if (c < chunks) {
-                    const int32_t head = 16 * c / p.head_dim % p.num_heads_kv;
                     kx[u] = __ldg(ks + c);
                     vx[u] = __ldg(vs + c);
-                    ksc[u] = __ldg(p.key_scales + scales + head);
-                    vsc[u] = __ldg(p.value_scales + scales + head);
                 }
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const int32_t c = c0 + u * static_cast<int32_t>(blockDim.x);
                 if (c < chunks) {
-                    expand16_scaled<INT8>(kx[u], ksc[u], kd + 2 * c);
-                    expand16_scaled<INT8>(vx[u], vsc[u], vd + 2 * c);
+                    expand16_codes<INT8>(kx[u], false, kd + 2 * c);
+                    expand16_codes<INT8>(vx[u], true, vd + 2 * c);
                 }
             }
+        }
+        for (int32_t h = threadIdx.x; h < p.num_heads_kv; h += blockDim.x) {
+            const float kf = dev::used_scale(__ldg(p.key_scales + static_cast<int64_t>(src) * p.num_heads_kv + h));
+            const float vf = dev::used_scale(__ldg(p.value_scales + static_cast<int64_t>(src) * p.num_heads_kv + h));
+            fd[static_cast<int64_t>(h) * p.n_dst] = make_float4(kf * p.scale_log2, dev::lg2(vf), 1.f / vf, 0.f);
         }
     }
 }
@@ -381,8 +379,8 @@ cudaError_t launch_write_kv_fp8(const void *key, const void *value, const int64_
 cudaError_t launch_dequant(int grid, const DequantParams &p, cudaStream_t stream, bool pdl) {
     if (grid <= 0) return cudaSuccess;
     if (p.key_scales != nullptr)
-        return p.int8 ? launch_ex(dequant_scaled_kernel<true>, dim3(grid), dim3(256), 0, stream, pdl, p)
-                      : launch_ex(dequant_scaled_kernel<false>, dim3(grid), dim3(256), 0, stream, pdl, p);
+        return p.int8 ? launch_ex(expand_scaled_kernel<true>, dim3(grid), dim3(256), 0, stream, pdl, p)
+                      : launch_ex(expand_scaled_kernel<false>, dim3(grid), dim3(256), 0, stream, pdl, p);
     return launch_ex(dequant_kernel, dim3(grid), dim3(256), 0, stream, pdl, p);
 }
 

@@ -516,7 +516,7 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
         }
         P->scratch_table.assign(reqs.size() * static_cast<size_t>(P->max_blocks), 0);
         for (size_t row = 0; row < reqs.size(); ++row)
-            for (int32_t b = lo[row]; b < hi[row]; ++b) {
+            for (int32_t b = lo[row]; b < hi[row]; ++b) {   // consecutive copies (block-scaled tiles rely on it)
                 DequantItem di{};
                 di.req = reqs[row];
                 di.block = b;
@@ -798,6 +798,10 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
     off = align_up(off + scratch_bytes, 1024);
     P->off_vscr = off;
     off = align_up(off + scratch_bytes, 256);
+    if (P->scaled) {
+        P->off_factors = off;
+        off = align_up(off + static_cast<size_t>(P->cap_dequant) * P->Hkv * sizeof(float4), 256);
+    }
     P->ws_bytes = off;
     P->blob.assign(P->blob_bytes, 0);
     auto put = [&](size_t at, const void *src, size_t n) {
@@ -906,7 +910,8 @@ pa_status prepare_plan(pa_plan_s *P) {
     if (P->ncta > 0 && (P->scaled ? prepare_scaled_decode(P->D, P->HG, P->int8) : prepare_decode(P->D, P->HG, P->kv8)) !=
                            cudaSuccess)
         return PA_ERR_CUDA;
-    if (P->cap_tiles > 0 && prepare_extend(P->D) != cudaSuccess) return PA_ERR_CUDA;
+    if (P->cap_tiles > 0 && (P->scaled ? prepare_scaled_extend(P->D) : prepare_extend(P->D)) != cudaSuccess)
+        return PA_ERR_CUDA;
     if (P->fork && side_stream() == nullptr) return PA_ERR_CUDA;
     P->prepared = true;
     return PA_OK;
@@ -995,7 +1000,7 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
             return PA_ERR_CUDA;
     }
     if (P->cap_tiles > 0) {
-        // E4M3: the tiles read bf16 copies of their blocks, made here
+        // 8-bit caches: the tiles read 16-bit copies of their blocks, made here
         CUtensorMap tm_tk = tm_k, tm_tv = tm_v;
         const int32_t *tile_table = block_table;
         int32_t tile_blocks = P->num_blocks;
@@ -1015,13 +1020,17 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
             qp.key_scales = scales.key;
             qp.value_scales = scales.value;
             qp.num_heads_kv = P->Hkv;
-            qp.head_dim = P->D;
+            qp.factors = reinterpret_cast<float4 *>(ws + P->off_factors);
+            qp.n_dst = P->cap_dequant;
             qp.int8 = P->int8 ? 1 : 0;
+            qp.scale_log2 = P->scale_log2;
             if (launch_dequant(std::min(P->cap_dequant, 8 * sms), qp, tile_stream, !fork) != cudaSuccess)
                 return PA_ERR_CUDA;
             const uint64_t srows = static_cast<uint64_t>(std::max(1, P->cap_dequant)) * kBlockSize;
-            if (!make_map(&tm_tk, ws + P->off_kscr, P->D, P->Hkv, srows, 1, kBlockSize) ||
-                !make_map(&tm_tv, ws + P->off_vscr, P->D, P->Hkv, srows, 1, kBlockSize))
+            // (block-scaled: a key tile's copies in one box)
+            const uint32_t box = P->scaled ? kTileKeys : kBlockSize;
+            if (!make_map(&tm_tk, ws + P->off_kscr, P->D, P->Hkv, srows, 1, box) ||
+                !make_map(&tm_tv, ws + P->off_vscr, P->D, P->Hkv, srows, 1, box))
                 return PA_ERR_CUDA;
             tile_table = reinterpret_cast<const int32_t *>(ws + P->off_scrtab);
             tile_blocks = P->cap_dequant;
@@ -1047,7 +1056,9 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
         ep.scale_log2 = P->scale_log2;
         ep.out_scale = P->out_scale;
         if (rec(1, true, tile_stream) != cudaSuccess) return PA_ERR_CUDA;
-        if (launch_extend(P->D, P->ext_ctas, tm_q, tm_tk, tm_tv, ep, tile_stream, !fork) != cudaSuccess)
+        const ScaledExtendParams sep{ep, reinterpret_cast<const float4 *>(ws + P->off_factors)};
+        if ((P->scaled ? launch_scaled_extend(P->D, P->ext_ctas, tm_q, tm_tk, tm_tv, sep, tile_stream, !fork)
+                       : launch_extend(P->D, P->ext_ctas, tm_q, tm_tk, tm_tv, ep, tile_stream, !fork)) != cudaSuccess)
             return PA_ERR_CUDA;
         if (rec(1, false, tile_stream) != cudaSuccess) return PA_ERR_CUDA;
         // staged: the rows from the decode prefix on are the tiles' alone

@@ -163,7 +163,14 @@ struct ExtendParams {
     float out_scale;            // v_scale (1 for bf16 caches)
 };
 
-// FP8 caches: one cache block the tensor-core tiles read, expanded to bf16.
+// The same over block-scaled 8-bit caches (base.out_scale is unused): the K
+// tiles are bf16 copies, the V tiles f16 copies of the codes.
+struct ScaledExtendParams {
+    ExtendParams base;
+    const float4 *factors;      // [Hkv][base.num_blocks copies]: {ks * scale_log2, log2 vs, 1 / vs, 0}
+};
+
+// 8-bit caches: one cache block the tensor-core tiles read, expanded to 16 bits.
 struct DequantItem {
     int32_t req;                // block-table row of the source block
     int32_t block;              // logical block index in that row
@@ -183,10 +190,12 @@ struct DequantParams {
     int32_t max_blocks;
     int32_t num_blocks;
     int32_t block_elems;        // 16 * Hkv * D
-    // block-scaled caches: the copies hold code * scale, rounded once to bf16
-    const float *key_scales;    // [num_blocks][Hkv]; null: the code values
+    // block-scaled caches: K as bf16, V as f16 code values, and the factors
+    const float *key_scales;    // [num_blocks][Hkv]; null: E4M3, one scale per tensor
     const float *value_scales;
-    int32_t num_heads_kv, head_dim, int8;
+    float4 *factors;            // [Hkv][n_dst] (see ScaledExtendParams)
+    int32_t num_heads_kv, n_dst, int8;
+    float scale_log2;
 };
 
 struct MergeParams {
@@ -337,6 +346,9 @@ cudaError_t launch_scaled_decode(int head_dim, int hg, bool int8, int num_ctas, 
                                  const CUtensorMap &tm_v, const ScaledDecodeParams &p, cudaStream_t stream);
 cudaError_t launch_extend(int head_dim, int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const ExtendParams &p, cudaStream_t stream, bool pdl = true);
+cudaError_t launch_scaled_extend(int head_dim, int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
+                                 const CUtensorMap &tm_v, const ScaledExtendParams &p, cudaStream_t stream,
+                                 bool pdl = true);
 cudaError_t launch_merge(int head_dim, int grid, const MergeParams &p, cudaStream_t stream, bool pdl = true);
 // Copy `bytes` (a multiple of 16) from device-accessible pinned host memory
 // to device memory with a kernel.
@@ -356,5 +368,6 @@ cudaError_t launch_zero_blocks(const int32_t *ids, int32_t num_ids, int32_t num_
 cudaError_t prepare_decode(int head_dim, int hg, bool kv8);
 cudaError_t prepare_scaled_decode(int head_dim, int hg, bool int8);
 cudaError_t prepare_extend(int head_dim);
+cudaError_t prepare_scaled_extend(int head_dim);
 
 }  // namespace pa

@@ -41,7 +41,7 @@ struct pa_plan_s {
     int32_t num_slots = 0;
     // workspace layout
     size_t off_part = 0, off_cta = 0, off_items = 0, off_tiles = 0, off_merges = 0;
-    size_t off_scrtab = 0, off_dequant = 0, off_kscr = 0, off_vscr = 0, off_runs = 0;
+    size_t off_scrtab = 0, off_dequant = 0, off_kscr = 0, off_vscr = 0, off_factors = 0, off_runs = 0;
     size_t off_ctb = 0, off_ctiles = 0;
     size_t blob_bytes = 0, off_opart = 0, off_ml = 0, ws_bytes = 0;
     // launch shape: exact sizes for pa_plan, capacities for pa_plan_fixed

@@ -134,7 +134,6 @@ class Case:
                     self.vc[self.table[r, b], self.seq[r] % BLOCK:] = bad
         sc[:, ~torch.from_numpy(used)] = float("nan")          # scales of unread blocks: anything
         self.ks, self.vs = sc[0].contiguous(), sc[1].contiguous()
-        self.exact_copies = scales != "any"
         self.T = int(self.q_lens.sum())
         self.q = (torch.randn(max(self.T, 1), hq, d, generator=g) * q_size).to(torch.bfloat16)
         self.qsl = np.concatenate([[0], np.cumsum(self.q_lens)]).astype(np.int32)
@@ -150,17 +149,14 @@ class Case:
         return kw
 
     def reference(self):
-        """(out, tolerance) [T, Hq, D] in float64, and whether the tiles' bound
-        applies is left to the larger of the two bounds.
+        """(out, tolerance) [T, Hq, D] in float64.
 
         Per row: A = sum p |v|, S = scale * max_j sum_d |q_d k_jd|.  Scores: the
         fp32 accumulation of D products and the block-wise factors stay within
-        2^-20 S, exponentials and logarithms add 2^-20.  Decode kernel: weights
-        rounded to f16 (2^-11 each, or 2^-24 absolute below its normal range, the
-        largest weight times value scale being at least 1: n 2^-24 M, M = max p_j
-        vs_j QMAX).  Tiles: weights rounded to bf16 (2^-8), and for scales that are no
-        powers of two K and V rounded to bf16 (2^-8 S in the score, 2^-8 A).  A score
-        error e changes out by at most 2 e A.  The output: half a bf16 step."""
+        2^-20 S, exponentials and logarithms add 2^-20; a score error e changes out
+        by at most 2 e A.  Weights are rounded to f16: 2^-11 each, or 2^-24 absolute
+        below its normal range, the largest weight times value scale being at least
+        1 (n 2^-24 M, M = max p_j vs_j QMAX).  The output: half a bf16 step."""
         T, hq, d = max(self.T, 1), self.hq, self.d
         out, tol = np.zeros((T, hq, d)), np.zeros((T, hq, d))
         kv = [(values(c.numpy(), self.code), s.double().numpy()) for c, s in ((self.kc, self.ks), (self.vc, self.vs))]
@@ -182,16 +178,9 @@ class Case:
                     o, A = p @ v, p @ np.abs(v)
                     M = (p * vs).max(1) * QMAX[self.code]
                     es = S * 2.0 ** -20 + 2.0 ** -20
-                    dec = A * (2.0 ** -11 + 2 * es[:, None]) + (n * 2.0 ** -24 * M)[:, None]
-                    et = es if self.exact_copies else es + S * BF16
-                    # (e^x - 1 for errors that are not small)
-                    tile = A * (BF16 + 2 * np.expm1(np.minimum(et, 50))[:, None] + (0 if self.exact_copies else BF16))
                     out[t, h * G:(h + 1) * G] = o
-                    tol[t, h * G:(h + 1) * G] = BF16 * np.abs(o) + (np.maximum(dec, tile) if self.on_tiles(r) else dec)
+                    tol[t, h * G:(h + 1) * G] = BF16 * np.abs(o) + A * (2.0 ** -11 + 2 * es[:, None]) + (n * 2.0 ** -24 * M)[:, None]
         return out, tol
-
-    def on_tiles(self, r):
-        return self.n_common > 0 or self.hq // self.hkv > 16 or self.q_lens[r] > max(1, 16 // (self.hq // self.hkv))
 
 
 class OnGpu:

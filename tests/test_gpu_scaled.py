@@ -48,7 +48,7 @@ def test_verify_rows(code, hq, hkv, d):
 
 
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
-@pytest.mark.parametrize("scales", ["power", "any"])
+@pytest.mark.parametrize("scales", ["power", "any", "wild"])
 @pytest.mark.parametrize("hq,hkv,d", [(4, 2, 64), (8, 2, 128), (32, 1, 128), (40, 2, 64), (28, 4, 128)])
 def test_tile_rows(code, scales, hq, hkv, d):
     """Chunks on the tensor-core tiles (odd lengths, cached contexts that end
@@ -97,8 +97,9 @@ def test_one_key_is_its_value():
 
 
 def test_matches_the_tensor_scale_kernel():
-    """Equal scales everywhere: the E4M3 kernel with one scale per tensor on the
-    same codes agrees within both kernels' bounds."""
+    """Equal scales everywhere: the E4M3 kernels with one scale per tensor on the
+    same codes agree within both bounds (theirs: bf16 weights on the tiles,
+    2^-8 of sum p |v|, at most the largest value)."""
     c = oc.Case(hq=8, hkv=2, d=128, q_lens=[1, 4, 1, 60], seq_lens=[700, 90, 33, 200], code="e4m3", seed=7)
     used = torch.isfinite(c.ks)
     c.ks[used], c.vs[used] = 0.03125, 0.0625
@@ -108,7 +109,7 @@ def test_matches_the_tensor_scale_kernel():
     ws = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device=DEV)
     binding.pa_attention(plan, g.q, g.kc, g.vc, g.table, out, ws)
     ref, tol = c.reference()
-    oc.assert_within(out, ref, 2 * tol)
+    oc.assert_within(out, ref, 2 * tol + oc.BF16 * 448 * 0.0625)
 
 
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
