@@ -12,6 +12,7 @@ import os
 from dataclasses import dataclass
 
 import numpy as np
+import torch
 
 from . import build as _build
 
@@ -304,7 +305,6 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
         return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
@@ -589,44 +589,32 @@ def pa_rope_status(*, rotary_dim, layout=PA_ROPE_HALF, base=10000.0, scaling=PA_
     return st
 
 
-def _rows(t, name: str) -> int:
-    """Token stride of bf16 rows [T, heads, D] whose heads are dense (views of
+_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+_PLAIN_CACHES = {torch.bfloat16: PA_KV_BF16, torch.uint8: PA_KV_FP8_E4M3}
+_SCALED_CACHES = {torch.uint8: PA_KV_FP8_E4M3_BLOCK, torch.int8: PA_KV_INT8_BLOCK}
+
+
+def _rows(t, d: int, name: str) -> int:
+    """Token stride of bf16 rows [tokens, heads, d] with dense heads (views of
     a packed projection output are)."""
-    if t.dim() != 3 or t.element_size() != 2 or t.stride(2) != 1 or t.stride(1) != t.shape[2]:
-        raise ValueError(f"{name}: bf16 rows [tokens, heads, head_dim] with dense heads wanted")
-    return int(t.stride(0)) if t.shape[0] > 1 else max(int(t.stride(0)), t.shape[1] * t.shape[2])
-
-
-def _same_rows(a, b, what: str):
-    if tuple(a.shape) != tuple(b.shape):
-        raise ValueError(f"{what}: shapes {tuple(a.shape)} and {tuple(b.shape)} differ")
-
-
-def _dense(t, dtype: str, shape, name: str):
-    """A contiguous tensor of this dtype (and shape, unless None)."""
-    if str(t.dtype) != "torch." + dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
-        raise ValueError(f"{name}: a contiguous {dtype} tensor{'' if shape is None else f' of shape {tuple(shape)}'} wanted")
+    s = t.stride()
+    if t.dtype is not _BF16 or len(s) != 3 or s[2] != 1 or s[1] != d:
+        raise ValueError(f"{name}: bf16 rows [tokens, heads, {d}] with dense heads wanted")
+    return s[0]
 
 
 def pa_rotary(rope: Rope, x, positions, out, stream=None):
     """out = x (bf16 [T, H, D], token stride free) rotated by positions (int32
     [T]); out may be x."""
-    xs, os_ = _rows(x, "x"), _rows(out, "out")
-    _same_rows(x, out, "x and out")
-    T, H, D = x.shape
-    _dense(positions, "int32", (T,), "positions")
-    _check(load().pa_rotary(rope.handle, _ptr(x), xs, _ptr(positions), T, H, D, _ptr(out), os_, _stream(stream)),
-           "pa_rotary")
-
-
-def _cache_dtype(cache, scales) -> int:
-    """PA_KV_* of a cache tensor: bf16, uint8 (E4M3 codes, block-scaled when
-    there are scales) or int8 (block-scaled)."""
-    kind = {"torch.bfloat16": PA_KV_BF16, "torch.uint8": PA_KV_FP8_E4M3 if scales is None else PA_KV_FP8_E4M3_BLOCK,
-            "torch.int8": PA_KV_INT8_BLOCK}.get(str(cache.dtype))
-    if kind is None or (kind in (PA_KV_BF16,) and scales is not None) or (kind == PA_KV_INT8_BLOCK and scales is None):
-        raise ValueError(f"a cache of {cache.dtype} {'with' if scales is not None else 'without'} block scales is none of PA_KV_*")
-    return kind
+    shape = T, H, D = x.shape
+    xs, os_ = _rows(x, D, "x"), _rows(out, D, "out")
+    if out.shape != shape or positions.dtype is not _I32 or positions.numel() != T or not positions.is_contiguous():
+        raise ValueError("out: x's shape wanted; positions: contiguous int32 [tokens]")
+    if T <= 1:   # a single row's stride is anything
+        xs = os_ = H * D
+    st = load().pa_rotary(rope.handle, x.data_ptr(), xs, positions.data_ptr(), T, H, D, out.data_ptr(), os_, _stream(stream))
+    if st:
+        _check(st, "pa_rotary")
 
 
 def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, block_table, key_cache, value_cache, *,
@@ -636,40 +624,46 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
     (see pa.h).  The cache's type follows from the tensors: bf16; uint8 E4M3
     codes with k_scale / v_scale; uint8 or int8 codes with key_scales and
     value_scales (float [num_blocks, Hkv])."""
-    T, hkv, d = key.shape
-    _same_rows(key, value, "key and value")
-    nb, bs = key_cache.shape[:2]
-    kind = _cache_dtype(key_cache, key_scales)
-    for c, name in ((key_cache, "key_cache"), (value_cache, "value_cache")):
-        _dense(c, str(key_cache.dtype)[6:], (nb, bs, hkv, d), name)
-    if (key_scales is None) != (value_scales is None):
-        raise ValueError("key_scales and value_scales come together")
-    if key_scales is not None:
-        _dense(key_scales, "float32", (nb, hkv), "key_scales")
-        _dense(value_scales, "float32", (nb, hkv), "value_scales")
-    R = int(num_computed.numel())
-    _dense(num_computed, "int32", (R,), "num_computed")
-    _dense(query_start_loc, "int32", (R + 1,), "query_start_loc")
-    _dense(block_table, "int32", (R, block_table.shape[-1]), "block_table")
-    a = AppendArgs()
-    a.num_reqs, a.num_tokens, a.num_heads_kv, a.head_dim, a.block_size = R, T, hkv, d, bs
-    a.num_blocks, a.max_blocks_per_req, a.kv_cache_dtype = nb, int(block_table.shape[1]), kind
-    a.k_scale, a.v_scale = float(k_scale), float(v_scale)
-    a.query_start_loc, a.num_computed_tokens, a.block_table = _ptr(query_start_loc), _ptr(num_computed), _ptr(block_table)
-    a.key, a.key_stride, a.value, a.value_stride = _ptr(key), _rows(key, "key"), _ptr(value), _rows(value, "value")
-    if (q is None) != (q_out is None):
+    shape = T, hkv, d = key.shape
+    ks, vs = _rows(key, d, "key"), _rows(value, d, "value")
+    pool, dtype = key_cache.shape, key_cache.dtype
+    nb, bs = pool[0], pool[1]
+    if value.shape != shape or pool != (nb, bs, hkv, d) or value_cache.shape != pool or value_cache.dtype is not dtype or \
+            not key_cache.is_contiguous() or not value_cache.is_contiguous():
+        raise ValueError(f"value: key's shape wanted; caches: contiguous [num_blocks, block_size, {hkv}, {d}] of one type")
+    ksc = vsc = 0
+    if key_scales is not None and value_scales is not None:
+        kind = _SCALED_CACHES.get(dtype)
+        if key_scales.dtype is not _F32 or value_scales.dtype is not _F32 or key_scales.shape != (nb, hkv) or \
+                value_scales.shape != (nb, hkv) or not key_scales.is_contiguous() or not value_scales.is_contiguous():
+            raise ValueError(f"scales: contiguous float [{nb}, {hkv}] wanted")
+        ksc, vsc = key_scales.data_ptr(), value_scales.data_ptr()
+    else:
+        kind = _PLAIN_CACHES.get(dtype) if key_scales is value_scales else None
+    if kind is None:
+        raise ValueError(f"caches of {dtype} with these scales are none of PA_KV_*")
+    R, mb = block_table.shape
+    if num_computed.dtype is not _I32 or query_start_loc.dtype is not _I32 or block_table.dtype is not _I32 or \
+            num_computed.numel() != R or query_start_loc.numel() != R + 1 or not block_table.is_contiguous() or \
+            not num_computed.is_contiguous() or not query_start_loc.is_contiguous():
+        raise ValueError("query_start_loc [R + 1], num_computed [R], block_table [R, blocks]: contiguous int32 wanted")
+    hq = qp = qs = op = os_ = 0
+    if q is not None and q_out is not None:
+        hq, qp, op = q.shape[1], q.data_ptr(), q_out.data_ptr()
+        qs, os_ = _rows(q, d, "q"), _rows(q_out, d, "q_out")
+        if q.shape != (T, hq, d) or q_out.shape != (T, hq, d):
+            raise ValueError(f"q, q_out: rows [{T}, heads, {d}] wanted")
+    elif q is not q_out:
         raise ValueError("q and q_out come together")
-    if q is not None:
-        _same_rows(q, q_out, "q and q_out")
-        if q.shape[0] != T or q.shape[2] != d:
-            raise ValueError("q: rows of key's tokens and head_dim wanted")
-        a.num_heads_q = q.shape[1]
-        a.q, a.q_stride, a.q_out, a.q_out_stride = _ptr(q), _rows(q, "q"), _ptr(q_out), _rows(q_out, "q_out")
-    a.key_cache, a.value_cache = _ptr(key_cache), _ptr(value_cache)
-    a.key_scales, a.value_scales = _ptr(key_scales), _ptr(value_scales)
-    a.device_error_word = _ptr(device_error_word)
-    _check(load().pa_append_kv(rope.handle if rope is not None else None, ctypes.byref(a), _stream(stream)),
-           "pa_append_kv")
+    if T <= 1:   # a single row's stride is anything
+        ks = vs = hkv * d
+        qs = os_ = hq * d
+    a = AppendArgs(R, T, hq, hkv, d, bs, nb, mb, kind, k_scale, v_scale, query_start_loc.data_ptr(), num_computed.data_ptr(),
+                   block_table.data_ptr(), key.data_ptr(), value.data_ptr(), ks, vs, qp, op, qs, os_, key_cache.data_ptr(),
+                   value_cache.data_ptr(), ksc, vsc, _ptr(device_error_word))
+    st = load().pa_append_kv(rope.handle if rope is not None else None, a, _stream(stream))
+    if st:
+        _check(st, "pa_append_kv")
 
 
 def pa_attention_scaled(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace,

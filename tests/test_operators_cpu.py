@@ -137,6 +137,8 @@ def test_append_wrapper_checks():
                 dict(key_scales=None), dict(value_scales=None), dict(key_scales=c.ks.double()), dict(key_scales=c.ks[:, :1]),
                 dict(key_cache=c.kc.to(torch.int16)), dict(value_cache=c.vc.view(torch.uint8)), dict(key_cache=c.kc.to(torch.bfloat16)),
                 dict(query_start_loc=i32(c.qsl)[:-1]), dict(num_computed=i32(c.nc).long()), dict(rope=rope, q=c.q),
+                dict(block_table=i32(c.table).long()), dict(key_cache=c.kc[:, :, :1]), dict(rope=rope, q_out=c.q.contiguous()),
+                dict(key_scales=None, value_scales=None), dict(rope=rope, q=c.q[:2], q_out=c.q[:2]),
                 dict(rope=rope, q=c.q, q_out=torch.empty(4, 2, 64, dtype=torch.bfloat16))):
         with pytest.raises(ValueError):
             binding.pa_append_kv(**{**good, **bad})
