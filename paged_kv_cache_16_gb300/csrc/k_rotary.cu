@@ -40,91 +40,159 @@ __device__ __forceinline__ void fill_table(float *tab, const RopeParams &rope, i
     }
 }
 
-// A unit is eight elements of a row that one thread handles, as two groups of
-// four at element offsets a and b.  Half layout: dims 4u.. and their partners
-// rd / 2 + 4u..; interleaved and pass-through: dims 8u .. 8u + 7.
+// A unit is 2 W elements of a row that one thread handles, as two groups of W
+// (8 or 16 bytes) at element offsets a and b.  Half layout: dims W u.. and their
+// partners rd / 2 + W u..; interleaved and pass-through: dims 2 W u .. + 2 W - 1.
+// W = 8 where rotary_dim and head_dim are multiples of 16, else 4.
+template <int W>
 struct Unit {
     int a, b;       // element offsets
-    int freq;       // first of its four pairs; < 0: passes through
+    int freq;       // first of its W pairs; < 0: passes through
     bool inter;
-    __device__ __forceinline__ explicit Unit(int u) : a(8 * u), b(8 * u + 4), freq(-1), inter(false) {}
-    __device__ __forceinline__ Unit(int u, const RopeParams &r) {
+    __device__ __forceinline__ explicit Unit(int u) : a(2 * W * u), b(2 * W * u + W), freq(-1), inter(false) {}
+    __device__ __forceinline__ Unit(int u, const RopeParams &r) : Unit(u) {
+        if (2 * W * u >= r.rotary_dim) return;
+        freq = W * u;
         inter = r.interleaved != 0;
-        if (8 * u < r.rotary_dim) {
-            freq = 4 * u;
-            a = inter ? 8 * u : 4 * u;
-            b = inter ? 8 * u + 4 : r.rotary_dim / 2 + 4 * u;
-        } else {
-            freq = -1;
-            a = 8 * u;
-            b = 8 * u + 4;
+        if (!inter) {
+            a = W * u;
+            b = r.rotary_dim / 2 + W * u;
         }
     }
 };
 
-__device__ __forceinline__ void unpack4(uint2 w, float (&x)[4]) {
-    x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
+template <int W>
+struct Raw {   // W bf16
+    uint32_t w[W / 2];
+};
+
+template <int W>
+__device__ __forceinline__ Raw<W> load_raw(const uint16_t *p) {
+    Raw<W> r;
+    if constexpr (W == 8) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(p);
+        r.w[0] = v.x; r.w[1] = v.y; r.w[2] = v.z; r.w[3] = v.w;
+    } else {
+        const uint2 v = *reinterpret_cast<const uint2 *>(p);
+        r.w[0] = v.x; r.w[1] = v.y;
+    }
+    return r;
 }
 
-// xa, xb: the unit's two groups; tab: its token's table row.  A product and an
-// fma: two roundings in 32 bits.
-__device__ __forceinline__ void rotate(const Unit &u, const float *tab, int half, float (&xa)[4], float (&xb)[4]) {
-    if (u.freq < 0) return;
-    const float4 c4 = *reinterpret_cast<const float4 *>(tab + u.freq);
-    const float4 s4 = *reinterpret_cast<const float4 *>(tab + half + u.freq);
-    const float c[4] = {c4.x, c4.y, c4.z, c4.w}, s[4] = {s4.x, s4.y, s4.z, s4.w};
-    auto turn = [](float &x, float &y, float cc, float ss) {
-        const float nx = fmaf(x, cc, -(y * ss)), ny = fmaf(y, cc, x * ss);
-        x = nx;
-        y = ny;
-    };
-    if (u.inter) {
-        turn(xa[0], xa[1], c[0], s[0]);
-        turn(xa[2], xa[3], c[1], s[1]);
-        turn(xb[0], xb[1], c[2], s[2]);
-        turn(xb[2], xb[3], c[3], s[3]);
-    } else {
+template <int W>
+__device__ __forceinline__ void store_raw(uint16_t *p, const Raw<W> &r) {
+    if constexpr (W == 8) *reinterpret_cast<uint4 *>(p) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+    else *reinterpret_cast<uint2 *>(p) = make_uint2(r.w[0], r.w[1]);
+}
+
+template <int W>
+__device__ __forceinline__ void unpack(const Raw<W> &r, float (&x)[W]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) turn(xa[i], xb[i], c[i], s[i]);
+    for (int i = 0; i < W / 2; ++i) {
+        x[2 * i] = bf16_lo(r.w[i]);
+        x[2 * i + 1] = bf16_hi(r.w[i]);
     }
 }
+
+template <int W>
+__device__ __forceinline__ Raw<W> pack(const float (&x)[W]) {
+    Raw<W> r;
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) r.w[i] = pack_bf16x2(x[2 * i], x[2 * i + 1]);
+    return r;
+}
+
+// cos and sin of a unit's pairs at one token's position
+template <int W>
+struct Turn {
+    float c[W], s[W];
+    __device__ __forceinline__ void load(const Unit<W> &u, const float *tab, int half) {
+        if (u.freq < 0) return;
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const float4 c4 = *reinterpret_cast<const float4 *>(tab + u.freq + i);
+            const float4 s4 = *reinterpret_cast<const float4 *>(tab + half + u.freq + i);
+            c[i] = c4.x; c[i + 1] = c4.y; c[i + 2] = c4.z; c[i + 3] = c4.w;
+            s[i] = s4.x; s[i + 1] = s4.y; s[i + 2] = s4.z; s[i + 3] = s4.w;
+        }
+    }
+    // a product and an fma: two roundings in 32 bits
+    __device__ __forceinline__ void apply(const Unit<W> &u, float (&xa)[W], float (&xb)[W]) const {
+        if (u.freq < 0) return;
+        auto turn = [](float &x, float &y, float cc, float ss) {
+            const float nx = fmaf(x, cc, -(y * ss)), ny = fmaf(y, cc, x * ss);
+            x = nx;
+            y = ny;
+        };
+        if (u.inter) {
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+                turn(xa[2 * i], xa[2 * i + 1], c[i], s[i]);
+                turn(xb[2 * i], xb[2 * i + 1], c[W / 2 + i], s[W / 2 + i]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) turn(xa[i], xb[i], c[i], s[i]);
+        }
+    }
+};
 
 // Rotate `n_tok` x `n_heads` rows of bf16 (x and out: first row of the first
-// token; consecutive heads D apart) by the table of the tokens.
+// token; consecutive heads D apart) by the table of the tokens.  The threads are
+// dealt to 1 << log_tokens >= n_tok tokens; a thread keeps one unit of one
+// token, its cos and sin in registers, and walks the heads with kBatch rows'
+// loads before the first of their stores.
+template <int W, int kBatch>
 __device__ __forceinline__ void rotate_rows(const float *tab, const RopeParams &rope, const uint16_t *x, int64_t x_stride,
-                                            uint16_t *out, int64_t out_stride, int n_tok, int n_heads, int head_dim) {
-    const int upr = head_dim / 8;                   // units per row
-    const int rpi = kThreads / upr;                 // rows of one pass over the threads
-    const int first = threadIdx.x / upr;
-    if (first >= rpi) return;                       // head_dim does not divide the threads' elements
-    const Unit u(threadIdx.x % upr, rope);
-    const int half = rope.rotary_dim / 2;
-    const int rows = n_tok * n_heads;
-#pragma unroll 4
-    for (int r = first; r < rows; r += rpi) {
-        const int j = r / n_heads, h = r - j * n_heads;
-        const uint16_t *src = x + j * x_stride + h * head_dim;
-        uint16_t *dst = out + j * out_stride + h * head_dim;
-        float xa[4], xb[4];
-        unpack4(*reinterpret_cast<const uint2 *>(src + u.a), xa);
-        unpack4(*reinterpret_cast<const uint2 *>(src + u.b), xb);
-        rotate(u, tab + j * rope.rotary_dim, half, xa, xb);
-        *reinterpret_cast<uint2 *>(dst + u.a) = make_uint2(pack_bf16x2(xa[0], xa[1]), pack_bf16x2(xa[2], xa[3]));
-        *reinterpret_cast<uint2 *>(dst + u.b) = make_uint2(pack_bf16x2(xb[0], xb[1]), pack_bf16x2(xb[2], xb[3]));
+                                            uint16_t *out, int64_t out_stride, int n_tok, int log_tokens, int n_heads,
+                                            int head_dim) {
+    const int per = kThreads >> log_tokens;         // threads of a token
+    const int j = threadIdx.x / per, r = threadIdx.x % per;
+    const int upr = head_dim / (2 * W);             // units per row
+    const int lanes = per / upr;                    // rows at a time
+    const int h0 = r / upr;
+    if (j >= n_tok || h0 >= lanes) return;
+    const Unit<W> u(r % upr, rope);
+    Turn<W> turn;
+    turn.load(u, tab + j * rope.rotary_dim, rope.rotary_dim / 2);
+    x += j * x_stride;
+    out += j * out_stride;
+    for (int h = h0; h < n_heads; h += kBatch * lanes) {
+        Raw<W> wa[kBatch], wb[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int hk = h + k * lanes;
+            if (hk < n_heads) {
+                wa[k] = load_raw<W>(x + hk * head_dim + u.a);
+                wb[k] = load_raw<W>(x + hk * head_dim + u.b);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int hk = h + k * lanes;
+            if (hk >= n_heads) break;
+            float xa[W], xb[W];
+            unpack<W>(wa[k], xa);
+            unpack<W>(wb[k], xb);
+            turn.apply(u, xa, xb);
+            store_raw<W>(out + hk * head_dim + u.a, pack<W>(xa));
+            store_raw<W>(out + hk * head_dim + u.b, pack<W>(xb));
+        }
     }
 }
 
+template <int W>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RopeParams rope, const RotaryParams p) {
     extern __shared__ float4 smem4[];
     float *tab = reinterpret_cast<float *>(smem4);
     grid_launch_dependents();
     grid_dep_wait();
-    const int t0 = blockIdx.x * p.tokens_per_cta, h0 = blockIdx.y * p.heads_per_cta;
-    const int n = min(p.tokens_per_cta, p.num_tokens - t0), nh = min(p.heads_per_cta, p.num_heads - h0);
+    const int t0 = blockIdx.x << p.log_tokens, h0 = blockIdx.y * p.heads_per_cta;
+    const int n = min(1 << p.log_tokens, p.num_tokens - t0), nh = min(p.heads_per_cta, p.num_heads - h0);
     fill_table(tab, rope, n, [&](int j) { return __ldg(p.positions + t0 + j); });
     __syncthreads();
-    rotate_rows(tab, rope, p.x + t0 * p.x_stride + h0 * p.head_dim, p.x_stride,
-                p.out + t0 * p.out_stride + h0 * p.head_dim, p.out_stride, n, nh, p.head_dim);
+    rotate_rows<W, W == 8 ? 5 : 8>(tab, rope, p.x + t0 * p.x_stride + h0 * p.head_dim, p.x_stride,
+                   p.out + t0 * p.out_stride + h0 * p.head_dim, p.out_stride, n, p.log_tokens, nh, p.head_dim);
 }
 
 // ------------------------------------------------------------------ append --
@@ -140,13 +208,16 @@ struct Segment {
 // floor(query_start_loc[r] / 16) + 2 r on, which are as many as it can have
 // segments (a request of q tokens spans at most floor(q / 16) + 2 blocks), so
 // that a grid of num_tokens / 16 + 2 num_reqs CTAs covers every step without
-// the lengths being known on the host.  The request is found by a search with
-// 32 probes a step, one per lane.  Every warp of a CTA makes the same search.
-__device__ __forceinline__ Segment find_segment(const AppendParams &p, int id, bool report) {
+// the lengths being known on the host.  Every warp of a CTA makes the same
+// search: 32 probes a step, one per lane, while there are more than 128 requests
+// left, then the starts and lengths of all of them at once, so that two
+// dependent loads (these, the block id) stand before the scales and the stores.
+__device__ __forceinline__ Segment find_segment(const AppendParams &p, int id) {
     const int lane = threadIdx.x & 31;
     Segment s{0, 0, 0, 0};
-    int lo = 0, len = p.num_reqs;   // the last r in [lo, lo + len) whose first id is <= id (r = lo always is)
-    while (len > 1) {
+    // the last request in [lo, lo + len) whose first id is <= id (lo always is)
+    int lo = 0, len = p.num_reqs;
+    while (len > 128) {
         const int step = (len + 31) / 32;
         const int r = lo + lane * step;
         const bool le = lane * step < len && p.query_start_loc[r] / kBlockSize + 2 * r <= id;
@@ -154,31 +225,61 @@ __device__ __forceinline__ Segment find_segment(const AppendParams &p, int id, b
         len = min(step, len - k * step);
         lo += k * step;
     }
-    const int qb = p.query_start_loc[lo], qe = min(p.query_start_loc[lo + 1], p.num_tokens);
-    const int nc = p.num_computed[lo];
+    // up to 128 requests: all their starts and lengths in one round of loads, lane
+    // l holding requests lo + l + 32 k
+    int32_t qs[4], cs[4], last = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = lane + 32 * k;
+        qs[k] = i < len ? p.query_start_loc[lo + i] : 0;
+        cs[k] = i < len ? p.num_computed[lo + i] : 0;
+    }
+    if (lane == 0) last = p.query_start_loc[lo + len];
+    int at = -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        at += __popc(__ballot_sync(0xffffffffu, lane + 32 * k < len && qs[k] / kBlockSize + 2 * (lo + lane + 32 * k) <= id));
+    at = max(at, 0);
+    auto pick = [&](const int32_t (&v)[4], int i) {
+        int32_t r = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const int32_t y = __shfl_sync(0xffffffffu, v[k], i & 31);
+            if (i >> 5 == k) r = y;
+        }
+        return r;
+    };
+    const int qb = pick(qs, at), nc = pick(cs, at);
+    const int end = __shfl_sync(0xffffffffu, last, 0), next = pick(qs, at + 1);
+    const int qe = min(at + 1 < len ? next : end, p.num_tokens);
+    lo += at;
     const int k = id - (qb / kBlockSize + 2 * lo);
     const int off = nc % kBlockSize;
     const int i0 = k == 0 ? 0 : k * kBlockSize - off;   // first token of the segment within the request
     if (qb < 0 || nc < 0 || k < 0 || i0 >= qe - qb) return s;
     s.pos = nc + i0;
-    const int page = s.pos / kBlockSize;
-    s.block = page < p.max_blocks ? p.block_table[static_cast<int64_t>(lo) * p.max_blocks + page] : -1;
-    if (s.block < 0 || s.block >= p.num_blocks) {
-        if (report && threadIdx.x == 0 && p.err != nullptr) atomicOr(p.err, kErrBlockRange);
-        s.block = -1;                                   // q is still rotated
-    }
     s.t0 = qb + i0;
     s.n = min(kBlockSize - s.pos % kBlockSize, qe - qb - i0);
+    const int page = s.pos / kBlockSize;
+    s.block = page < p.max_blocks ? p.block_table[static_cast<int64_t>(lo) * p.max_blocks + page] : -1;
     return s;
 }
 
+// whether the segment's block exists (else reported); first use of the id
+__device__ __forceinline__ bool block_ok(const AppendParams &p, const Segment &s, bool report) {
+    if (s.block >= 0 && s.block < p.num_blocks) return true;
+    if (report && threadIdx.x == 0 && p.err != nullptr) atomicOr(p.err, kErrBlockRange);
+    return false;
+}
+
 // Four values in units of the scale -> four codes (lowest byte first): to
-// nearest, ties to even, saturating.
+// nearest, ties to even, saturating.  int8: the sum with 1.5 x 2^23 rounds to a
+// whole number, two's complement in its low byte.
 template <bool INT8>
 __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
     if constexpr (INT8) {
-        auto one = [](float x) { return static_cast<uint32_t>(__float2int_rn(fminf(fmaxf(x, -127.f), 127.f))) & 0xFFu; };
-        return one(a) | one(b) << 8 | one(c) << 16 | one(d) << 24;
+        auto one = [](float x) { return __float_as_uint(__fadd_rn(fminf(fmaxf(x, -127.f), 127.f), 12582912.f)); };
+        return prmt(prmt(one(a), one(b), 0x0040u), prmt(one(c), one(d), 0x0040u), 0x5410u);
     } else {
         return static_cast<uint32_t>(pack_e4m3x2(a, b)) | static_cast<uint32_t>(pack_e4m3x2(c, d)) << 16;
     }
@@ -210,181 +311,249 @@ __device__ __forceinline__ float power_scale(float amax) {
     return __uint_as_float(static_cast<uint32_t>(max(e, -64) + 127) << 23);
 }
 
-// One head's rows of a segment in registers: lane (rsub, u) holds unit u of
-// rows it * RPI + rsub as fp32.
-template <int D>
+// One head's rows of a segment: lane (rsub, u) of its warp holds unit u of rows
+// it * RPI + rsub; rows past the segment hold zeros.
+template <int D, int W>
 struct HeadRows {
-    static constexpr int UPR = D / 8, RPI = 32 / UPR, NIT = kBlockSize / RPI;
-    float a[NIT][4], b[NIT][4];
+    static constexpr int UPR = D / (2 * W), RPI = 32 / UPR, NIT = kBlockSize / RPI;
 };
+
+// the largest finite magnitude (infinities saturate and do not count), and
+// whether there is a NaN
+template <int W>
+__device__ __forceinline__ void track(const float (&x)[W], float &amax, bool &nan) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+        const float v = fabsf(x[i]);
+        amax = fmaxf(amax, v <= 3.4028234663852886e38f ? v : 0.f);
+        nan |= v != v;
+    }
+}
+
+template <int W>
+__device__ __forceinline__ void store_codes(uint8_t *p, const uint32_t (&c)[W / 4]) {
+    if constexpr (W == 8) *reinterpret_cast<uint2 *>(p) = make_uint2(c[0], c[1]);
+    else *reinterpret_cast<uint32_t *>(p) = c[0];
+}
 
 // Codes of one head's new rows into block-scaled caches, with the block's new
 // scale; earlier rows of the block are re-coded when it grows.
-template <int D, bool INT8>
-__device__ __forceinline__ void store_scaled(const HeadRows<D> &x, const Unit &u, uint8_t *block, int64_t row_stride,
-                                             float *scale_at, float old, int first, int n, int lane) {
-    using H = HeadRows<D>;
-    float amax = 0.f;
-    bool nan = false;
-#pragma unroll
-    for (int it = 0; it < H::NIT; ++it)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {   // rows past n hold zeros
-            const float va = fabsf(x.a[it][i]), vb = fabsf(x.b[it][i]);
-            // infinities saturate and do not count
-            amax = fmaxf(amax, va <= 3.4028234663852886e38f ? va : 0.f);
-            amax = fmaxf(amax, vb <= 3.4028234663852886e38f ? vb : 0.f);
-            if (INT8) nan |= va != va || vb != vb;
-        }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+// rows(it, xa, xb) gives the lane's two groups of row it * RPI + rsub.
+template <int D, int W, bool INT8, typename Rows>
+__device__ __forceinline__ void store_scaled(Rows rows, float amax, bool nan, const Unit<W> &u, uint8_t *block,
+                                             int64_t row_stride, float *scale_at, float old, int first, int n, int lane) {
+    using H = HeadRows<D, W>;
     float scale = power_scale<INT8>(amax);
-    if (INT8 && __any_sync(0xffffffffu, nan)) scale = __uint_as_float(0x7FC00000u);   // int8 has no NaN: the block's scale is
+    if (INT8 && nan) scale = __uint_as_float(0x7FC00000u);   // int8 has no NaN: the block's scale is
     if (first > 0 && !(scale != scale)) scale = old != old ? old : fmaxf(old, scale);
     if (lane == 0 && (first == 0 || scale != old)) *scale_at = scale;
     const int rsub = lane / H::UPR, unit = lane % H::UPR;
     if (first > 0 && scale > old) {
         const float ratio = __fdiv_rn(old, scale);
         for (int r = rsub; r < first; r += H::RPI) {
-            uint2 *at = reinterpret_cast<uint2 *>(block + r * row_stride + 8 * unit);
-            const uint2 w = *at;
-            float y[4], z[4];
-            decode4<INT8>(w.x, y);
-            decode4<INT8>(w.y, z);
-            *at = make_uint2(encode4<INT8>(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio),
-                             encode4<INT8>(z[0] * ratio, z[1] * ratio, z[2] * ratio, z[3] * ratio));
+            uint8_t *at = block + r * row_stride + 2 * W * unit;
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                uint2 *q = reinterpret_cast<uint2 *>(at) + i;
+                const uint2 w = *q;
+                float y[4], z[4];
+                decode4<INT8>(w.x, y);
+                decode4<INT8>(w.y, z);
+                *q = make_uint2(encode4<INT8>(y[0] * ratio, y[1] * ratio, y[2] * ratio, y[3] * ratio),
+                                encode4<INT8>(z[0] * ratio, z[1] * ratio, z[2] * ratio, z[3] * ratio));
+            }
         }
     }
-    // x / scale; by the reciprocal when it is exact (a power of two)
-    const bool exact = (__float_as_uint(scale) & 0x7FFFFFu) == 0;
-    const float inv = __fdiv_rn(1.f, scale);
-    auto q = [&](float v) { return exact ? v * inv : __fdiv_rn(v, scale); };
+    auto store = [&](auto quotient) {
 #pragma unroll
-    for (int it = 0; it < H::NIT; ++it) {
-        const int r = it * H::RPI + rsub;
-        if (r >= n) continue;
-        uint8_t *row = block + (first + r) * row_stride;
-        *reinterpret_cast<uint32_t *>(row + u.a) = encode4<INT8>(q(x.a[it][0]), q(x.a[it][1]), q(x.a[it][2]), q(x.a[it][3]));
-        *reinterpret_cast<uint32_t *>(row + u.b) = encode4<INT8>(q(x.b[it][0]), q(x.b[it][1]), q(x.b[it][2]), q(x.b[it][3]));
+        for (int it = 0; it < H::NIT; ++it) {
+            if (it * H::RPI >= n) break;
+            const int r = it * H::RPI + rsub;
+            float xa[W], xb[W];
+            rows(it, xa, xb);
+            uint32_t ca[W / 4], cb[W / 4];
+#pragma unroll
+            for (int i = 0; i < W; ++i) { xa[i] = quotient(xa[i]); xb[i] = quotient(xb[i]); }
+#pragma unroll
+            for (int i = 0; i < W / 4; ++i) {
+                ca[i] = encode4<INT8>(xa[4 * i], xa[4 * i + 1], xa[4 * i + 2], xa[4 * i + 3]);
+                cb[i] = encode4<INT8>(xb[4 * i], xb[4 * i + 1], xb[4 * i + 2], xb[4 * i + 3]);
+            }
+            if (r < n) {
+                uint8_t *row = block + (first + r) * row_stride;
+                store_codes<W>(row + u.a, ca);
+                store_codes<W>(row + u.b, cb);
+            }
+        }
+    };
+    // x / scale; by the reciprocal when it is exact (a power of two).  A scale of
+    // another writer's goes the slow way, kept out of the unrolled code
+    if ((__float_as_uint(scale) & 0x7FFFFFu) == 0) {
+        const float inv = __uint_as_float((254u << 23) - __float_as_uint(scale));   // 2^-e of 2^e, |e| < 127
+        const bool plain = __float_as_uint(scale) - (1u << 23) < (252u << 23);
+        store([inv = plain ? inv : __fdiv_rn(1.f, scale)](float v) { return v * inv; });
+    } else {
+        store([scale](float v) { return __fdiv_rn(v, scale); });
     }
 }
 
-template <int D, int KIND>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ RopeParams rope, const AppendParams p) {
-    using H = HeadRows<D>;
+__device__ __forceinline__ int log2_up(int n) { return n <= 1 ? 0 : 32 - __clz(n - 1); }
+
+template <int D, int KIND, int W>
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ RopeParams rope, const AppendParams p) {
+    using H = HeadRows<D, W>;
     constexpr bool BLOCK_SCALED = KIND == kCacheE4m3Block || KIND == kCacheInt8Block;
+    constexpr bool INT8 = KIND == kCacheInt8Block;
     __shared__ float4 smem4[kBlockSize * D / 4];
     float *tab = reinterpret_cast<float *>(smem4);
     grid_launch_dependents();
     grid_dep_wait();
     const int kv_parts = (p.num_heads_kv + 7) / 8;
     const bool kv = static_cast<int>(blockIdx.y) < kv_parts;
-    const Segment s = find_segment(p, blockIdx.x, blockIdx.y == 0);
+    const Segment s = find_segment(p, blockIdx.x);
     if (s.n == 0) return;
     const int half = rope.rotary_dim / 2;
     if (!kv) {
         fill_table(tab, rope, s.n, [&](int j) { return s.pos + j; });
         __syncthreads();
         const int h0 = (static_cast<int>(blockIdx.y) - kv_parts) * p.q_heads_per_cta;
-        rotate_rows(tab, rope, p.q + s.t0 * p.q_stride + h0 * D, p.q_stride, p.q_out + s.t0 * p.q_out_stride + h0 * D,
-                    p.q_out_stride, s.n, min(p.q_heads_per_cta, p.num_heads_q - h0), D);
+        rotate_rows<W, 8>(tab, rope, p.q + s.t0 * p.q_stride + h0 * D, p.q_stride, p.q_out + s.t0 * p.q_out_stride + h0 * D,
+                       p.q_out_stride, s.n, log2_up(s.n), min(p.q_heads_per_cta, p.num_heads_q - h0), D);
         return;
     }
-    if (s.block < 0) return;
     const int lane = threadIdx.x & 31;
     const int h = blockIdx.y * 8 + threadIdx.x / 32;
     const bool mine = h < p.num_heads_kv;
     const int rsub = lane / H::UPR;
-    const Unit u(lane % H::UPR, rope);
-    const Unit uv(lane % H::UPR);   // values: eight consecutive dims
+    const Unit<W> u(lane % H::UPR, rope);
+    const Unit<W> uv(lane % H::UPR);   // values: consecutive dims
     const int first = s.pos % kBlockSize;
-    // every row's loads before the first use
-    uint2 ka[H::NIT], kb[H::NIT];
-    uint4 v[H::NIT];
-    float old_k = 0.f, old_v = 0.f;
-    if (mine) {
-        const int64_t at = static_cast<int64_t>(s.block) * p.num_heads_kv + h;
-        if (BLOCK_SCALED && first > 0) {
-            old_k = p.key_scales[at];
-            old_v = p.value_scales[at];
-        }
+    // every row's loads before the first use of the block id
+    Raw<W> ka[H::NIT], kb[H::NIT], va[H::NIT], vb[H::NIT];
 #pragma unroll
-        for (int it = 0; it < H::NIT; ++it) {
-            const int r = it * H::RPI + rsub;
-            ka[it] = kb[it] = make_uint2(0, 0);
-            v[it] = make_uint4(0, 0, 0, 0);
-            if (r < s.n) {
-                const uint16_t *k = p.key + (s.t0 + r) * p.key_stride + h * D;
-                ka[it] = *reinterpret_cast<const uint2 *>(k + u.a);
-                kb[it] = *reinterpret_cast<const uint2 *>(k + u.b);
-                v[it] = *reinterpret_cast<const uint4 *>(p.value + (s.t0 + r) * p.value_stride + h * D + uv.a);
-            }
+    for (int it = 0; it < H::NIT; ++it) {
+        const int r = it * H::RPI + rsub;
+        ka[it] = kb[it] = va[it] = vb[it] = Raw<W>{};
+        if (mine && r < s.n) {
+            const uint16_t *k = p.key + (s.t0 + r) * p.key_stride + h * D;
+            const uint16_t *v = p.value + (s.t0 + r) * p.value_stride + h * D;
+            ka[it] = load_raw<W>(k + u.a);
+            kb[it] = load_raw<W>(k + u.b);
+            va[it] = load_raw<W>(v + uv.a);
+            vb[it] = load_raw<W>(v + uv.b);
         }
     }
     if (half > 0) fill_table(tab, rope, s.n, [&](int j) { return s.pos + j; });
     __syncthreads();
-    if (!mine) return;
+    if (!block_ok(p, s, blockIdx.y == 0) || !mine) return;
     const int64_t row_stride = static_cast<int64_t>(p.num_heads_kv) * D;
     const int64_t base = static_cast<int64_t>(s.block) * kBlockSize * row_stride + h * D;   // element of row 0
     if constexpr (BLOCK_SCALED) {
         const int64_t at = static_cast<int64_t>(s.block) * p.num_heads_kv + h;
-        H x;
+        float old_k = 0.f, old_v = 0.f;
+        if (first > 0) {
+            old_k = p.key_scales[at];
+            old_v = p.value_scales[at];
+        }
+        // (rotated once for the maximum and once more for the codes: 32 registers
+        // fewer than keeping the rotated rows, which would spill)
+        auto key_row = [&](int it, float (&a)[W], float (&b)[W]) {
+            unpack<W>(ka[it], a);
+            unpack<W>(kb[it], b);
+            if (half == 0) return;
+            Turn<W> turn;   // (a row past the segment: of its last token, zeros all the same)
+            turn.load(u, tab + min(it * H::RPI + rsub, s.n - 1) * rope.rotary_dim, half);
+            turn.apply(u, a, b);
+        };
+        auto value_row = [&](int it, float (&a)[W], float (&b)[W]) {
+            unpack<W>(va[it], a);
+            unpack<W>(vb[it], b);
+        };
+        float mk = 0.f, mv = 0.f;
+        bool nan_k = false, nan_v = false;
 #pragma unroll
         for (int it = 0; it < H::NIT; ++it) {
-            unpack4(ka[it], x.a[it]);
-            unpack4(kb[it], x.b[it]);
-            if (it * H::RPI + rsub < s.n) rotate(u, tab + (it * H::RPI + rsub) * rope.rotary_dim, half, x.a[it], x.b[it]);
+            if (it * H::RPI >= s.n) break;
+            float xa[W], xb[W];
+            key_row(it, xa, xb);
+            track<W>(xa, mk, nan_k);
+            track<W>(xb, mk, nan_k);
+            value_row(it, xa, xb);
+            track<W>(xa, mv, nan_v);
+            track<W>(xb, mv, nan_v);
         }
-        store_scaled<D, KIND == kCacheInt8Block>(x, u, static_cast<uint8_t *>(p.key_cache) + base, row_stride,
-                                                 p.key_scales + at, old_k, first, s.n, lane);
 #pragma unroll
-        for (int it = 0; it < H::NIT; ++it) {
-            unpack4(make_uint2(v[it].x, v[it].y), x.a[it]);
-            unpack4(make_uint2(v[it].z, v[it].w), x.b[it]);
+        for (int o = 16; o > 0; o >>= 1) {
+            mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
+            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
         }
-        store_scaled<D, KIND == kCacheInt8Block>(x, uv, static_cast<uint8_t *>(p.value_cache) + base, row_stride,
-                                                 p.value_scales + at, old_v, first, s.n, lane);
+        if (INT8) {
+            nan_k = __any_sync(0xffffffffu, nan_k);
+            nan_v = __any_sync(0xffffffffu, nan_v);
+        }
+        store_scaled<D, W, INT8>(key_row, mk, nan_k, u, static_cast<uint8_t *>(p.key_cache) + base, row_stride,
+                                 p.key_scales + at, old_k, first, s.n, lane);
+        store_scaled<D, W, INT8>(value_row, mv, nan_v, uv, static_cast<uint8_t *>(p.value_cache) + base, row_stride,
+                                 p.value_scales + at, old_v, first, s.n, lane);
     } else {
 #pragma unroll
         for (int it = 0; it < H::NIT; ++it) {
             const int r = it * H::RPI + rsub;
             if (r >= s.n) continue;
-            float xa[4], xb[4];
-            unpack4(ka[it], xa);
-            unpack4(kb[it], xb);
-            rotate(u, tab + r * rope.rotary_dim, half, xa, xb);
+            float xa[W], xb[W];
+            unpack<W>(ka[it], xa);
+            unpack<W>(kb[it], xb);
+            Turn<W> turn;
+            turn.load(u, tab + r * rope.rotary_dim, half);
+            turn.apply(u, xa, xb);
             const int64_t row = base + (first + r) * row_stride;
             if constexpr (KIND == kCacheBf16) {
-                uint16_t *k = static_cast<uint16_t *>(p.key_cache) + row;
+                uint16_t *k = static_cast<uint16_t *>(p.key_cache) + row, *v = static_cast<uint16_t *>(p.value_cache) + row;
                 if (half > 0) {
-                    ka[it] = make_uint2(pack_bf16x2(xa[0], xa[1]), pack_bf16x2(xa[2], xa[3]));
-                    kb[it] = make_uint2(pack_bf16x2(xb[0], xb[1]), pack_bf16x2(xb[2], xb[3]));
+                    ka[it] = pack<W>(xa);
+                    kb[it] = pack<W>(xb);
                 }   // else a bit copy (a NaN keeps its bits)
-                *reinterpret_cast<uint2 *>(k + u.a) = ka[it];
-                *reinterpret_cast<uint2 *>(k + u.b) = kb[it];
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.value_cache) + row + uv.a) = v[it];
+                store_raw<W>(k + u.a, ka[it]);
+                store_raw<W>(k + u.b, kb[it]);
+                store_raw<W>(v + uv.a, va[it]);
+                store_raw<W>(v + uv.b, vb[it]);
             } else {
                 // codes of x / k_scale, the quotient rounded in 32 bits as pa_write_kv_fp8 does
-                uint8_t *k = static_cast<uint8_t *>(p.key_cache) + row;
-                auto q = [&](float y) { return __fdiv_rn(y, p.k_scale); };
-                *reinterpret_cast<uint32_t *>(k + u.a) = encode4<false>(q(xa[0]), q(xa[1]), q(xa[2]), q(xa[3]));
-                *reinterpret_cast<uint32_t *>(k + u.b) = encode4<false>(q(xb[0]), q(xb[1]), q(xb[2]), q(xb[3]));
-                *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.value_cache) + row + uv.a) =
-                    e4m3_quantize8(v[it], p.v_scale);
+                uint8_t *k = static_cast<uint8_t *>(p.key_cache) + row, *v = static_cast<uint8_t *>(p.value_cache) + row;
+                uint32_t ca[W / 4], cb[W / 4];
+                auto codes = [&](const float (&y)[W], float scale, uint32_t (&c)[W / 4]) {
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i)
+                        c[i] = encode4<false>(__fdiv_rn(y[4 * i], scale), __fdiv_rn(y[4 * i + 1], scale),
+                                              __fdiv_rn(y[4 * i + 2], scale), __fdiv_rn(y[4 * i + 3], scale));
+                };
+                codes(xa, p.k_scale, ca);
+                codes(xb, p.k_scale, cb);
+                store_codes<W>(k + u.a, ca);
+                store_codes<W>(k + u.b, cb);
+                unpack<W>(va[it], xa);
+                unpack<W>(vb[it], xb);
+                codes(xa, p.v_scale, ca);
+                codes(xb, p.v_scale, cb);
+                store_codes<W>(v + uv.a, ca);
+                store_codes<W>(v + uv.b, cb);
             }
         }
     }
 }
 
-template <int D>
+// units of 2 x 8 elements where every group of a row is 16-byte aligned
+bool wide_units(const RopeParams &rope, int head_dim) { return rope.rotary_dim % 16 == 0 && head_dim % 16 == 0; }
+
+template <int D, int W>
 cudaError_t launch_append_d(int kind, const RopeParams &rope, const AppendParams &p, dim3 grid, cudaStream_t stream) {
     switch (kind) {
-        case kCacheBf16: return launch_pdl(append_kernel<D, kCacheBf16>, grid, dim3(kThreads), 0, stream, rope, p);
-        case kCacheE4m3: return launch_pdl(append_kernel<D, kCacheE4m3>, grid, dim3(kThreads), 0, stream, rope, p);
+        case kCacheBf16: return launch_pdl(append_kernel<D, kCacheBf16, W>, grid, dim3(kThreads), 0, stream, rope, p);
+        case kCacheE4m3: return launch_pdl(append_kernel<D, kCacheE4m3, W>, grid, dim3(kThreads), 0, stream, rope, p);
         case kCacheE4m3Block:
-            return launch_pdl(append_kernel<D, kCacheE4m3Block>, grid, dim3(kThreads), 0, stream, rope, p);
+            return launch_pdl(append_kernel<D, kCacheE4m3Block, W>, grid, dim3(kThreads), 0, stream, rope, p);
         case kCacheInt8Block:
-            return launch_pdl(append_kernel<D, kCacheInt8Block>, grid, dim3(kThreads), 0, stream, rope, p);
+            return launch_pdl(append_kernel<D, kCacheInt8Block, W>, grid, dim3(kThreads), 0, stream, rope, p);
     }
     return cudaErrorInvalidValue;
 }
@@ -394,11 +563,20 @@ cudaError_t launch_append_d(int kind, const RopeParams &rope, const AppendParams
 cudaError_t launch_rotary(const RopeParams &rope, const RotaryParams &p0, cudaStream_t stream) {
     RotaryParams p = p0;
     if (p.num_tokens <= 0) return cudaSuccess;
-    p.tokens_per_cta = p.num_tokens > 2048 ? 16 : p.num_tokens > 512 ? 4 : 1;
-    p.heads_per_cta = p.num_heads < 16 ? p.num_heads : 16;
-    const dim3 grid((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta,
+    p.heads_per_cta = p.num_heads < 40 ? p.num_heads : 40;
+    // tokens of a CTA: as many as give its threads up to 10 units each, while
+    // there is a CTA for every SM and a thread for every unit of a row
+    const bool wide = wide_units(rope, p.head_dim);
+    const int upr = p.head_dim / (wide ? 16 : 8);
+    p.log_tokens = 0;
+    while (p.log_tokens < 4 && (p.heads_per_cta * upr << (p.log_tokens + 1)) <= 10 * kThreads &&
+           p.num_tokens >> (p.log_tokens + 1) >= 152 && kThreads >> (p.log_tokens + 1) >= upr)
+        ++p.log_tokens;
+    const dim3 grid((p.num_tokens + (1 << p.log_tokens) - 1) >> p.log_tokens,
                     (p.num_heads + p.heads_per_cta - 1) / p.heads_per_cta);
-    return launch_pdl(rotary_kernel, grid, dim3(kThreads), sizeof(float) * p.tokens_per_cta * rope.rotary_dim, stream, rope, p);
+    const size_t smem = sizeof(float) * (rope.rotary_dim << p.log_tokens);
+    return wide ? launch_pdl(rotary_kernel<8>, grid, dim3(kThreads), smem, stream, rope, p)
+                : launch_pdl(rotary_kernel<4>, grid, dim3(kThreads), smem, stream, rope, p);
 }
 
 cudaError_t launch_append(int head_dim, int kind, const RopeParams &rope, const AppendParams &p0, cudaStream_t stream) {
@@ -407,8 +585,11 @@ cudaError_t launch_append(int head_dim, int kind, const RopeParams &rope, const 
     p.q_heads_per_cta = p.num_heads_q < 16 ? p.num_heads_q : 16;
     const int q_parts = p.q == nullptr ? 0 : (p.num_heads_q + p.q_heads_per_cta - 1) / p.q_heads_per_cta;
     const dim3 grid(p.num_tokens / kBlockSize + 2 * p.num_reqs, (p.num_heads_kv + 7) / 8 + q_parts);
-    if (head_dim == 128) return launch_append_d<128>(kind, rope, p, grid, stream);
-    if (head_dim == 64) return launch_append_d<64>(kind, rope, p, grid, stream);
+    const bool wide = wide_units(rope, head_dim);
+    if (head_dim == 128)
+        return wide ? launch_append_d<128, 8>(kind, rope, p, grid, stream) : launch_append_d<128, 4>(kind, rope, p, grid, stream);
+    if (head_dim == 64)
+        return wide ? launch_append_d<64, 8>(kind, rope, p, grid, stream) : launch_append_d<64, 4>(kind, rope, p, grid, stream);
     return cudaErrorInvalidValue;
 }
 

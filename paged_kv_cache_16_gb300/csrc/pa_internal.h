@@ -271,7 +271,7 @@ struct RotaryParams {
     const int32_t *positions;   // [T]
     int64_t x_stride, out_stride;
     int32_t num_tokens, num_heads, head_dim;
-    int32_t tokens_per_cta, heads_per_cta;
+    int32_t log_tokens, heads_per_cta;   // a CTA's tokens (log2) and heads
 };
 
 // Element types of the cache an append writes.
