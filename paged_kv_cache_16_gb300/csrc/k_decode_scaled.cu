@@ -62,25 +62,43 @@ __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Words of a lane's piece of one value row: D / 8 codes.
+template <int D>
+struct Piece {
+    uint32_t w[D / 32];
+    __device__ __forceinline__ void load(uint32_t vb, uint32_t row, uint32_t g) {
+        if constexpr (D == 128) {
+            const uint4 v = lds_v4(vb + tile_at<D>(row, g));
+            w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+        } else {
+            const uint2 v = lds_v2(vb + tile_at<D>(row, g >> 1) + 8u * (g & 1u));
+            w[0] = v.x; w[1] = v.y;
+        }
+    }
+};
+
 template <int D, int HG, bool INT8>
 struct Consumer {
     using C = ScaledCfg<D, HG>;
+    static constexpr int CH = D / 64;   // 16-byte chunks of a key row per lane of a quad
+    static constexpr float kUnset = -1e30f;
     const ScaledDecodeParams &p;
     uint32_t stage0, scale0, full0, empty0;   // shared memory: stages, scales, barriers
     volatile int *abort_flag;
     int warp, lane, g, t4;
+    int slot = 0;         // next stage of the ring and the parity of its phase
+    uint32_t parity = 0;
 
-    __device__ __forceinline__ uint32_t stage(int s) const { return stage0 + static_cast<uint32_t>(s) * C::STAGE; }
-    // scale of tensor (0 K, 1 V) and this warp's head in stage s
-    __device__ __forceinline__ float scale(int s, int tensor) const {
-        return used_scale(lds_f32(scale0 + 4u * (static_cast<uint32_t>(2 * s + tensor) * HG + warp)));
-    }
-
-    // One item, NT tiles of 8 query rows.  Lane (g, t) holds, of tile n, the
-    // scores of keys g and g + 8 for the rows 8n + 2t and 8n + 2t + 1, and of O
-    // the dims 64h + 32jr + 4g + i in ot[n][4h + i][2jr + {0, 1}] for the two.
+    // One item, NT tiles of 8 query rows.  The contraction runs over a permuted
+    // order of dims: step (h, w) takes, from lane t of a quad, the four dims
+    // 16 (CH t + h) + 4 w .. + 3, so a lane reads its keys' codes (and q) in
+    // 16-byte chunks.  Lane (g, t) holds, of tile n, the scores of keys g and
+    // g + 8 for the rows 8n + 2t and 8n + 2t + 1; of a value row it reads the
+    // dims of its piece, D / 8 from D / 8 g on, and of O the same dims for the
+    // two rows: dim 4j + {0, 1, 2, 3} of the piece of row e in
+    // ot[n][2j][e], ot[n][2j][2 + e], ot[n][2j + 1][e], ot[n][2j + 1][2 + e].
     template <int NT>
-    __device__ __forceinline__ bool run(const DecodeItem &item, int &consumed) const {
+    __device__ __forceinline__ bool run(const DecodeItem &item) {
         const DecodeParams &b = p.base;
         const int G = b.group;
         const int kvh = item.head_group * HG + warp;
@@ -96,11 +114,17 @@ struct Consumer {
             const uint16_t *qg = b.q + (static_cast<int64_t>(item.token + r / G) * b.num_heads_q + kvh * G + r % G) * D;
             float amax = 0.f;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk)
+            for (int h = 0; h < CH; ++h)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    qt[n][kk][e] = r < nrow ? __ldg(reinterpret_cast<const uint32_t *>(qg + kk * 16 + 4 * t4 + 2 * e)) : 0u;
-                    amax = max3(amax, fabsf(bf16_lo(qt[n][kk][e])), fabsf(bf16_hi(qt[n][kk][e])));
+                for (int i = 0; i < 2; ++i) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (r < nrow) v = __ldg(reinterpret_cast<const uint4 *>(qg + 16 * (CH * t4 + h)) + i);
+                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        qt[n][4 * h + 2 * i + k / 2][k & 1] = w[k];
+                        amax = max3(amax, fabsf(bf16_lo(w[k])), fabsf(bf16_hi(w[k])));
+                    }
                 }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
@@ -126,72 +150,79 @@ struct Consumer {
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) ot[n][j][0] = ot[n][j][1] = ot[n][j][2] = ot[n][j][3] = 0.f;
             lt[n][0] = lt[n][1] = 0.f;
-            ref[n][0] = ref[n][1] = -INFINITY;
+            ref[n][0] = ref[n][1] = kUnset;
         }
 
         auto qk = [&](uint32_t kb, float (&s)[NT][4]) {
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
+            for (int h = 0; h < CH; ++h) {
+                const uint4 k0 = lds_v4(kb + tile_at<D>(g, CH * t4 + h)), k1 = lds_v4(kb + tile_at<D>(g + 8, CH * t4 + h));
+                const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t a[4];
-                codes_to_f16<INT8>(lds_u32(kb + tile_at<D>(g, kk) + 4 * t4), a[0], a[2]);
-                codes_to_f16<INT8>(lds_u32(kb + tile_at<D>(g + 8, kk) + 4 * t4), a[1], a[3]);
+                for (int w = 0; w < 4; ++w) {
+                    uint32_t a[4];
+                    codes_to_f16<INT8>(w0[w], a[0], a[2]);
+                    codes_to_f16<INT8>(w1[w], a[1], a[3]);
 #pragma unroll
-                for (int n = 0; n < NT; ++n) mma_f16_16816(s[n], a, qt[n][kk][0], qt[n][kk][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        if (h == 0 && w == 0) mma_f16_16816_first(s[n], a, qt[n][0][0], qt[n][0][1]);
+                        else mma_f16_16816(s[n], a, qt[n][4 * h + w][0], qt[n][4 * h + w][1]);
+                    }
+                }
             }
         };
         // O^T += V^T P^T of one block; codes of rows at or past `valid` (MASKED:
         // they may be anything, also NaN) count as 0
         auto pv = [&](auto masked, uint32_t vb, const uint32_t (&w)[NT][2], int valid) {
-            uint32_t mA = ~0u, mB = ~0u, mC = ~0u, mD = ~0u;
-            if constexpr (decltype(masked)::value) {
-                mA = 2 * t4 < valid ? ~0u : 0u;
-                mB = 2 * t4 + 1 < valid ? ~0u : 0u;
-                mC = 2 * t4 + 8 < valid ? ~0u : 0u;
-                mD = 2 * t4 + 9 < valid ? ~0u : 0u;
+            Piece<D> v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int row = 2 * t4 + (i & 1) + 8 * (i >> 1);
+                v[i].load(vb, row, g);
+                if constexpr (decltype(masked)::value) {
+#pragma unroll
+                    for (int j = 0; j < D / 32; ++j) v[i].w[j] = row < valid ? v[i].w[j] : 0u;
+                }
             }
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h) {
-                uint32_t a[4][4];
+            for (int j = 0; j < D / 32; ++j) {
+                uint32_t a0[4], a1[4];
+                codes_to_f16<INT8>(prmt(v[0].w[j], v[1].w[j], 0x5140u), a0[0], a0[1]);
+                codes_to_f16<INT8>(prmt(v[2].w[j], v[3].w[j], 0x5140u), a0[2], a0[3]);
+                codes_to_f16<INT8>(prmt(v[0].w[j], v[1].w[j], 0x7362u), a1[0], a1[1]);
+                codes_to_f16<INT8>(prmt(v[2].w[j], v[3].w[j], 0x7362u), a1[2], a1[3]);
 #pragma unroll
-                for (int jr = 0; jr < 2; ++jr) {
-                    const uint32_t chunk = 4u * h + 2u * jr + static_cast<uint32_t>(g >> 2);
-                    const uint32_t in = vb + 4u * (g & 3);
-                    uint32_t wA = lds_u32(in + tile_at<D>(2 * t4, chunk)), wB = lds_u32(in + tile_at<D>(2 * t4 + 1, chunk));
-                    uint32_t wC = lds_u32(in + tile_at<D>(2 * t4 + 8, chunk)), wD = lds_u32(in + tile_at<D>(2 * t4 + 9, chunk));
-                    if constexpr (decltype(masked)::value) {
-                        wA &= mA; wB &= mB; wC &= mC; wD &= mD;
-                    }
-                    codes_to_f16<INT8>(prmt(wA, wB, 0x5140u), a[0][jr], a[1][jr]);
-                    codes_to_f16<INT8>(prmt(wA, wB, 0x7362u), a[2][jr], a[3][jr]);
-                    codes_to_f16<INT8>(prmt(wC, wD, 0x5140u), a[0][2 + jr], a[1][2 + jr]);
-                    codes_to_f16<INT8>(prmt(wC, wD, 0x7362u), a[2][2 + jr], a[3][2 + jr]);
+                for (int n = 0; n < NT; ++n) {
+                    mma_f16_16816(ot[n][2 * j], a0, w[n][0], w[n][1]);
+                    mma_f16_16816(ot[n][2 * j + 1], a1, w[n][0], w[n][1]);
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) mma_f16_16816(ot[n][4 * h + i], a[i], w[n][0], w[n][1]);
             }
         };
         // one softmax round over one (TWO = false) or two blocks
         auto round = [&](auto two_c, int pg) -> bool {
             constexpr int NB = decltype(two_c)::value ? 2 : 1;
-            int st[NB];
-            float sc[NB][NT][4], kf[NB], lv[NB], iv[NB];
+            uint32_t st[NB], fin[NB];
+            float sc[NB][NT][4], kf[NB][NT][2], lv[NB], iv[NB];
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
-                st[k] = (consumed + k) % C::NS;
-                if (!warp_wait(full0 + 8u * st[k], ((consumed + k) / C::NS) & 1, abort_flag)) return false;
-            }
-#pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                qk(stage(st[k]) + warp * C::BOX, sc[k]);
-                kf[k] = scale(st[k], 0);
-                const float vs = scale(st[k], 1);
+                if (!warp_wait(full0 + 8u * slot, parity, abort_flag)) return false;
+                st[k] = stage0 + static_cast<uint32_t>(slot) * C::STAGE + warp * C::BOX;
+                fin[k] = empty0 + 8u * slot;
+                const uint32_t sa = scale0 + 4u * (2 * HG * slot + warp);
+                const float ks = used_scale(lds_f32(sa)), vs = used_scale(lds_f32(sa + 4u * HG));
                 lv[k] = lg2(vs);
                 iv[k] = __fdividef(1.f, vs);
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) kf[k][n][e] = ks * rf[n][e];
+                if (++slot == C::NS) {
+                    slot = 0;
+                    parity ^= 1u;
+                }
             }
+#pragma unroll
+            for (int k = 0; k < NB; ++k) qk(st[k], sc[k]);
             const int key0 = pg * kBlockSize;
             const int valid = item.key_end - key0;   // V rows past it may be anything
             if (lim_lo - key0 < NB * kBlockSize) {
@@ -209,15 +240,20 @@ struct Consumer {
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float m = -INFINITY;
-#pragma unroll
-                    for (int k = 0; k < NB; ++k)
-                        m = fmaxf(m, fmaf(fmaxf(sc[k][n][e], sc[k][n][e + 2]), kf[k] * rf[n][e], lv[k]));
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                    float m = fmaf(fmaxf(sc[0][n][e], sc[0][n][e + 2]), kf[0][n][e], lv[0]);
+                    if constexpr (NB == 2) m = fmaxf(m, fmaf(fmaxf(sc[1][n][e], sc[1][n][e + 2]), kf[1][n][e], lv[1]));
                     mx[n][e] = m;
-                    grow |= m > ref[n][e] + 8.f;
                 }
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) mx[n][e] = fmaxf(mx[n][e], __shfl_xor_sync(0xffffffffu, mx[n][e], o));
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) grow |= mx[n][e] > ref[n][e] + 8.f;
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -235,34 +271,34 @@ struct Consumer {
                     }
                 }
             }
+            uint32_t w[NB][NT][2];
 #pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                uint32_t w[NT][2];
+            for (int k = 0; k < NB; ++k)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float x[4];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float f = kf[k] * rf[n][e], c = lv[k] - (ref[n][e] == -INFINITY ? 0.f : ref[n][e]);
-                        x[e] = ex2(fmaf(sc[k][n][e], f, c));
-                        x[e + 2] = ex2(fmaf(sc[k][n][e + 2], f, c));
+                        const float c = lv[k] - ref[n][e];
+                        x[e] = ex2(fmaf(sc[k][n][e], kf[k][n][e], c));
+                        x[e + 2] = ex2(fmaf(sc[k][n][e + 2], kf[k][n][e], c));
                         lt[n][e] = fmaf(x[e] + x[e + 2], iv[k], lt[n][e]);
                     }
                     // P^T as B fragments: rows (8n + 2t, 8n + 2t + 1) of key g
                     // (g + 8), transposed 8x8
-                    w[n][0] = movmatrix_trans(pack_f16x2(x[0], x[1]));
-                    w[n][1] = movmatrix_trans(pack_f16x2(x[2], x[3]));
+                    w[k][n][0] = movmatrix_trans(pack_f16x2(x[0], x[1]));
+                    w[k][n][1] = movmatrix_trans(pack_f16x2(x[2], x[3]));
                 }
-                const uint32_t vb = stage(st[k]) + C::TSTAGE + warp * C::BOX;
-                if (valid < (k + 1) * kBlockSize) pv(std::true_type{}, vb, w, valid - k * kBlockSize);
-                else pv(std::false_type{}, vb, w, kBlockSize);
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                if (valid < (k + 1) * kBlockSize) pv(std::true_type{}, st[k] + C::TSTAGE, w[k], valid - k * kBlockSize);
+                else pv(std::false_type{}, st[k] + C::TSTAGE, w[k], kBlockSize);
             }
             __syncwarp();
             if (lane == 0) {
 #pragma unroll
-                for (int k = 0; k < NB; ++k) mbar_arrive(empty0 + 8u * st[k]);
+                for (int k = 0; k < NB; ++k) mbar_arrive(fin[k]);
             }
-            consumed += NB;
             return true;
         };
         int pg = item.page_begin;
@@ -283,30 +319,28 @@ struct Consumer {
                 // a NaN stays one; no visible key: 0
                 const float inv = l == 0.f ? 0.f : 1.f / l;
                 const int tok = item.token + r / G, head = kvh * G + r % G;
+                auto o4 = [&](int j) {   // dims 4j .. 4j + 3 of the piece
+                    return make_float4(ot[n][2 * j][e] * inv, ot[n][2 * j][2 + e] * inv, ot[n][2 * j + 1][e] * inv,
+                                       ot[n][2 * j + 1][2 + e] * inv);
+                };
                 if (item.part < 0) {
-                    uint16_t *o = b.out + (static_cast<int64_t>(tok) * b.num_heads_q + head) * D + 4 * g;
+                    uint16_t *o = b.out + (static_cast<int64_t>(tok) * b.num_heads_q + head) * D + D / 8 * g;
 #pragma unroll
-                    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-                        for (int jr = 0; jr < 2; ++jr)
-                            *reinterpret_cast<uint2 *>(o + 64 * h + 32 * jr) =
-                                make_uint2(pack_bf16x2(ot[n][4 * h][2 * jr + e] * inv, ot[n][4 * h + 1][2 * jr + e] * inv),
-                                           pack_bf16x2(ot[n][4 * h + 2][2 * jr + e] * inv, ot[n][4 * h + 3][2 * jr + e] * inv));
+                    for (int j = 0; j < D / 32; j += 2) {
+                        const float4 x = o4(j), y = o4(j + 1);
+                        *reinterpret_cast<uint4 *>(o + 4 * j) = make_uint4(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w),
+                                                                           pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+                    }
                 } else {
-                    const int64_t slot = static_cast<int64_t>(b.part_offset[tok * b.n_groups + item.head_group]) + item.part;
-                    float *o = b.o_part + (slot * b.num_heads_q + head) * D + 4 * g;
+                    const int64_t slot_at = static_cast<int64_t>(b.part_offset[tok * b.n_groups + item.head_group]) + item.part;
+                    float *o = b.o_part + (slot_at * b.num_heads_q + head) * D + D / 8 * g;
 #pragma unroll
-                    for (int h = 0; h < D / 64; ++h)
-#pragma unroll
-                        for (int jr = 0; jr < 2; ++jr)
-                            *reinterpret_cast<float4 *>(o + 64 * h + 32 * jr) =
-                                make_float4(ot[n][4 * h][2 * jr + e] * inv, ot[n][4 * h + 1][2 * jr + e] * inv,
-                                            ot[n][4 * h + 2][2 * jr + e] * inv, ot[n][4 * h + 3][2 * jr + e] * inv);
+                    for (int j = 0; j < D / 32; ++j) *reinterpret_cast<float4 *>(o + 4 * j) = o4(j);
                     // the partial's weight in the merge is 2^m l: kept as l = 1, so
                     // that L's own range (1 / vs) does not enter there; a NaN
                     // takes the merge over
                     if (g == 0)
-                        b.ml_part[slot * b.num_heads_q + head] =
+                        b.ml_part[slot_at * b.num_heads_q + head] =
                             l == 0.f ? make_float2(-INFINITY, 0.f)
                                      : make_float2(l != l ? 3.0e38f : ref[n][e] + lg2(l), 1.f);
                 }
@@ -407,12 +441,11 @@ scaled_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
     } else {
         // ----------------------------------------------------- consumers --
-        const Consumer<D, HG, INT8> c{sp, base, scale0, bar0, bar0 + 8u * C::NS, &abort_flag, warp, lane, lane >> 2, lane & 3};
-        int consumed = 0;
+        Consumer<D, HG, INT8> c{sp, base, scale0, bar0, bar0 + 8u * C::NS, &abort_flag, warp, lane, lane >> 2, lane & 3};
         bool ok = true;
         for (int it = item_begin; it < item_end && ok; ++it) {
             const DecodeItem item = p.items[it];
-            ok = item.n_tok * p.group <= 8 ? c.template run<1>(item, consumed) : c.template run<2>(item, consumed);
+            ok = item.n_tok * p.group <= 8 ? c.template run<1>(item) : c.template run<2>(item);
             if (!ok && lane == 0) raise_abort(&abort_flag, p.err, kErrTimeout);
         }
     }
