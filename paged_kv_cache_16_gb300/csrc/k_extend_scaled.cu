@@ -7,12 +7,22 @@
 // in fp32, per block of 16 key columns, as in the split-KV kernel:
 //   w = 2^(s + log2 vs - R), s = softmax_scale log2(e) ks <q, kcode>,
 //   O += w vcode,  L += (sum of the block's w) / vs,  out = O / L,
-// so a tile loses nothing to the quantisation's form: the weights have f16's 11
-// bits (bf16 weights and dequantised bf16 K and V cost 2.6 times the error of the
-// output's own rounding; this adds 0.1 of it).  Three factors per (block, kv
-// head), written by the expansion kernel as one 16-byte record, travel with the V
-// stage: a softmax warp may wait for that stage, which is not given back before
-// its weights have been used.
+// so a tile loses nothing to the quantisation's form (bf16 weights and dequantised
+// bf16 K and V gave 2.6 times the error of the output's own rounding; this adds
+// nothing visible).  Three factors per (block, kv head), written by the expansion
+// kernel as one 16-byte record, travel with the V stage: a softmax warp may wait
+// for that stage, which is not given back before its weights have been used.
+//
+// Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 254 us at
+// 2070 MHz, 1353 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
+// 260 (its 8 boxes per key tile against one here).  A step of 128 keys takes ~3700
+// cycles for 2048 of MMAs: with the softmax arithmetic taken out 205 us, what the
+// MMA thread's commits and waits leave of the pipe; the rest is the chain S ->
+// softmax -> P of a sub-tile.  Measured and not kept (us): weights through
+// shared memory, QK^T a step ahead, 312 (every operand from shared memory fills
+// its bandwidth); one S buffer for both sub-tiles and QK^T a step ahead, 353 with
+// one MMA thread, 283 with one for QK^T and one for PV; an MMA thread per sub-tile,
+// 317, taking turns at the pipe 260; and with two threads per row 293.
 #include "dev.cuh"
 
 namespace pa {

@@ -118,8 +118,7 @@ __device__ __forceinline__ void expand16_codes(const uint4 codes, bool value, ui
             o[2 * i + 1] = dev::pack_bf16x2(dev::f16_lo(o[2 * i + 1]), dev::f16_hi(o[2 * i + 1]));
         }
     }
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    dev::st_global_v8(dst, o[0], o[1], o[2], o[3], o[4], o[5], o[6], o[7]);   // a whole sector per lane
 }
 
 template <bool INT8>
@@ -143,27 +142,13 @@ __global__ void expand_scaled_kernel(DequantParams p) {
         }
         const uint4 *ks = reinterpret_cast<const uint4 *>(p.key_cache + static_cast<int64_t>(src) * p.block_elems);
         const uint4 *vs = reinterpret_cast<const uint4 *>(p.value_cache + static_cast<int64_t>(src) * p.block_elems);
-        // a thread's chunks of the block are all loaded before any is
-        // stored: one round trip to memory instead of one per chunk
-        constexpr int U = 4;
-        for (int32_t c0 = threadIdx.x; c0 < chunks; c0 += U * blockDim.x) {
-            uint4 kx[U], vx[U];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int32_t c = c0 + u * static_cast<int32_t>(blockDim.x);
-                if (c < chunks) {
-                    kx[u] = __ldg(ks + c);
-                    vx[u] = __ldg(vs + c);
-                }
-            }
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int32_t c = c0 + u * static_cast<int32_t>(blockDim.x);
-                if (c < chunks) {
-                    expand16_codes<INT8>(kx[u], false, kd + 2 * c);
-                    expand16_codes<INT8>(vx[u], true, vd + 2 * c);
-                }
-            }
+        // bound by the writes.  One chunk of each a time: two or four in flight, as
+        // dequant_kernel has them, took 3 and 4 us more for 704 blocks (the grid
+        // covers every block at once), 16-byte stores another 6
+        for (int32_t c = threadIdx.x; c < chunks; c += blockDim.x) {
+            const uint4 kx = __ldg(ks + c), vx = __ldg(vs + c);
+            expand16_codes<INT8>(kx, false, kd + 2 * c);
+            expand16_codes<INT8>(vx, true, vd + 2 * c);
         }
         for (int32_t h = threadIdx.x; h < p.num_heads_kv; h += blockDim.x) {
             const float kf = dev::used_scale(__ldg(p.key_scales + static_cast<int64_t>(src) * p.num_heads_kv + h));
