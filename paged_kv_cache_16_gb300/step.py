@@ -11,11 +11,31 @@ from . import binding
 from .workloads import Batch
 
 
-class DeviceStep:
-    """Device-resident metadata, plan, workspace and output of one batch."""
+KV_DTYPES = {"bf16": binding.PA_KV_BF16, "fp8": binding.PA_KV_FP8_E4M3, "fp8_block": binding.PA_KV_FP8_E4M3_BLOCK,
+             "int8_block": binding.PA_KV_INT8_BLOCK}
 
-    def __init__(self, batch: Batch, device="cuda", num_sms: int = 0, plan: bool = True):
+
+def _append(rope, step, k_scale, v_scale, q, key, value, key_cache, value_cache, key_scales, value_scales, stream):
+    """pa_append_kv with a step's metadata: the cache write with the rotation (if
+    any) on the way; returns the queries to attend with."""
+    rotated = {} if rope is None else dict(q=q, q_out=step.q_rot[:q.shape[0]])
+    binding.pa_append_kv(rope, key, value, step.qsl, step.num_computed, step.block_table, key_cache, value_cache,
+                         key_scales=key_scales, value_scales=value_scales, k_scale=k_scale, v_scale=v_scale,
+                         device_error_word=step.error_word, stream=stream, **rotated)
+    return q if rope is None else step.q_rot[:q.shape[0]]
+
+
+class DeviceStep:
+    """Device-resident metadata, plan, workspace and output of one batch.
+
+    ``rope`` (binding.pa_rope_create): run_append rotates queries and keys by
+    their positions on the way into the cache.  Block-scaled caches
+    ("fp8_block", "int8_block") go through run_append / append and attend, with
+    their scales."""
+
+    def __init__(self, batch: Batch, device="cuda", num_sms: int = 0, plan: bool = True, rope=None):
         self.batch = batch
+        self.rope = rope
         dev = torch.device(device)
         self.device = dev
         self.qsl = torch.as_tensor(batch.query_start_loc, device=dev)
@@ -25,6 +45,7 @@ class DeviceStep:
         T = batch.num_tokens
         self.slots = torch.empty(max(T, 1), dtype=torch.int64, device=dev)
         self.out = torch.empty(max(T, 1), batch.num_heads_q, batch.head_dim, dtype=torch.bfloat16, device=dev)
+        self.q_rot = torch.empty_like(self.out) if rope is not None else None
         self.num_sms = num_sms
         self.plan = self.make_plan() if plan else None
         ws = self.plan.workspace_bytes if self.plan else 256
@@ -39,8 +60,7 @@ class DeviceStep:
                                num_common_prefix_blocks=b.num_common_prefix_blocks,
                                softmax_scale=b.softmax_scale, num_sms=self.num_sms,
                                block_size=b.block_size,
-                               kv_cache_dtype=binding.PA_KV_FP8_E4M3 if b.kv_cache_dtype == "fp8" else binding.PA_KV_BF16,
-                               k_scale=b.k_scale, v_scale=b.v_scale)
+                               kv_cache_dtype=KV_DTYPES[b.kv_cache_dtype], k_scale=b.k_scale, v_scale=b.v_scale)
 
     @property
     def error_word(self) -> torch.Tensor:
@@ -59,10 +79,25 @@ class DeviceStep:
         else:
             binding.pa_write_kv(key, value, self.slots, key_cache, value_cache, self.error_word, stream)
 
-    def attend(self, q, key_cache, value_cache, stream=None, plan=None):
-        binding.pa_attention(plan or self.plan, q, key_cache, value_cache, self.block_table, self.out,
-                             self.workspace, stream)
+    def attend(self, q, key_cache, value_cache, stream=None, plan=None, key_scales=None, value_scales=None):
+        if key_scales is None:
+            binding.pa_attention(plan or self.plan, q, key_cache, value_cache, self.block_table, self.out,
+                                 self.workspace, stream)
+        else:
+            binding.pa_attention_scaled(plan or self.plan, q, key_cache, value_cache, key_scales, value_scales,
+                                        self.block_table, self.out, self.workspace, stream)
         return self.out[:self.batch.num_tokens]
+
+    def append(self, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None, stream=None):
+        """Cache write of the new rows into any cache type, keys rotated if the
+        step has a rope; returns the (then rotated) queries."""
+        return _append(self.rope, self, self.batch.k_scale, self.batch.v_scale, q, key, value, key_cache, value_cache,
+                       key_scales, value_scales, stream)
+
+    def run_append(self, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None, stream=None):
+        """append -> attention; returns out [T, Hq, D]."""
+        q = self.append(q, key, value, key_cache, value_cache, key_scales, value_scales, stream)
+        return self.attend(q, key_cache, value_cache, stream, None, key_scales, value_scales)
 
     def run(self, q, key, value, key_cache, value_cache, stream=None):
         """slot mapping -> cache write -> attention; returns out [T, Hq, D]."""
@@ -157,20 +192,24 @@ class GraphStep:
     also brings the step's inputs in from a page-locked input image (one copy:
     q, key, value and the request metadata share one layout) and copies the
     output back to page-locked memory, so a replay goes from host memory to
-    host memory.
+    host memory.  With a ``rope``, and for block-scaled caches (whose scales
+    capture and run take), the graphs hold pa_append_kv and the attention
+    launch instead.
     """
 
     def __init__(self, *, num_heads_q, num_heads_kv, head_dim, num_blocks, max_blocks_per_req, softmax_scale,
                  max_tokens, max_reqs, max_extend_tiles=0, max_dequant_blocks=0, max_partial_slots=0,
                  kv_cache_dtype="bf16", k_scale=1.0, v_scale=1.0, num_sms=0, device="cuda", fused=True,
-                 host_io=False):
+                 host_io=False, rope=None):
         dev = torch.device(device)
         self.device = dev
         self.fused = fused
+        self.rope = rope
+        self.scaled = kv_cache_dtype in ("fp8_block", "int8_block")
         self.model = dict(num_heads_q=num_heads_q, num_heads_kv=num_heads_kv, head_dim=head_dim,
                           num_blocks=num_blocks, max_blocks_per_req=max_blocks_per_req,
                           softmax_scale=softmax_scale, num_sms=num_sms,
-                          kv_cache_dtype=binding.PA_KV_FP8_E4M3 if kv_cache_dtype == "fp8" else binding.PA_KV_BF16,
+                          kv_cache_dtype=KV_DTYPES[kv_cache_dtype],
                           k_scale=k_scale, v_scale=v_scale)
         self.shape = dict(max_tokens=max_tokens, max_reqs=max_reqs, max_extend_tiles=max_extend_tiles,
                           max_dequant_blocks=max_dequant_blocks, max_partial_slots=max_partial_slots)
@@ -186,6 +225,7 @@ class GraphStep:
         self.q, self.key, self.value = views["q"], views["key"], views["value"]
         self.qsl, self.num_computed, self.block_table = views["qsl"], views["num_computed"], views["block_table"]
         self.out = torch.zeros_like(self.q)
+        self.q_rot = torch.zeros_like(self.q) if rope is not None else None
         self.slots = torch.zeros(max_tokens, dtype=torch.int64, device=dev)
         # host_io: each graph also copies a page-locked input image (the
         # layout above) to the device first and the output back last, so a
@@ -247,10 +287,21 @@ class GraphStep:
         self.done[i].synchronize()
         return self.host_out[i][:num_tokens]
 
-    def enqueue(self, plan: binding.Plan, key_cache, value_cache, stream=None):
+    def enqueue(self, plan: binding.Plan, key_cache, value_cache, stream=None, key_scales=None, value_scales=None):
         """Slot mapping, cache write and attention over the static buffers
         (every launch sized by the capacities; capturable).  Fused: one
-        pa_attention_with_kv_update_launch does all three."""
+        pa_attention_with_kv_update_launch does all three.  With a rope or block
+        scales: the append, then attention."""
+        if self.rope is not None or self.scaled:
+            q = _append(self.rope, self, self.k_scale, self.v_scale, self.q, self.key, self.value, key_cache, value_cache,
+                        key_scales, value_scales, stream)
+            if self.scaled:
+                binding.pa_attention_scaled_launch(plan, q, key_cache, value_cache, key_scales, value_scales,
+                                                   self.block_table, self.out, self.workspace, stream)
+            else:
+                binding.pa_attention_launch(plan, q, key_cache, value_cache, self.block_table, self.out,
+                                            self.workspace, stream)
+            return
         if self.fused:
             binding.pa_attention_with_kv_update_launch(plan, self.q, self.key, self.value, key_cache, value_cache,
                                                        self.block_table, self.out, self.workspace, self.slots, stream)
@@ -265,9 +316,9 @@ class GraphStep:
         binding.pa_attention_launch(plan, self.q, key_cache, value_cache, self.block_table, self.out,
                                     self.workspace, stream)
 
-    def capture(self, plan: binding.Plan, key_cache, value_cache):
+    def capture(self, plan: binding.Plan, key_cache, value_cache, key_scales=None, value_scales=None):
         """Capture the upload of each metadata image followed by enqueue();
-        the caches are part of the graphs."""
+        the caches (and scales) are part of the graphs."""
         if self.workspace is None:
             self.workspace = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device=self.device)
         binding.pa_upload_metadata(plan, self.workspace)   # prepares the kernels (not capturable)
@@ -282,13 +333,17 @@ class GraphStep:
                 if self.host_in is not None:
                     self._in.copy_(self.host_in[len(self.graphs)], non_blocking=True)
                 binding.pa_upload_metadata_from(img, nbytes, self.workspace)
-                self.enqueue(plan, key_cache, value_cache)
+                self.enqueue(plan, key_cache, value_cache, None, key_scales, value_scales)
                 if self.host_out is not None:
                     self.host_out[len(self.graphs)].copy_(self.out, non_blocking=True)
             self.graphs.append(g)
         self.done = [torch.cuda.Event(), torch.cuda.Event()]
         self.turn = 0
-        self.caches = (key_cache.data_ptr(), value_cache.data_ptr())
+        self.caches = self._addresses(key_cache, value_cache, key_scales, value_scales)
+
+    @staticmethod
+    def _addresses(*tensors):
+        return tuple(None if t is None else t.data_ptr() for t in tensors)
 
     def prepare_replay(self, plan: binding.Plan):
         """Write the plan's metadata image for the next replay (host work)."""
@@ -308,13 +363,13 @@ class GraphStep:
         self.prepare_replay(plan)
         self.launch_replay()
 
-    def run(self, batch: Batch, q, key, value, key_cache, value_cache) -> torch.Tensor:
+    def run(self, batch: Batch, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None) -> torch.Tensor:
         """One step: plan, copy in, replay (capturing on first use)."""
         plan = self.make_plan(batch)
         self.stage(batch, q, key, value)
         if self.graphs is None:
-            self.capture(plan, key_cache, value_cache)
-        elif self.caches != (key_cache.data_ptr(), value_cache.data_ptr()):
+            self.capture(plan, key_cache, value_cache, key_scales, value_scales)
+        elif self.caches != self._addresses(key_cache, value_cache, key_scales, value_scales):
             raise ValueError("a captured step replays on the caches it was captured with")
         self.replay(plan)
         return self.out[:batch.num_tokens]
@@ -378,8 +433,7 @@ class NativeGraphStep:
                        decode_prefix_tokens=decode_prefix_tokens),
             host=host, buffers=bufs, num_reqs=0, fused=fused, num_heads_q=num_heads_q, num_heads_kv=num_heads_kv,
             head_dim=head_dim, num_blocks=num_blocks, softmax_scale=softmax_scale, num_sms=num_sms,
-            kv_cache_dtype=binding.PA_KV_FP8_E4M3 if kv_cache_dtype == "fp8" else binding.PA_KV_BF16,
-            k_scale=k_scale, v_scale=v_scale)
+            kv_cache_dtype=KV_DTYPES[kv_cache_dtype], k_scale=k_scale, v_scale=v_scale)
         self._last = None   # graph index of the last step launched
         self._keep = (key_cache, value_cache)
 

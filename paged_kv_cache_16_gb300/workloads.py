@@ -20,6 +20,9 @@ Recipe (all seeded):
   * FP8 (E4M3) caches: the same N(0, 1) pool divided by the tensor's scale and
     cast with torch's float8_e4m3fn conversion (clamped to +-448), so the codes
     spread over the format's range; poison is the code 0x7E (448) or 0x7F (NaN).
+  * block-scaled caches ("fp8_block", "int8_block"): the same pool divided by a
+    power of two drawn per (block, kv head) and cast; poison as for FP8, or the
+    code 127, and a NaN scale of the padding block.
 """
 from __future__ import annotations
 
@@ -54,9 +57,12 @@ class Batch:
     value_cache: torch.Tensor        # bf16 [num_blocks, block_size, Hkv, D]
     poison_block: int
     meta: dict = field(default_factory=dict)
-    kv_cache_dtype: str = "bf16"     # "bf16" or "fp8" (E4M3 codes, uint8 caches)
+    kv_cache_dtype: str = "bf16"     # "bf16", "fp8" (E4M3 codes, uint8 caches), "fp8_block" or
+                                     # "int8_block" (uint8 / int8 codes with block scales)
     k_scale: float = 1.0
     v_scale: float = 1.0
+    key_scales: torch.Tensor | None = None     # block-scaled: float32 [num_blocks, Hkv]
+    value_scales: torch.Tensor | None = None
 
     @property
     def num_reqs(self) -> int:
@@ -116,6 +122,28 @@ def _to_e4m3(pool: torch.Tensor, scale: float) -> torch.Tensor:
         x = flat_in[start:start + chunk].float() / scale
         flat_out[start:start + chunk] = x.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
     return out
+
+
+def _poison_int8(n: int, kind: str, device) -> torch.Tensor:
+    """int8 poison: the largest code, alternating sign (int8 has no NaN)."""
+    codes = torch.full((n,), 127, dtype=torch.int8, device=device)
+    codes[1::2] = -127
+    return codes
+
+
+def _to_block_codes(pool: torch.Tensor, kind: str, gen: torch.Generator):
+    """bf16 pool -> (codes, scales): codes of pool / 2^e, e drawn per (block,
+    head) so that N(0, 1) values fill most of the codes' range."""
+    nb, _, hkv, _ = pool.shape
+    low, high = (-6, -4) if kind == "int8_block" else (-8, -5)
+    scales = torch.exp2(torch.randint(low, high + 1, (nb, hkv), generator=gen, device=pool.device).float())
+    out = torch.empty(pool.shape, dtype=torch.int8 if kind == "int8_block" else torch.uint8, device=pool.device)
+    chunk = max(1, (1 << 26) // int(np.prod(pool.shape[1:])))
+    for b in range(0, nb, chunk):
+        x = pool[b:b + chunk].float() / scales[b:b + chunk, None, :, None]
+        out[b:b + chunk] = x.round().clamp(-127, 127).to(torch.int8) if kind == "int8_block" else \
+            x.clamp(-448.0, 448.0).to(torch.float8_e4m3fn).view(torch.uint8)
+    return out, scales
 
 
 def _poison_values(n: int, kind: str, device) -> torch.Tensor:
@@ -191,9 +219,13 @@ def make_batch(*, name: str, num_heads_q: int, num_heads_kv: int, head_dim: int,
     vc = _randn_bf16((num_blocks, block_size, num_heads_kv, head_dim), gen_pool, pdev)
 
     fp8 = kv_cache_dtype == "fp8"
+    key_scales = value_scales = None
     if fp8:
         kc, vc = _to_e4m3(kc, k_scale), _to_e4m3(vc, v_scale)
-    poison_fn = _poison_codes if fp8 else _poison_values
+    elif kv_cache_dtype != "bf16":
+        (kc, key_scales), (vc, value_scales) = (_to_block_codes(c, kv_cache_dtype, gen_pool) for c in (kc, vc))
+        key_scales[poison_block] = value_scales[poison_block] = float("nan")
+    poison_fn = {"bf16": _poison_values, "int8_block": _poison_int8}.get(kv_cache_dtype, _poison_codes)
 
     # Poison: (a) the padding block, (b) every slot at or past num_computed in
     # a request's own (unshared) blocks -- the new tokens' destinations and
@@ -223,7 +255,8 @@ def make_batch(*, name: str, num_heads_q: int, num_heads_kv: int, head_dim: int,
                  softmax_scale=1.0 / math.sqrt(head_dim), q=q, key=key, value=value,
                  key_cache=kc, value_cache=vc, poison_block=poison_block,
                  meta={"seed": seed, "poison": poison}, kv_cache_dtype=kv_cache_dtype,
-                 k_scale=float(k_scale) if fp8 else 1.0, v_scale=float(v_scale) if fp8 else 1.0)
+                 k_scale=float(k_scale) if fp8 else 1.0, v_scale=float(v_scale) if fp8 else 1.0,
+                 key_scales=key_scales, value_scales=value_scales)
 
 
 # ---------------------------------------------------------------------------

@@ -6,7 +6,8 @@ import torch
 
 import operators_common as oc
 from gpu_common import ensure_library
-from paged_kv_cache_16_gb300 import binding
+from paged_kv_cache_16_gb300 import binding, workloads
+from paged_kv_cache_16_gb300.step import DeviceStep, GraphStep
 
 pytestmark = pytest.mark.gpu
 DEV = torch.device("cuda")
@@ -295,3 +296,71 @@ def test_steps_of_append_and_attention(code):
         c.q, c.kc, c.vc, c.ks, c.vs = (t.cpu() for t in (q_rot, kc, vc, ks, vs))
         ref, tol = c.reference()
         oc.assert_within(out, ref, tol, f"step {step}")
+
+
+def batch_case(b, q, kc, vc, ks, vs):
+    """An oc.Case over a workloads batch and the device state after its append."""
+    c = oc.Case.__new__(oc.Case)
+    c.hq, c.hkv, c.d, c.code, c.n_common = b.num_heads_q, b.num_heads_kv, b.head_dim, \
+        "int8" if b.kv_cache_dtype == "int8_block" else "e4m3", b.num_common_prefix_blocks
+    c.q_lens, c.seq, c.table, c.nb, c.T = b.q_lens, b.seq_lens, b.block_table, b.num_blocks, b.num_tokens
+    c.qsl, c.scale = b.query_start_loc, b.softmax_scale
+    c.q, c.kc, c.vc, c.ks, c.vs = (t.cpu() for t in (q, kc, vc, ks, vs))
+    return c
+
+
+@pytest.mark.parametrize("kind", ["int8_block", "fp8_block"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_device_step_run_append(kind, d):
+    """DeviceStep.run_append with a rope over block-scaled caches: a mixed step
+    against 64-bit attention over the cache it leaves; without a rope the queries
+    are the caller's."""
+    b = workloads.make_batch(name="scaled", num_heads_q=8, num_heads_kv=2, head_dim=d, q_lens=[1, 1, 40, 3, 1],
+                             seq_lens=[90, 33, 100, 20, 1], num_blocks=40, seed=d, kv_cache_dtype=kind)
+    for rope in (binding.pa_rope_create(rotary_dim=d), None):
+        q, k, v, kc, vc, ks, vs = (t.to(DEV) for t in (b.q, b.key, b.value, b.key_cache, b.value_cache, b.key_scales,
+                                                       b.value_scales))
+        st = DeviceStep(b, "cuda", rope=rope)
+        out = st.run_append(q, k, v, kc, vc, ks, vs)
+        torch.cuda.synchronize()
+        assert st.check_errors() == 0
+        used = q if rope is None else st.q_rot
+        if rope is not None:
+            pos = np.concatenate([np.arange(n, n + m) for n, m in zip(b.num_computed, b.q_lens)])
+            want = torch.empty_like(q)
+            binding.pa_rotary(rope, q, torch.as_tensor(pos, dtype=torch.int32, device=DEV), want)
+            assert torch.equal(st.q_rot, want)
+        ref, tol = batch_case(b, used, kc, vc, ks, vs).reference()
+        oc.assert_within(out, ref, tol)
+
+
+@pytest.mark.parametrize("kind", ["int8_block", "bf16", "fp8"])
+def test_graph_step_with_rope(kind):
+    """GraphStep with a rope replays steps of changing size, bit-equal to
+    DeviceStep.run_append: caches, scales and outputs."""
+    rope = binding.pa_rope_create(rotary_dim=64, layout=binding.PA_ROPE_INTERLEAVED)
+    mk = lambda ql, sl, seed: workloads.make_batch(name="g", num_heads_q=8, num_heads_kv=2, head_dim=128, q_lens=ql,  # noqa: E731
+                                                   seq_lens=sl, num_blocks=60, seed=seed, kv_cache_dtype=kind)
+    steps = [mk([1, 1, 30], [200, 17, 60], 1), mk([1, 2, 1, 1], [90, 40, 300, 16], 2), mk([50], [50], 3)]
+    first = steps[0]
+    pool = [t.to(DEV) for t in (first.key_cache, first.value_cache)]
+    scales = [t.to(DEV) for t in (first.key_scales, first.value_scales)] if kind == "int8_block" else [None, None]
+    gs = GraphStep(num_heads_q=8, num_heads_kv=2, head_dim=128, num_blocks=60, max_blocks_per_req=24,
+                   softmax_scale=first.softmax_scale, max_tokens=64, max_reqs=6, max_extend_tiles=16,
+                   max_dequant_blocks=0 if kind == "bf16" else 64, kv_cache_dtype=kind, k_scale=first.k_scale,
+                   v_scale=first.v_scale, rope=rope)
+    for b in steps:
+        for t, src in zip(pool + scales, (b.key_cache, b.value_cache, b.key_scales, b.value_scales)):
+            if t is not None:
+                t.copy_(src)
+        eager = [t.clone() if t is not None else None for t in pool + scales]
+        q, k, v = (t.to(DEV) for t in (b.q, b.key, b.value))
+        got = gs.run(b, q, k, v, *pool, *scales)
+        st = DeviceStep(b, "cuda", rope=rope)
+        want = st.run_append(q, k, v, *eager)
+        torch.cuda.synchronize()
+        assert gs.check_errors() == 0 and st.check_errors() == 0
+        assert torch.equal(got, want)
+        for x, y in zip(pool + scales, eager):
+            if x is not None:
+                assert x.float().nan_to_num(7e4).equal(y.float().nan_to_num(7e4))
