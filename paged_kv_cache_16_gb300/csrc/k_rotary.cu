@@ -181,6 +181,9 @@ __device__ __forceinline__ void rotate_rows(const float *tab, const RopeParams &
     }
 }
 
+// Bound by HBM (8192 tokens x 40 heads of 128: 28.6 us, 5.9 TB/s; 43.3 us with
+// cos and sin read from shared memory per row, 8-byte pieces and one row of a thread
+// in flight) and by the launch for a decode step (64 tokens: 2.2 us).
 template <int W>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RopeParams rope, const RotaryParams p) {
     extern __shared__ float4 smem4[];
@@ -399,6 +402,15 @@ __device__ __forceinline__ void store_scaled(Rows rows, float amax, bool nan, co
 
 __device__ __forceinline__ int log2_up(int n) { return n <= 1 ? 0 : 32 - __clz(n - 1); }
 
+// Which part of a segment a CTA handles: the queries of up to 32 heads, or keys
+// or values of 8 kv heads (one per warp).  The queries, the longest parts, come
+// first in the grid.  K and V of a block are independent (each has scales of its
+// own): in CTAs of their own the dependent chain of a decode step is shorter
+// (64 requests, Hq 32, Hkv 8, int8: 3.6 us against 4.5 with both in one CTA; two
+// chunks of 2048 tokens into E4M3 codes 19.6 against 21.2, 4.4 TB/s of 12.7 us at
+// the copy rate; four into bf16 31.8 against 30.5, 5.7 TB/s).  Two CTAs per SM with
+// 8 rows of a thread in flight: bound by latency below a wave of CTAs (a decode
+// step: launch, starts and lengths, block id, scale), by HBM above.
 template <int D, int KIND, int W>
 __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ RopeParams rope, const AppendParams p) {
     using H = HeadRows<D, W>;
@@ -409,134 +421,102 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
     grid_launch_dependents();
     grid_dep_wait();
     const int kv_parts = (p.num_heads_kv + 7) / 8;
-    const bool kv = static_cast<int>(blockIdx.y) < kv_parts;
+    const int part = (static_cast<int>(blockIdx.y) + 2 * kv_parts) % static_cast<int>(gridDim.y);
     const Segment s = find_segment(p, blockIdx.x);
     if (s.n == 0) return;
-    const int half = rope.rotary_dim / 2;
-    if (!kv) {
-        fill_table(tab, rope, s.n, [&](int j) { return s.pos + j; });
+    auto pos_of = [&](int j) { return s.pos + j; };
+    if (part >= 2 * kv_parts) {
+        fill_table(tab, rope, s.n, pos_of);
         __syncthreads();
-        const int h0 = (static_cast<int>(blockIdx.y) - kv_parts) * p.q_heads_per_cta;
+        const int h0 = (part - 2 * kv_parts) * p.q_heads_per_cta;
         rotate_rows<W, 8>(tab, rope, p.q + s.t0 * p.q_stride + h0 * D, p.q_stride, p.q_out + s.t0 * p.q_out_stride + h0 * D,
-                       p.q_out_stride, s.n, log2_up(s.n), min(p.q_heads_per_cta, p.num_heads_q - h0), D);
+                          p.q_out_stride, s.n, log2_up(s.n), min(p.q_heads_per_cta, p.num_heads_q - h0), D);
         return;
     }
+    const bool value = part >= kv_parts;
+    const int half = value ? 0 : rope.rotary_dim / 2;   // > 0: rotate
     const int lane = threadIdx.x & 31;
-    const int h = blockIdx.y * 8 + threadIdx.x / 32;
+    const int h = (value ? part - kv_parts : part) * 8 + threadIdx.x / 32;
     const bool mine = h < p.num_heads_kv;
     const int rsub = lane / H::UPR;
-    const Unit<W> u(lane % H::UPR, rope);
-    const Unit<W> uv(lane % H::UPR);   // values: consecutive dims
+    const Unit<W> u = half > 0 ? Unit<W>(lane % H::UPR, rope) : Unit<W>(lane % H::UPR);
     const int first = s.pos % kBlockSize;
     // every row's loads before the first use of the block id
-    Raw<W> ka[H::NIT], kb[H::NIT], va[H::NIT], vb[H::NIT];
+    const uint16_t *src = value ? p.value : p.key;
+    const int64_t stride = value ? p.value_stride : p.key_stride;
+    Raw<W> ra[H::NIT], rb[H::NIT];
 #pragma unroll
     for (int it = 0; it < H::NIT; ++it) {
         const int r = it * H::RPI + rsub;
-        ka[it] = kb[it] = va[it] = vb[it] = Raw<W>{};
+        ra[it] = rb[it] = Raw<W>{};
         if (mine && r < s.n) {
-            const uint16_t *k = p.key + (s.t0 + r) * p.key_stride + h * D;
-            const uint16_t *v = p.value + (s.t0 + r) * p.value_stride + h * D;
-            ka[it] = load_raw<W>(k + u.a);
-            kb[it] = load_raw<W>(k + u.b);
-            va[it] = load_raw<W>(v + uv.a);
-            vb[it] = load_raw<W>(v + uv.b);
+            const uint16_t *x = src + (s.t0 + r) * stride + h * D;
+            ra[it] = load_raw<W>(x + u.a);
+            rb[it] = load_raw<W>(x + u.b);
         }
     }
-    if (half > 0) fill_table(tab, rope, s.n, [&](int j) { return s.pos + j; });
+    if (half > 0) fill_table(tab, rope, s.n, pos_of);
     __syncthreads();
-    if (!block_ok(p, s, blockIdx.y == 0) || !mine) return;
+    if (!block_ok(p, s, part == 0) || !mine) return;
     const int64_t row_stride = static_cast<int64_t>(p.num_heads_kv) * D;
     const int64_t base = static_cast<int64_t>(s.block) * kBlockSize * row_stride + h * D;   // element of row 0
+    void *cache = value ? p.value_cache : p.key_cache;
+    // the lane's two groups of row it * RPI + rsub, rotated (for the maximum and
+    // once more for the codes: fewer registers than keeping the rotated rows)
+    auto row_of = [&](int it, float (&a)[W], float (&b)[W]) {
+        unpack<W>(ra[it], a);
+        unpack<W>(rb[it], b);
+        if (half == 0) return;
+        Turn<W> turn;   // (a row past the segment: of its last token, zeros all the same)
+        turn.load(u, tab + min(it * H::RPI + rsub, s.n - 1) * rope.rotary_dim, half);
+        turn.apply(u, a, b);
+    };
     if constexpr (BLOCK_SCALED) {
-        const int64_t at = static_cast<int64_t>(s.block) * p.num_heads_kv + h;
-        float old_k = 0.f, old_v = 0.f;
-        if (first > 0) {
-            old_k = p.key_scales[at];
-            old_v = p.value_scales[at];
-        }
-        // (rotated once for the maximum and once more for the codes: 32 registers
-        // fewer than keeping the rotated rows, which would spill)
-        auto key_row = [&](int it, float (&a)[W], float (&b)[W]) {
-            unpack<W>(ka[it], a);
-            unpack<W>(kb[it], b);
-            if (half == 0) return;
-            Turn<W> turn;   // (a row past the segment: of its last token, zeros all the same)
-            turn.load(u, tab + min(it * H::RPI + rsub, s.n - 1) * rope.rotary_dim, half);
-            turn.apply(u, a, b);
-        };
-        auto value_row = [&](int it, float (&a)[W], float (&b)[W]) {
-            unpack<W>(va[it], a);
-            unpack<W>(vb[it], b);
-        };
-        float mk = 0.f, mv = 0.f;
-        bool nan_k = false, nan_v = false;
+        float *scale_at = (value ? p.value_scales : p.key_scales) + static_cast<int64_t>(s.block) * p.num_heads_kv + h;
+        const float old = first > 0 ? *scale_at : 0.f;
+        float amax = 0.f;
+        bool nan = false;
 #pragma unroll
         for (int it = 0; it < H::NIT; ++it) {
             if (it * H::RPI >= s.n) break;
             float xa[W], xb[W];
-            key_row(it, xa, xb);
-            track<W>(xa, mk, nan_k);
-            track<W>(xb, mk, nan_k);
-            value_row(it, xa, xb);
-            track<W>(xa, mv, nan_v);
-            track<W>(xb, mv, nan_v);
+            row_of(it, xa, xb);
+            track<W>(xa, amax, nan);
+            track<W>(xb, amax, nan);
         }
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            mk = fmaxf(mk, __shfl_xor_sync(0xffffffffu, mk, o));
-            mv = fmaxf(mv, __shfl_xor_sync(0xffffffffu, mv, o));
-        }
-        if (INT8) {
-            nan_k = __any_sync(0xffffffffu, nan_k);
-            nan_v = __any_sync(0xffffffffu, nan_v);
-        }
-        store_scaled<D, W, INT8>(key_row, mk, nan_k, u, static_cast<uint8_t *>(p.key_cache) + base, row_stride,
-                                 p.key_scales + at, old_k, first, s.n, lane);
-        store_scaled<D, W, INT8>(value_row, mv, nan_v, uv, static_cast<uint8_t *>(p.value_cache) + base, row_stride,
-                                 p.value_scales + at, old_v, first, s.n, lane);
+        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        if (INT8) nan = __any_sync(0xffffffffu, nan);
+        store_scaled<D, W, INT8>(row_of, amax, nan, u, static_cast<uint8_t *>(cache) + base, row_stride, scale_at, old, first,
+                                 s.n, lane);
     } else {
 #pragma unroll
         for (int it = 0; it < H::NIT; ++it) {
+            if (it * H::RPI >= s.n) break;
             const int r = it * H::RPI + rsub;
-            if (r >= s.n) continue;
             float xa[W], xb[W];
-            unpack<W>(ka[it], xa);
-            unpack<W>(kb[it], xb);
-            Turn<W> turn;
-            turn.load(u, tab + r * rope.rotary_dim, half);
-            turn.apply(u, xa, xb);
+            row_of(it, xa, xb);
+            if (r >= s.n) continue;
             const int64_t row = base + (first + r) * row_stride;
             if constexpr (KIND == kCacheBf16) {
-                uint16_t *k = static_cast<uint16_t *>(p.key_cache) + row, *v = static_cast<uint16_t *>(p.value_cache) + row;
-                if (half > 0) {
-                    ka[it] = pack<W>(xa);
-                    kb[it] = pack<W>(xb);
-                }   // else a bit copy (a NaN keeps its bits)
-                store_raw<W>(k + u.a, ka[it]);
-                store_raw<W>(k + u.b, kb[it]);
-                store_raw<W>(v + uv.a, va[it]);
-                store_raw<W>(v + uv.b, vb[it]);
+                uint16_t *c = static_cast<uint16_t *>(cache) + row;
+                // (not rotated: a bit copy, a NaN keeps its bits)
+                store_raw<W>(c + u.a, half > 0 ? pack<W>(xa) : ra[it]);
+                store_raw<W>(c + u.b, half > 0 ? pack<W>(xb) : rb[it]);
             } else {
-                // codes of x / k_scale, the quotient rounded in 32 bits as pa_write_kv_fp8 does
-                uint8_t *k = static_cast<uint8_t *>(p.key_cache) + row, *v = static_cast<uint8_t *>(p.value_cache) + row;
+                // codes of x / scale, the quotient rounded in 32 bits as pa_write_kv_fp8 does
+                uint8_t *c = static_cast<uint8_t *>(cache) + row;
+                const float scale = value ? p.v_scale : p.k_scale;
                 uint32_t ca[W / 4], cb[W / 4];
-                auto codes = [&](const float (&y)[W], float scale, uint32_t (&c)[W / 4]) {
 #pragma unroll
-                    for (int i = 0; i < W / 4; ++i)
-                        c[i] = encode4<false>(__fdiv_rn(y[4 * i], scale), __fdiv_rn(y[4 * i + 1], scale),
-                                              __fdiv_rn(y[4 * i + 2], scale), __fdiv_rn(y[4 * i + 3], scale));
-                };
-                codes(xa, p.k_scale, ca);
-                codes(xb, p.k_scale, cb);
-                store_codes<W>(k + u.a, ca);
-                store_codes<W>(k + u.b, cb);
-                unpack<W>(va[it], xa);
-                unpack<W>(vb[it], xb);
-                codes(xa, p.v_scale, ca);
-                codes(xb, p.v_scale, cb);
-                store_codes<W>(v + uv.a, ca);
-                store_codes<W>(v + uv.b, cb);
+                for (int i = 0; i < W / 4; ++i) {
+                    ca[i] = encode4<false>(__fdiv_rn(xa[4 * i], scale), __fdiv_rn(xa[4 * i + 1], scale),
+                                           __fdiv_rn(xa[4 * i + 2], scale), __fdiv_rn(xa[4 * i + 3], scale));
+                    cb[i] = encode4<false>(__fdiv_rn(xb[4 * i], scale), __fdiv_rn(xb[4 * i + 1], scale),
+                                           __fdiv_rn(xb[4 * i + 2], scale), __fdiv_rn(xb[4 * i + 3], scale));
+                }
+                store_codes<W>(c + u.a, ca);
+                store_codes<W>(c + u.b, cb);
             }
         }
     }
@@ -582,9 +562,9 @@ cudaError_t launch_rotary(const RopeParams &rope, const RotaryParams &p0, cudaSt
 cudaError_t launch_append(int head_dim, int kind, const RopeParams &rope, const AppendParams &p0, cudaStream_t stream) {
     AppendParams p = p0;
     if (p.num_tokens <= 0 || p.num_reqs <= 0) return cudaSuccess;
-    p.q_heads_per_cta = p.num_heads_q < 16 ? p.num_heads_q : 16;
+    p.q_heads_per_cta = p.num_heads_q < 32 ? p.num_heads_q : 32;
     const int q_parts = p.q == nullptr ? 0 : (p.num_heads_q + p.q_heads_per_cta - 1) / p.q_heads_per_cta;
-    const dim3 grid(p.num_tokens / kBlockSize + 2 * p.num_reqs, (p.num_heads_kv + 7) / 8 + q_parts);
+    const dim3 grid(p.num_tokens / kBlockSize + 2 * p.num_reqs, 2 * ((p.num_heads_kv + 7) / 8) + q_parts);
     const bool wide = wide_units(rope, head_dim);
     if (head_dim == 128)
         return wide ? launch_append_d<128, 8>(kind, rope, p, grid, stream) : launch_append_d<128, 4>(kind, rope, p, grid, stream);
