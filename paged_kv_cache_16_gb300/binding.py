@@ -303,8 +303,16 @@ def _ptr(t) -> int | None:
     return int(t.data_ptr())
 
 
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int | None:
     if stream is None:
+        # the current stream's handle without a Stream object (0.2 us against
+        # 2.9: as long as the C call itself)
+        if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_raw_device())
         return int(torch.cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
@@ -669,19 +677,21 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
 def pa_attention_scaled(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace,
                         stream=None):
     """Attention over block-scaled 8-bit caches (see pa.h)."""
-    nbytes = workspace.numel() * workspace.element_size()
-    _check(load().pa_attention_scaled(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(key_scales),
-                                      _ptr(value_scales), _ptr(block_table), _ptr(out), _ptr(workspace), nbytes,
-                                      _stream(stream)), "pa_attention_scaled")
+    st = load().pa_attention_scaled(plan.handle, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                    key_scales.data_ptr(), value_scales.data_ptr(), block_table.data_ptr(),
+                                    out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st:
+        _check(st, "pa_attention_scaled")
 
 
 def pa_attention_scaled_launch(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out,
                                workspace, stream=None):
     """Its kernels alone, after pa_upload_metadata (capturable in a CUDA graph)."""
-    nbytes = workspace.numel() * workspace.element_size()
-    _check(load().pa_attention_scaled_launch(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(key_scales),
-                                             _ptr(value_scales), _ptr(block_table), _ptr(out), _ptr(workspace), nbytes,
-                                             _stream(stream)), "pa_attention_scaled_launch")
+    st = load().pa_attention_scaled_launch(plan.handle, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                           key_scales.data_ptr(), value_scales.data_ptr(), block_table.data_ptr(),
+                                           out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    if st:
+        _check(st, "pa_attention_scaled_launch")
 
 
 NO_ALLOC_SCRATCH_BYTES = 16 << 20
