@@ -107,7 +107,6 @@ struct Consumer {
         // (bf16's range does not fit f16's): the factor returns in the scores
         uint32_t qt[NT][D / 16][2];
         float rf[NT][2];
-        int lim[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const int r = 8 * n + g;
@@ -137,11 +136,7 @@ struct Consumer {
                     qt[n][kk][e] = pack_f16x2(bf16_lo(qt[n][kk][e]) * down, bf16_hi(qt[n][kk][e]) * down);
             const float up = __uint_as_float(static_cast<uint32_t>(127 + e2) << 23) * b.scale_log2;
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                rf[n][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e));   // of row 8n + 2t + e
-                // token i of the item sees keys < key_end - (n_tok - 1 - i)
-                lim[n][e] = min(item.key_end, item.key_end - (item.n_tok - 1 - (8 * n + 2 * t4 + e) / G));
-            }
+            for (int e = 0; e < 2; ++e) rf[n][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e));   // of row 8n + 2t + e
         }
         const int lim_lo = item.key_end - (item.n_tok - 1);
         float ot[NT][D / 16][4], lt[NT][2], ref[NT][2];
@@ -202,16 +197,15 @@ struct Consumer {
         auto round = [&](auto two_c, int pg) -> bool {
             constexpr int NB = decltype(two_c)::value ? 2 : 1;
             uint32_t st[NB], fin[NB];
-            float sc[NB][NT][4], kf[NB][NT][2], lv[NB], iv[NB];
+            float sc[NB][NT][4], kf[NB][NT][2], lv[NB];
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 if (!warp_wait(full0 + 8u * slot, parity, abort_flag)) return false;
                 st[k] = stage0 + static_cast<uint32_t>(slot) * C::STAGE + warp * C::BOX;
                 fin[k] = empty0 + 8u * slot;
                 const uint32_t sa = scale0 + 4u * (2 * HG * slot + warp);
-                const float ks = used_scale(lds_f32(sa)), vs = used_scale(lds_f32(sa + 4u * HG));
-                lv[k] = lg2(vs);
-                iv[k] = __fdividef(1.f, vs);
+                const float ks = used_scale(lds_f32(sa));
+                lv[k] = lg2(used_scale(lds_f32(sa + 4u * HG)));
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -226,13 +220,18 @@ struct Consumer {
             const int key0 = pg * kBlockSize;
             const int valid = item.key_end - key0;   // V rows past it may be anything
             if (lim_lo - key0 < NB * kBlockSize) {
+                // token i of the item sees keys < key_end - (n_tok - 1 - i)
 #pragma unroll
-                for (int k = 0; k < NB; ++k)
+                for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
+                    for (int e = 0; e < 2; ++e) {
+                        const int lim = min(item.key_end, lim_lo + (8 * n + 2 * t4 + e) / G) - key0;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)   // a key past the row's causal limit
-                            if (key0 + 16 * k + g + 8 * (e >> 1) >= lim[n][e & 1]) sc[k][n][e] = -INFINITY;
+                        for (int k = 0; k < NB; ++k) {
+                            if (16 * k + g >= lim) sc[k][n][e] = -INFINITY;
+                            if (16 * k + g + 8 >= lim) sc[k][n][e + 2] = -INFINITY;
+                        }
+                    }
             }
             bool grow = false;
             float mx[NT][2];
@@ -273,7 +272,8 @@ struct Consumer {
             }
             uint32_t w[NB][NT][2];
 #pragma unroll
-            for (int k = 0; k < NB; ++k)
+            for (int k = 0; k < NB; ++k) {
+                const float iv = ex2(-lv[k]);   // 1 / vs, the inverse of what the exponents hold
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     float x[4];
@@ -282,13 +282,14 @@ struct Consumer {
                         const float c = lv[k] - ref[n][e];
                         x[e] = ex2(fmaf(sc[k][n][e], kf[k][n][e], c));
                         x[e + 2] = ex2(fmaf(sc[k][n][e + 2], kf[k][n][e], c));
-                        lt[n][e] = fmaf(x[e] + x[e + 2], iv[k], lt[n][e]);
+                        lt[n][e] = fmaf(x[e] + x[e + 2], iv, lt[n][e]);
                     }
                     // P^T as B fragments: rows (8n + 2t, 8n + 2t + 1) of key g
                     // (g + 8), transposed 8x8
                     w[k][n][0] = movmatrix_trans(pack_f16x2(x[0], x[1]));
                     w[k][n][1] = movmatrix_trans(pack_f16x2(x[2], x[3]));
                 }
+            }
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 if (valid < (k + 1) * kBlockSize) pv(std::true_type{}, st[k] + C::TSTAGE, w[k], valid - k * kBlockSize);
