@@ -204,8 +204,10 @@ struct Consumer {
                 st[k] = stage0 + static_cast<uint32_t>(slot) * C::STAGE + warp * C::BOX;
                 fin[k] = empty0 + 8u * slot;
                 const uint32_t sa = scale0 + 4u * (2 * HG * slot + warp);
-                const float ks = used_scale(lds_f32(sa));
-                lv[k] = lg2(used_scale(lds_f32(sa + 4u * HG)));
+                // (a NaN value scale shows in the scores, where masks can take it out)
+                const float vs = used_scale(lds_f32(sa + 4u * HG));
+                const float ks = vs == vs ? used_scale(lds_f32(sa)) : vs;
+                lv[k] = vs == vs ? lg2(vs) : 0.f;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -230,6 +232,7 @@ struct Consumer {
                         for (int k = 0; k < NB; ++k) {
                             if (16 * k + g >= lim) sc[k][n][e] = -INFINITY;
                             if (16 * k + g + 8 >= lim) sc[k][n][e + 2] = -INFINITY;
+                            if (16 * k >= lim) kf[k][n][e] = 1.f;   // none of the block: its scale, NaN even, plays no part
                         }
                     }
             }

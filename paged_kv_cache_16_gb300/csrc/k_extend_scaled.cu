@@ -419,6 +419,9 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
                         if (c >= lim) sr[c] = __float_as_uint(-INFINITY);
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)   // none of the block: its scale, NaN even, plays no part
+                        if (kBlockSize * b >= lim) fs[b] = 1.f;
                 }
                 // row max of s + log2 vs
                 float mxs = -INFINITY;

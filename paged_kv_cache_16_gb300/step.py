@@ -73,6 +73,8 @@ class DeviceStep:
         return self.slots[:b.num_tokens]
 
     def write(self, key, value, key_cache, value_cache, stream=None):
+        if self.batch.kv_cache_dtype not in ("bf16", "fp8"):
+            raise ValueError("block-scaled caches are written by append (run_append)")
         if self.batch.kv_cache_dtype == "fp8":
             binding.pa_write_kv_fp8(key, value, self.slots, key_cache, value_cache, self.batch.k_scale,
                                     self.batch.v_scale, self.error_word, stream)

@@ -218,6 +218,40 @@ def test_append_scaled_nan_and_infinity(code):
     check_scaled(c, run_append(c), None)
 
 
+def test_append_int8_nan_scale_lasts_until_the_block_starts_anew():
+    c = oc.AppendCase(hq=2, hkv=2, d=64, q_lens=[2, 2, 2], computed=[4, 30, 16], code="int8", seed=1)
+    c.ks[c.table[0, 0], 1] = float("nan")       # joined: stays
+    c.vs[c.table[1, 1], 0] = float("nan")       # the first of its two blocks: stays
+    c.ks[c.table[2, 1], 0] = float("nan")       # starts anew at slot 0: gone
+    got = run_append(c)
+    check_scaled(c, got, None)
+    assert torch.isnan(got[3][c.table[0, 0], 1]) and torch.isnan(got[4][c.table[1, 1], 0])
+    assert torch.isfinite(got[3][c.table[2, 1], 0])
+
+
+def test_append_in_place_in_the_packed_projection():
+    """q rotated in place beside the keys and values that are being stored."""
+    c = oc.AppendCase(hq=4, hkv=2, d=64, q_lens=[19, 1], computed=[3, 40], code="int8", seed=2)
+    rope = binding.pa_rope_create(rotary_dim=64)
+    want = run_append(c, rope)
+    rows = torch.cat([c.q, c.key, c.value], 1).to(DEV)
+    before = rows.clone()
+    q, k, v = rows[:, :4], rows[:, 4:6], rows[:, 6:]
+    kc, vc, ks, vs = (t.to(DEV) for t in (c.kc, c.vc, c.ks, c.vs))
+    binding.pa_append_kv(rope, k, v, i32(c.qsl), i32(c.nc), i32(c.table), kc, vc, key_scales=ks, value_scales=vs, q=q, q_out=q)
+    torch.cuda.synchronize()
+    for x, y in zip((q, kc, vc, ks, vs), want):
+        assert torch.equal(x, y)
+    assert torch.equal(rows[:, 4:], before[:, 4:])
+
+
+def test_wrappers_refuse_tensors_of_other_devices():
+    rope = binding.pa_rope_create(rotary_dim=64)
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        binding.pa_rotary(rope, x, torch.zeros(3, dtype=torch.int32), x)
+
+
 def test_append_scaled_foreign_scales():
     """Old scales that are no powers of two: kept where large enough, codes
     re-coded by the true ratio where not."""

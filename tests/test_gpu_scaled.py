@@ -125,9 +125,23 @@ def test_nan_scales_reach_the_output(code):
     bad = torch.isnan(out).any(-1)
     want = torch.zeros_like(bad)
     want[0, 4:8] = True
-    want[2:, 0:4] = True
-    # chunk tokens before block 1 (positions 70 .. 99 see keys 16 .. on): all see it
+    want[2:, 0:4] = True                 # positions 70 .. 99 all see block 1
     assert torch.equal(bad, want)
+
+
+@pytest.mark.parametrize("q_len", [4, 40])
+@pytest.mark.parametrize("which", ["ks", "vs"])
+def test_nan_scales_of_later_blocks(q_len, which):
+    """Tokens of a verify row or a chunk that stand before a block with a NaN scale
+    do not see it; the others' rows of its head are NaN."""
+    c = oc.Case(hq=8, hkv=2, d=128, q_lens=[q_len], seq_lens=[82], code="int8", seed=5)
+    clean, tol = c.reference()
+    getattr(c, which)[c.table[0, 5], 1] = float("nan")          # block 5: positions 80, 81
+    out = oc.OnGpu(c).run()
+    seen = np.arange(82 - q_len, 82) >= 80
+    bad = torch.isnan(out.float().cpu()).any(-1).numpy()
+    assert np.array_equal(bad[:, 4:], np.repeat(seen[:, None], 4, 1)) and not bad[:, :4].any()
+    oc.assert_within(out[:q_len - 2], clean[:q_len - 2], tol[:q_len - 2])
 
 
 def test_tiny_and_zero_scales():
