@@ -22,6 +22,12 @@
 // V^T P^T): the 16 keys of a block are the MMA rows, the query rows (token,
 // head) its columns, NT tiles of 8 of them, so a code is converted to f16 once
 // for all query rows.
+//
+// Bound by HBM: 8 contexts of 131072 int8 keys (Hq 64, Hkv 8, D 128) 319 us with
+// the merge, 6.7 TB/s (0.99 of the copy rate; 312 without the copies of the
+// scales); 64 contexts of 540..4068 53 us, 5.7 TB/s around the ring's fill, the tail
+// and the merge (51 with the consumers' arithmetic taken out); 128 rows of 4
+// tokens over E4M3 206 us (196).
 #include <type_traits>
 
 #include "dev.cuh"
