@@ -13,12 +13,12 @@
 // kernel as one 16-byte record, travel with the V stage: a softmax warp may wait
 // for that stage, which is not given back before its weights have been used.
 //
-// Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 254 us at
-// 2070 MHz, 1353 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
-// 260 (its 8 boxes per key tile against one here).  A step of 128 keys takes ~3700
-// cycles for 2048 of MMAs: with the softmax arithmetic taken out 205 us, what the
-// MMA thread's commits and waits leave of the pipe; the rest is the chain S ->
-// softmax -> P of a sub-tile.  Measured and not kept (us): weights through
+// Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 236 us at
+// 2070 MHz, 1456 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
+// 262.  A step of 128 keys has 2048 cycles of MMAs and takes ~3400: what the MMA
+// thread does between two MMAs leaves the pipe idle (ring indices by division and
+// all commits at the groups' ends: 254), the rest is the chain S -> softmax -> P of
+// a sub-tile.  Measured and not kept (us, against the 254): weights through
 // shared memory, QK^T a step ahead, 312 (every operand from shared memory fills
 // its bandwidth); one S buffer for both sub-tiles and QK^T a step ahead, 353 with
 // one MMA thread, 283 with one for QK^T and one for PV; an MMA thread per sub-tile,
@@ -247,49 +247,67 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer --
         if (lane == 0) {
-            int kc = 0, vc = 0;          // K and V tiles consumed (over all tiles)
-            int pc[2] = {0, 0};          // P tiles consumed per sub-tile
-            int n_q = 0;                 // Q tiles consumed
             bool ok = true;
-            // operand descriptors built once; each MMA only moves the start
-            // address (the issuing thread shares its issue slots with two
-            // softmax warps, so every instruction here counts)
+            // The pipe takes the next MMA only when the one before is nearly
+            // done, so whatever this thread does between two MMAs beyond ~60
+            // cycles leaves it idle: descriptors and barrier addresses are kept as
+            // running values, and what is left (barrier tests, stage releases,
+            // the next step's values) is spread over the gaps of the MMA groups.
             const uint64_t q_desc[2] = {sdesc_sw128(q_s(0), 16, 1024), sdesc_sw128(q_s(1), 16, 1024)};
             const uint64_t k_desc0 = sdesc_sw128(k_s(0), 16, 1024);
             const uint64_t v_desc0 = sdesc_sw128(v_s(0), C::HALF, 1024);
-            // readiness of the barriers the thread needs next, polled (one
-            // test each) between MMAs, where the pipe still holds queued work
+            const uint32_t sfull[2] = {bar(B_SFULL), bar(B_SFULL + 1)}, pfull[2] = {bar(B_PFULL), bar(B_PFULL + 1)};
+            const uint32_t k_bar0 = bar(B_KFULL), v_bar0 = bar(B_VFULL);
+            constexpr uint32_t kEmptyK = 8u * (B_KEMPTY - B_KFULL), kEmptyV = 8u * (B_VEMPTY - B_VFULL);
+            uint32_t k_slot = 0, k_par = 0, v_slot = 0, v_par = 0;   // next K and V tile: ring slot, phase parity
+            uint32_t k_bar = k_bar0, v_bar = v_bar0;                 // their full barriers
+            uint64_t k_desc = k_desc0, v_desc = v_desc0;
+            uint32_t p_par[2] = {0, 0};                              // parity of the next P
+            uint32_t n_q = 0;
+            // seen complete by a test in an MMA group
             bool p_ready[2] = {false, false}, k_ready = false, v_ready = false;
-            auto poll = [&](bool &flag, int b, int parity) {
-                if (!flag) flag = mbar_test_wait(bar(b), static_cast<uint32_t>(parity));
+            auto poll = [](bool &flag, uint32_t b, uint32_t parity) {
+                if (!flag) flag = mbar_test_wait(b, parity);
             };
-            auto qk = [&](int t, int s, auto mid) {
-                const uint64_t a0 = q_desc[t];
-                const uint64_t b0 = sdesc_advance(k_desc0, static_cast<uint32_t>(s) * C::KVB);
-                const uint32_t d = tmem + col_s(t);
+            auto need = [&](bool &flag, uint32_t b, uint32_t parity) -> bool {
+                if (!flag && !mbar_wait_spin(b, parity, &abort_flag)) return false;
+                flag = false;
+                return true;
+            };
+            auto next_k = [&] {
+                const bool wrap = k_slot + 1 == C::NSK;
+                k_slot = wrap ? 0 : k_slot + 1;
+                k_par ^= wrap ? 1u : 0u;
+                k_bar = k_bar0 + 8u * k_slot;
+                k_desc = sdesc_advance(k_desc0, k_slot * C::KVB);
+            };
+            auto next_v = [&] {
+                const bool wrap = v_slot + 1 == C::NSV;
+                v_slot = wrap ? 0 : v_slot + 1;
+                v_par ^= wrap ? 1u : 0u;
+                v_bar = v_bar0 + 8u * v_slot;
+                v_desc = sdesc_advance(v_desc0, v_slot * C::KVB);
+            };
+            // MMA groups; gap(kk) runs behind MMA kk
+            auto qk = [&](int t, auto gap) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = (kk / 4) * C::HALF + (kk % 4) * 32;
-                    tc_mma(d, sdesc_advance(a0, off), sdesc_advance(b0, off), C::IDESC_QK, kk > 0 ? 1u : 0u);
-                    if (kk == D / 32 - 1) mid();
+                    tc_mma(tmem + col_s(t), sdesc_advance(q_desc[t], off), sdesc_advance(k_desc, off), C::IDESC_QK,
+                           kk > 0 ? 1u : 0u);
+                    gap(kk);
                 }
-                tc_commit(bar(B_SFULL + t));
+                tc_commit(sfull[t]);
             };
-            auto pv = [&](int t, int sv, bool first, auto mid) -> bool {
-                if (!p_ready[t] && !mbar_wait_spin(bar(B_PFULL + t), pc[t] & 1, &abort_flag)) return false;
-                p_ready[t] = false;
-                ++pc[t];
-                tc_fence_after();
-                const uint64_t b0 = sdesc_advance(v_desc0, static_cast<uint32_t>(sv) * C::KVB);
-                const uint32_t d = tmem + col_o(t), a = tmem + col_s(t);
+            auto pv = [&](int t, uint32_t accumulate, auto gap) {
 #pragma unroll
                 for (int kk = 0; kk < kTileKeys / 16; ++kk) {
-                    tc_mma_ts(d, a + kk * 8, sdesc_advance(b0, kk * 2048), C::IDESC_PV, (!first || kk > 0) ? 1u : 0u);
-                    if (kk == 3) mid();
+                    tc_mma_ts(tmem + col_o(t), tmem + col_s(t) + kk * 8, sdesc_advance(v_desc, kk * 2048), C::IDESC_PV,
+                              kk > 0 ? 1u : accumulate);
+                    gap(kk);
                 }
-                return true;
             };
-            auto nothing = [] {};
+            auto nothing = [](int) {};
             for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
                 const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
                 const TileShape sh = tile_shape(tile, tpt);
@@ -299,61 +317,81 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     if (ok) tc_commit(bar(B_QEMPTY));
                     continue;
                 }
-                // QK^T still to issue in this tile; Q is released after the last
-                int q_left = sh.n_sub[0] + sh.n_sub[1];
-                ok = mbar_wait_spin(bar(B_KFULL + kc % C::NSK), (kc / C::NSK) & 1, &abort_flag);
-                if (!ok) break;
+                const int n0 = sh.n_sub[0], n1 = sh.n_sub[1], n = sh.n_tiles;
+                if (!need(k_ready, k_bar, k_par)) { ok = false; break; }
                 tc_fence_after();
+                if (n0 > 0) qk(0, nothing);
+                if (n1 > 0) qk(1, nothing);
+                tc_commit(k_bar + kEmptyK);   // K tile 0 read by both QK^T
+                if (n == 1) tc_commit(bar(B_QEMPTY));
+                next_k();
+                int j = 0;
+                // steps whose two sub-tiles both go on: PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1)
+                uint32_t k_release = 0;   // K stage to give back in the next gap
+                for (; j + 1 < min(n0, n1); ++j) {
+                    if (!need(v_ready, v_bar, v_par) || !need(p_ready[0], pfull[0], p_par[0])) { ok = false; break; }
+                    tc_fence_after();
+                    pv(0, j > 0 ? 1u : 0u, [&](int kk) {
+                        if (kk == 1 && k_release) tc_commit(k_release);
+                        if (kk == 3) p_par[0] ^= 1u;
+                        if (kk == 5) poll(k_ready, k_bar, k_par);
+                    });
+                    if (!need(k_ready, k_bar, k_par)) { ok = false; break; }
+                    tc_fence_after();
+                    // overwrites S_0: issued after the PV that reads P_0
+                    qk(0, [&](int kk) {
+                        if (kk == D / 16 - 3) poll(p_ready[1], pfull[1], p_par[1]);
+                    });
+                    if (!need(p_ready[1], pfull[1], p_par[1])) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t v_done = v_bar + kEmptyV;
+                    pv(1, j > 0 ? 1u : 0u, [&](int kk) {
+                        if (kk == 3) p_par[1] ^= 1u;
+                    });
+                    qk(1, [&](int kk) {
+                        if (kk == 0) tc_commit(v_done);   // V tile j read by both PV
+                        if (kk == 1) next_v();
+                        if (kk == 2) poll(v_ready, v_bar, v_par);
+                        if (kk == D / 16 - 2) poll(p_ready[0], pfull[0], p_par[0]);
+                    });
+                    k_release = k_bar + kEmptyK;   // K tile j+1 read by both QK^T
+                    next_k();
+                }
+                if (ok && k_release) {
+                    tc_commit(k_release);
+                    if (j + 1 == n) tc_commit(bar(B_QEMPTY));
+                }
+                // the last steps, of one sub-tile or without a QK^T
+                for (; j < n && ok; ++j) {
+                    ok = need(v_ready, v_bar, v_par);
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (sh.n_sub[t] > 0) {
-                        qk(t, kc % C::NSK, nothing);
-                        if (--q_left == 0) tc_commit(bar(B_QEMPTY));
-                    }
-                tc_commit(bar(B_KEMPTY + kc % C::NSK));   // K tile 0 read by both QK^T
-                ++kc;
-                for (int j = 0; j < sh.n_tiles && ok; ++j) {
-                    const int sv = vc % C::NSV;
-                    const int t_last = j < sh.n_sub[1] ? 1 : 0;   // last sub-tile that reads V tile j
-                    const bool k_next = j + 1 < sh.n_tiles;
-                    bool k_used = false;
-                    if (!v_ready) ok = mbar_wait_spin(bar(B_VFULL + sv), (vc / C::NSV) & 1, &abort_flag);
-                    v_ready = false;
-#pragma unroll
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (j >= sh.n_sub[t]) continue;
-                        // during PV_0: the next K tile; during PV_1: the next V tile
-                        if (t == 0)
-                            ok = pv(0, sv, j == 0, [&] { if (k_next) poll(k_ready, B_KFULL + kc % C::NSK, (kc / C::NSK) & 1); });
-                        else
-                            ok = pv(1, sv, j == 0, [&] { poll(v_ready, B_VFULL + (vc + 1) % C::NSV, ((vc + 1) / C::NSV) & 1); });
+                    for (int t = 0; t < 2; ++t) {
+                        const int nt = t ? n1 : n0;
+                        if (!ok || j >= nt) continue;
+                        ok = need(p_ready[t], pfull[t], p_par[t]);
                         if (!ok) break;
-                        if (t == t_last) tc_commit(bar(B_VEMPTY + sv));   // V tile j read by both PV
-                        if (j + 1 < sh.n_sub[t]) {
-                            if (!k_ready) {
-                                ok = mbar_wait_spin(bar(B_KFULL + kc % C::NSK), (kc / C::NSK) & 1, &abort_flag);
-                                if (!ok) break;
-                                k_ready = true;
-                            }
-                            k_used = true;
+                        p_par[t] ^= 1u;
+                        tc_fence_after();
+                        pv(t, j > 0 ? 1u : 0u, nothing);
+                        if (j + 1 < nt) {
+                            if (!k_ready) ok = mbar_wait_spin(k_bar, k_par, &abort_flag);
+                            if (!ok) break;
+                            k_ready = true;
                             tc_fence_after();
-                            // overwrites S_t: issued after the PV that reads P_t.
-                            // During QK_0 poll P_1 of this step, during QK_1 P_0 of the next
-                            if (t == 0)
-                                qk(0, kc % C::NSK, [&] { if (j < sh.n_sub[1]) poll(p_ready[1], B_PFULL + 1, pc[1] & 1); });
-                            else
-                                qk(1, kc % C::NSK, [&] { poll(p_ready[0], B_PFULL + 0, pc[0] & 1); });
-                            if (--q_left == 0) tc_commit(bar(B_QEMPTY));
+                            qk(t, nothing);
                         } else {
                             tc_commit(bar(B_ODONE + t));
                         }
                     }
-                    if (ok && k_used) {
-                        tc_commit(bar(B_KEMPTY + kc % C::NSK));   // K tile j+1 read by both QK^T
-                        ++kc;
+                    if (!ok) break;
+                    tc_commit(v_bar + kEmptyV);
+                    next_v();
+                    if (j + 1 < n) {
+                        tc_commit(k_bar + kEmptyK);
+                        next_k();
                         k_ready = false;
+                        if (j + 2 == n) tc_commit(bar(B_QEMPTY));
                     }
-                    ++vc;
                 }
             }
             if (!ok) raise_abort(&abort_flag, p.err, kErrTimeout);
