@@ -57,6 +57,13 @@ def test_tile_rows(code, scales, hq, hkv, d):
     check(oc.Case(hq=hq, hkv=hkv, d=d, q_lens=[37, 1, 129, 1], seq_lens=[37, 300, 300, 1], code=code, scales=scales, seed=d))
 
 
+@pytest.mark.parametrize("num_sms", [4, 5, 11])
+def test_tiles_evened_out(num_sms):
+    """26 tiles of 5 to 11 steps whose greedy assignment is 4% to 15% off the
+    mean, so that the planner packs them anew: every row is written once."""
+    check(oc.Case(hq=8, hkv=2, d=64, q_lens=[300, 500], seq_lens=[1200, 900], code="int8", seed=5), num_sms=num_sms)
+
+
 @pytest.mark.parametrize("code", ["int8", "e4m3"])
 def test_cascade(code):
     check(oc.Case(hq=8, hkv=2, d=128, q_lens=[1, 1, 3, 20], seq_lens=[600, 530, 700, 560], code=code, seed=1, shared=32))
