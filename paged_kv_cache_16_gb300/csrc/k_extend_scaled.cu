@@ -13,16 +13,21 @@
 // kernel as one 16-byte record, travel with the V stage: a softmax warp may wait
 // for that stage, which is not given back before its weights have been used.
 //
-// Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 236 us at
-// 2070 MHz, 1456 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
-// 262.  A step of 128 keys has 2048 cycles of MMAs and takes ~3400: what the MMA
+// Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 213 us at
+// 2070 MHz, 1612 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
+// 248.  A step of 128 keys has 2048 cycles of MMAs and takes ~3050: what the MMA
 // thread does between two MMAs leaves the pipe idle (ring indices by division and
-// all commits at the groups' ends: 254), the rest is the chain S -> softmax -> P of
-// a sub-tile.  Measured and not kept (us, against the 254): weights through
-// shared memory, QK^T a step ahead, 312 (every operand from shared memory fills
-// its bandwidth); one S buffer for both sub-tiles and QK^T a step ahead, 353 with
-// one MMA thread, 283 with one for QK^T and one for PV; an MMA thread per sub-tile,
-// 317, taking turns at the pipe 260; and with two threads per row 293.
+// all commits at the groups' ends: 8% more), the rest is the chain S -> softmax -> P
+// of a sub-tile (~1500 cycles), which its own PV and QK^T follow; P handed over in
+// halves, so that PV begins under the second half's exponentials, takes 3% off.
+// Measured and not kept, as parts of the time then: weights through shared memory,
+// QK^T a step ahead, +23% (every operand from shared memory fills its bandwidth);
+// one S buffer for both sub-tiles and QK^T a step ahead, +39% with one MMA thread,
+// +11% with one for QK^T and one for PV; an MMA thread per sub-tile, +25%, taking
+// turns at the pipe +2%; two threads per row +15%; weights against the old
+// reference beside the maximum that checks it, S read again where a row needs a
+// new one, +27% (registers); the blocks' factors read from shared memory where
+// they are used instead of held, +2% (+6% with P in halves).
 #include "dev.cuh"
 
 namespace pa {
@@ -73,10 +78,10 @@ enum : int {
     B_KEMPTY = 7,   // +stage (2)
     B_VEMPTY = 9,   // +stage (3)
     B_SFULL = 12,   // +sub-tile
-    B_PFULL = 14,   // +sub-tile
-    B_ODONE = 16,   // +sub-tile
-    B_DRAIN = 18,
-    NUM_BARS = 19
+    B_PFULL = 14,   // +sub-tile: keys 0..63 of P; +2: keys 64..127
+    B_ODONE = 18,   // +sub-tile
+    B_DRAIN = 20,
+    NUM_BARS = 21
 };
 
 // key tiles each sub-tile of a CTA tile needs (0 for an empty sub-tile)
@@ -148,6 +153,7 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(B_SFULL + t), 1);
             mbar_init(bar(B_PFULL + t), 128);
+            mbar_init(bar(B_PFULL + 2 + t), 128);
             mbar_init(bar(B_ODONE + t), 1);
         }
         mbar_init(bar(B_DRAIN), 1);
@@ -265,7 +271,7 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             uint32_t p_par[2] = {0, 0};                              // parity of the next P
             uint32_t n_q = 0;
             // seen complete by a test in an MMA group
-            bool p_ready[2] = {false, false}, k_ready = false, v_ready = false;
+            bool p_ready[2] = {false, false}, p_rest = false, k_ready = false, v_ready = false;
             auto poll = [](bool &flag, uint32_t b, uint32_t parity) {
                 if (!flag) flag = mbar_test_wait(b, parity);
             };
@@ -299,13 +305,21 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 }
                 tc_commit(sfull[t]);
             };
-            auto pv = [&](int t, uint32_t accumulate, auto gap) {
+            // (the first half of P has been waited for)
+            auto pv = [&](int t, uint32_t accumulate, auto gap) -> bool {
 #pragma unroll
                 for (int kk = 0; kk < kTileKeys / 16; ++kk) {
+                    if (kk == 3) poll(p_rest, pfull[t] + 16, p_par[t]);
+                    if (kk == kTileKeys / 32) {
+                        if (!need(p_rest, pfull[t] + 16, p_par[t])) return false;
+                        tc_fence_after();
+                        p_par[t] ^= 1u;
+                    }
                     tc_mma_ts(tmem + col_o(t), tmem + col_s(t) + kk * 8, sdesc_advance(v_desc, kk * 2048), C::IDESC_PV,
                               kk > 0 ? 1u : accumulate);
                     gap(kk);
                 }
+                return true;
             };
             auto nothing = [](int) {};
             for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
@@ -331,12 +345,11 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 for (; j + 1 < min(n0, n1); ++j) {
                     if (!need(v_ready, v_bar, v_par) || !need(p_ready[0], pfull[0], p_par[0])) { ok = false; break; }
                     tc_fence_after();
-                    pv(0, j > 0 ? 1u : 0u, [&](int kk) {
+                    ok = pv(0, j > 0 ? 1u : 0u, [&](int kk) {
                         if (kk == 1 && k_release) tc_commit(k_release);
-                        if (kk == 3) p_par[0] ^= 1u;
                         if (kk == 5) poll(k_ready, k_bar, k_par);
                     });
-                    if (!need(k_ready, k_bar, k_par)) { ok = false; break; }
+                    if (!ok || !need(k_ready, k_bar, k_par)) { ok = false; break; }
                     tc_fence_after();
                     // overwrites S_0: issued after the PV that reads P_0
                     qk(0, [&](int kk) {
@@ -345,9 +358,8 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     if (!need(p_ready[1], pfull[1], p_par[1])) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t v_done = v_bar + kEmptyV;
-                    pv(1, j > 0 ? 1u : 0u, [&](int kk) {
-                        if (kk == 3) p_par[1] ^= 1u;
-                    });
+                    ok = pv(1, j > 0 ? 1u : 0u, nothing);
+                    if (!ok) break;
                     qk(1, [&](int kk) {
                         if (kk == 0) tc_commit(v_done);   // V tile j read by both PV
                         if (kk == 1) next_v();
@@ -370,9 +382,9 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         if (!ok || j >= nt) continue;
                         ok = need(p_ready[t], pfull[t], p_par[t]);
                         if (!ok) break;
-                        p_par[t] ^= 1u;
                         tc_fence_after();
-                        pv(t, j > 0 ? 1u : 0u, nothing);
+                        ok = pv(t, j > 0 ? 1u : 0u, nothing);
+                        if (!ok) break;
                         if (j + 1 < nt) {
                             if (!k_ready) ok = mbar_wait_spin(k_bar, k_par, &abort_flag);
                             if (!ok) break;
@@ -502,46 +514,51 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         sr[8 * b + e] = pack_f16x2(p0, p1);
                     }
                     l2 = fma_f32x2(add_f32x2(w[0], w[1]), f32x2(iv[b], iv[b]), l2);
+                    if (b == 3) {   // the first half of P, under which its PV can begin
+                        tmem_st32(t_row + col_s(t) + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+                        if (j >= 1 && __any_sync(0xffffffffu, need)) {
+                            // O_t holds the tiles before j (their PV completed before S_t(j) did)
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t orr[32];
+                                tmem_ld32(t_row + col_o(t) + c, orr);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
+                                tmem_st32(t_row + col_o(t) + c, orr);
+                            }
+                        }
+                        tmem_wait_st();
+                        // value rows past the end of the key range may hold anything
+                        // (unwritten slots, stale blocks, NaN): zero them so that
+                        // 0 * row stays 0 inside the MMA.  Each sub-tile that reads
+                        // the last V tile zeroes them before handing over its P, so
+                        // the PV after it sees zeros (both write the same zeros).
+                        const int valid_keys = tile.key_end - kt0;
+                        if (valid_keys < kTileKeys && j == sh.n_tiles - 1) {
+                            const int s = vs_stage;   // (landed: waited for above)
+                            if (row >= valid_keys) {
+#pragma unroll
+                                for (int h = 0; h < C::NH; ++h)
+#pragma unroll
+                                    for (int ch = 0; ch < 8; ++ch) {
+                                        const uint32_t a = v_s(s) + h * C::HALF + row * 128 + ch * 16;
+                                        asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
+                                    }
+                            }
+                            fence_proxy_async_smem();
+                        }
+                        tc_fence_before();
+                        mbar_arrive(bar(B_PFULL + t));
+                    }
                 }
                 float l0, l1;
                 f32x2_split(l2, l0, l1);
                 l += l0 + l1;
-                tmem_st32(t_row + col_s(t) + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
                 tmem_st32(t_row + col_s(t) + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-                if (j >= 1 && __any_sync(0xffffffffu, need)) {
-                    // O_t holds the tiles before j (their PV completed before S_t(j) did)
-#pragma unroll 1
-                    for (int c = 0; c < D; c += 32) {
-                        uint32_t orr[32];
-                        tmem_ld32(t_row + col_o(t) + c, orr);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) orr[e] = __float_as_uint(__uint_as_float(orr[e]) * alpha);
-                        tmem_st32(t_row + col_o(t) + c, orr);
-                    }
-                }
                 tmem_wait_st();
-                // value rows past the end of the key range may hold anything
-                // (unwritten slots, stale blocks, NaN): zero them so that
-                // 0 * row stays 0 inside the MMA.  Each sub-tile that reads
-                // the last V tile zeroes them before handing over its P, so
-                // the PV after it sees zeros (both write the same zeros).
-                const int valid_keys = tile.key_end - kt0;
-                if (valid_keys < kTileKeys && j == sh.n_tiles - 1) {
-                    const int s = vs_stage;   // (landed: waited for above)
-                    if (row >= valid_keys) {
-#pragma unroll
-                        for (int h = 0; h < C::NH; ++h)
-#pragma unroll
-                            for (int ch = 0; ch < 8; ++ch) {
-                                const uint32_t a = v_s(s) + h * C::HALF + row * 128 + ch * 16;
-                                asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a), "r"(0) : "memory");
-                            }
-                    }
-                    fence_proxy_async_smem();
-                }
                 tc_fence_before();
-                mbar_arrive(bar(B_PFULL + t));
+                mbar_arrive(bar(B_PFULL + 2 + t));
             }
             if (!ok) break;
             vbase += sh.n_tiles;
