@@ -101,6 +101,20 @@ __device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, vo
     }
 }
 
+// mbar_wait_spin by every lane of a warp, with one warp-wide (uniform) answer.
+__device__ __forceinline__ bool warp_wait_spin(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+#pragma unroll 1
+    for (int i = 0; i < 1024; ++i)
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+    const uint64_t start = global_timer();
+#pragma unroll 1
+    while (true) {
+        if (__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) return true;
+        if (__any_sync(0xffffffffu, (abort_flag != nullptr && *abort_flag) || global_timer() - start > kWaitLimitNs))
+            return false;
+    }
+}
+
 // mbar_wait by every lane of a warp, with one warp-wide answer: either all
 // lanes go on or all stop (keeps later warp-collective instructions legal).
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int *abort_flag) {
@@ -569,6 +583,39 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint
 __device__ __forceinline__ void tc_commit(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+
+// The three above for a warp that runs its issue loop whole, so that descriptors
+// and addresses stay in uniform registers, and issues from its leading lane.
+__device__ __forceinline__ void tc_mma_if(bool lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                          uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(lead))
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_mma_ts_if(bool lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(lead))
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_if(bool lead, uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(static_cast<uint32_t>(lead))
         : "memory");
 }
 

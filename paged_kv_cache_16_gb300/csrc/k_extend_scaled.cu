@@ -13,21 +13,25 @@
 // kernel as one 16-byte record, travel with the V stage: a softmax warp may wait
 // for that stage, which is not given back before its weights have been used.
 //
-// Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 213 us at
-// 2070 MHz, 1612 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
-// 248.  A step of 128 keys has 2048 cycles of MMAs and takes ~3050: what the MMA
-// thread does between two MMAs leaves the pipe idle (ring indices by division and
-// all commits at the groups' ends: 8% more), the rest is the chain S -> softmax -> P
-// of a sub-tile (~1500 cycles), which its own PV and QK^T follow; P handed over in
-// halves, so that PV begins under the second half's exponentials, takes 3% off.
-// Measured and not kept, as parts of the time then: weights through shared memory,
-// QK^T a step ahead, +23% (every operand from shared memory fills its bandwidth);
-// one S buffer for both sub-tiles and QK^T a step ahead, +39% with one MMA thread,
-// +11% with one for QK^T and one for PV; an MMA thread per sub-tile, +25%, taking
-// turns at the pipe +2%; two threads per row +15%; weights against the old
-// reference beside the maximum that checks it, S read again where a row needs a
-// new one, +27% (registers); the blocks' factors read from shared memory where
-// they are used instead of held, +2% (+6% with P in halves).
+// Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 203 us at
+// 2070 MHz, 1692 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
+// 244.  A step of 128 keys has 2048 cycles of MMAs (and fills the shared-memory
+// bandwidth for as long) and takes ~2800: what the MMA warp does between two MMAs,
+// and the chain S -> softmax -> P of a sub-tile (~1500 cycles), which its own PV and
+// QK^T follow.  P is handed over in halves, so that PV begins under the second
+// half's exponentials (3%), by one arrival per warp (1.5%).  Between two tiles go
+// ~3 steps' time: the last softmax, the epilogue and the first QK^T in a row.
+// Measured and not kept, as parts of the time then: ring indices by division and
+// all commits at the groups' ends +8%; weights through shared memory, QK^T a step
+// ahead, +23% (every operand from shared memory fills its bandwidth); one S buffer
+// for both sub-tiles and QK^T a step ahead, +39% with one MMA thread, +11% with one
+// for QK^T and one for PV; an MMA thread per sub-tile, +25%, taking turns at the
+// pipe +2%; two threads per row +15%; the first half's weights against the old
+// reference, checked by their sum, beside the second half's maximum, S read again
+// where a row needs a new one, +3%; the blocks' factors read from shared memory
+// where they are used instead of held, +2%; stages given back by a softmax warp, or
+// tile descriptions in shared memory: no change; three K and two V stages: no
+// change.
 #include "dev.cuh"
 
 namespace pa {
@@ -133,7 +137,7 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     const int tile_begin = p.cta_tile_begin[blockIdx.x];
     const int tile_end = p.cta_tile_begin[blockIdx.x + 1];
     if (tile_begin >= tile_end) return;
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (uniform to the compiler)
     const int lane = threadIdx.x & 31;
     const int G = p.group;
     const int tpt = kTileRows / G;                    // tokens per 128-row sub-tile
@@ -152,8 +156,8 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(B_SFULL + t), 1);
-            mbar_init(bar(B_PFULL + t), 128);
-            mbar_init(bar(B_PFULL + 2 + t), 128);
+            mbar_init(bar(B_PFULL + t), 4);       // a warp each
+            mbar_init(bar(B_PFULL + 2 + t), 4);
             mbar_init(bar(B_ODONE + t), 1);
         }
         mbar_init(bar(B_DRAIN), 1);
@@ -252,165 +256,164 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer --
-        if (lane == 0) {
-            bool ok = true;
-            // The pipe takes the next MMA only when the one before is nearly
-            // done, so whatever this thread does between two MMAs beyond ~60
-            // cycles leaves it idle: descriptors and barrier addresses are kept as
-            // running values, and what is left (barrier tests, stage releases,
-            // the next step's values) is spread over the gaps of the MMA groups.
-            const uint64_t q_desc[2] = {sdesc_sw128(q_s(0), 16, 1024), sdesc_sw128(q_s(1), 16, 1024)};
-            const uint64_t k_desc0 = sdesc_sw128(k_s(0), 16, 1024);
-            const uint64_t v_desc0 = sdesc_sw128(v_s(0), C::HALF, 1024);
-            const uint32_t sfull[2] = {bar(B_SFULL), bar(B_SFULL + 1)}, pfull[2] = {bar(B_PFULL), bar(B_PFULL + 1)};
-            const uint32_t k_bar0 = bar(B_KFULL), v_bar0 = bar(B_VFULL);
-            constexpr uint32_t kEmptyK = 8u * (B_KEMPTY - B_KFULL), kEmptyV = 8u * (B_VEMPTY - B_VFULL);
-            uint32_t k_slot = 0, k_par = 0, v_slot = 0, v_par = 0;   // next K and V tile: ring slot, phase parity
-            uint32_t k_bar = k_bar0, v_bar = v_bar0;                 // their full barriers
-            uint64_t k_desc = k_desc0, v_desc = v_desc0;
-            uint32_t p_par[2] = {0, 0};                              // parity of the next P
-            uint32_t n_q = 0;
-            // seen complete by a test in an MMA group
-            bool p_ready[2] = {false, false}, p_rest = false, k_ready = false, v_ready = false;
-            auto poll = [](bool &flag, uint32_t b, uint32_t parity) {
-                if (!flag) flag = mbar_test_wait(b, parity);
-            };
-            auto need = [&](bool &flag, uint32_t b, uint32_t parity) -> bool {
-                if (!flag && !mbar_wait_spin(b, parity, &abort_flag)) return false;
-                flag = false;
-                return true;
-            };
-            auto next_k = [&] {
-                const bool wrap = k_slot + 1 == C::NSK;
-                k_slot = wrap ? 0 : k_slot + 1;
-                k_par ^= wrap ? 1u : 0u;
-                k_bar = k_bar0 + 8u * k_slot;
-                k_desc = sdesc_advance(k_desc0, k_slot * C::KVB);
-            };
-            auto next_v = [&] {
-                const bool wrap = v_slot + 1 == C::NSV;
-                v_slot = wrap ? 0 : v_slot + 1;
-                v_par ^= wrap ? 1u : 0u;
-                v_bar = v_bar0 + 8u * v_slot;
-                v_desc = sdesc_advance(v_desc0, v_slot * C::KVB);
-            };
-            // MMA groups; gap(kk) runs behind MMA kk
-            auto qk = [&](int t, auto gap) {
+        bool ok = true;
+        const bool lead = lane == 0;
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        // The warp runs the loop whole, on uniform conditions, and its leading
+        // lane issues: descriptors stay in uniform registers (one lane alone
+        // pays moves to them per MMA, and 2% more time).  The pipe takes the
+        // next MMA only when the one before is nearly done, so whatever happens
+        // between two MMAs beyond ~60 cycles leaves it idle: descriptors and
+        // barrier addresses are running values, and barrier tests, a stage's
+        // release and the next V tile's values sit in the gaps of the groups.
+        const uint64_t q_desc[2] = {sdesc_sw128(q_s(0), 16, 1024), sdesc_sw128(q_s(1), 16, 1024)};
+        const uint64_t k_desc0 = sdesc_sw128(k_s(0), 16, 1024);
+        const uint64_t v_desc0 = sdesc_sw128(v_s(0), C::HALF, 1024);
+        const uint32_t sfull[2] = {bar(B_SFULL), bar(B_SFULL + 1)}, pfull[2] = {bar(B_PFULL), bar(B_PFULL + 1)};
+        const uint32_t k_bar0 = bar(B_KFULL), v_bar0 = bar(B_VFULL);
+        constexpr uint32_t kEmptyK = 8u * (B_KEMPTY - B_KFULL), kEmptyV = 8u * (B_VEMPTY - B_VFULL);
+        uint32_t k_slot = 0, k_par = 0, v_slot = 0, v_par = 0;   // next K and V tile: ring slot, phase parity
+        uint32_t k_bar = k_bar0, v_bar = v_bar0;                 // their full barriers
+        uint64_t k_desc = k_desc0, v_desc = v_desc0;
+        uint32_t p_par[2] = {0, 0};                              // parity of the next P
+        uint32_t n_q = 0;
+        // seen complete by a test in an MMA group
+        bool p_ready[2] = {false, false}, p_rest = false, k_ready = false, v_ready = false;
+        auto poll = [](bool &flag, uint32_t b, uint32_t parity) {
+            if (!flag) flag = __all_sync(0xffffffffu, mbar_test_wait(b, parity));
+        };
+        auto need = [&](bool &flag, uint32_t b, uint32_t parity) -> bool {
+            if (!flag && !warp_wait_spin(b, parity, &abort_flag)) return false;
+            flag = false;
+            return true;
+        };
+        auto next_k = [&] {
+            const bool wrap = k_slot + 1 == C::NSK;
+            k_slot = wrap ? 0 : k_slot + 1;
+            k_par ^= wrap ? 1u : 0u;
+            k_bar = k_bar0 + 8u * k_slot;
+            k_desc = sdesc_advance(k_desc0, k_slot * C::KVB);
+        };
+        auto next_v = [&] {
+            const bool wrap = v_slot + 1 == C::NSV;
+            v_slot = wrap ? 0 : v_slot + 1;
+            v_par ^= wrap ? 1u : 0u;
+            v_bar = v_bar0 + 8u * v_slot;
+            v_desc = sdesc_advance(v_desc0, v_slot * C::KVB);
+        };
+        // MMA groups; gap(kk) runs behind MMA kk
+        auto qk = [&](int t, auto gap) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * C::HALF + (kk % 4) * 32;
-                    tc_mma(tmem + col_s(t), sdesc_advance(q_desc[t], off), sdesc_advance(k_desc, off), C::IDESC_QK,
-                           kk > 0 ? 1u : 0u);
-                    gap(kk);
-                }
-                tc_commit(sfull[t]);
-            };
-            // (the first half of P has been waited for)
-            auto pv = [&](int t, uint32_t accumulate, auto gap) -> bool {
+            for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk / 4) * C::HALF + (kk % 4) * 32;
+                tc_mma_if(lead, tm + col_s(t), sdesc_advance(q_desc[t], off), sdesc_advance(k_desc, off),
+                          C::IDESC_QK, kk > 0 ? 1u : 0u);
+                gap(kk);
+            }
+            tc_commit_if(lead, sfull[t]);
+        };
+        // (the first half of P has been waited for)
+        auto pv = [&](int t, uint32_t accumulate, auto gap) -> bool {
 #pragma unroll
-                for (int kk = 0; kk < kTileKeys / 16; ++kk) {
-                    if (kk == 3) poll(p_rest, pfull[t] + 16, p_par[t]);
-                    if (kk == kTileKeys / 32) {
-                        if (!need(p_rest, pfull[t] + 16, p_par[t])) return false;
-                        tc_fence_after();
-                        p_par[t] ^= 1u;
-                    }
-                    tc_mma_ts(tmem + col_o(t), tmem + col_s(t) + kk * 8, sdesc_advance(v_desc, kk * 2048), C::IDESC_PV,
-                              kk > 0 ? 1u : accumulate);
-                    gap(kk);
+            for (int kk = 0; kk < kTileKeys / 16; ++kk) {
+                if (kk == 3) poll(p_rest, pfull[t] + 16, p_par[t]);
+                if (kk == kTileKeys / 32) {
+                    if (!need(p_rest, pfull[t] + 16, p_par[t])) return false;
+                    tc_fence_after();
+                    p_par[t] ^= 1u;
                 }
-                return true;
-            };
-            auto nothing = [](int) {};
-            for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
-                const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-                const TileShape sh = tile_shape(tile, tpt);
-                ok = mbar_wait_spin(bar(B_QFULL), n_q & 1, &abort_flag);
-                ++n_q;
-                if (!ok || sh.n_tiles == 0) {
-                    if (ok) tc_commit(bar(B_QEMPTY));
-                    continue;
-                }
-                const int n0 = sh.n_sub[0], n1 = sh.n_sub[1], n = sh.n_tiles;
-                if (!need(k_ready, k_bar, k_par)) { ok = false; break; }
+                tc_mma_ts_if(lead, tm + col_o(t), tm + col_s(t) + kk * 8, sdesc_advance(v_desc, kk * 2048),
+                             C::IDESC_PV, kk > 0 ? 1u : accumulate);
+                gap(kk);
+            }
+            return true;
+        };
+        auto nothing = [](int) {};
+        const int ti_end = __shfl_sync(0xffffffffu, tile_end, 0);
+        for (int ti = __shfl_sync(0xffffffffu, tile_begin, 0); ti < ti_end && ok; ++ti) {
+            const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
+            const TileShape sh = tile_shape(tile, tpt);
+            const int n0 = __shfl_sync(0xffffffffu, sh.n_sub[0], 0), n1 = __shfl_sync(0xffffffffu, sh.n_sub[1], 0);
+            const int n = max(n0, n1), n_both = min(n0, n1);
+            ok = warp_wait_spin(bar(B_QFULL), n_q & 1, &abort_flag);
+            ++n_q;
+            if (!ok || n == 0) {
+                if (ok) tc_commit_if(lead, bar(B_QEMPTY));
+                continue;
+            }
+            if (!need(k_ready, k_bar, k_par)) { ok = false; break; }
+            tc_fence_after();
+            if (n0 > 0) qk(0, nothing);
+            if (n1 > 0) qk(1, nothing);
+            tc_commit_if(lead, k_bar + kEmptyK);   // K tile 0 read by both QK^T
+            if (n == 1) tc_commit_if(lead, bar(B_QEMPTY));
+            next_k();
+            int j = 0;
+            // steps whose two sub-tiles both go on: PV_0(j) QK_0(j+1) PV_1(j)
+            // QK_1(j+1)
+            for (; j + 1 < n_both; ++j) {
+                if (!need(v_ready, v_bar, v_par) || !need(p_ready[0], pfull[0], p_par[0])) { ok = false; break; }
                 tc_fence_after();
-                if (n0 > 0) qk(0, nothing);
-                if (n1 > 0) qk(1, nothing);
-                tc_commit(k_bar + kEmptyK);   // K tile 0 read by both QK^T
-                if (n == 1) tc_commit(bar(B_QEMPTY));
+                ok = pv(0, j > 0 ? 1u : 0u, [&](int kk) {
+                    if (kk == 5) poll(k_ready, k_bar, k_par);
+                });
+                if (!ok || !need(k_ready, k_bar, k_par)) { ok = false; break; }
+                tc_fence_after();
+                // overwrites S_0: issued after the PV that reads P_0
+                qk(0, [&](int kk) {
+                    if (kk == D / 16 - 3) poll(p_ready[1], pfull[1], p_par[1]);
+                });
+                if (!need(p_ready[1], pfull[1], p_par[1])) { ok = false; break; }
+                tc_fence_after();
+                ok = pv(1, j > 0 ? 1u : 0u, nothing);
+                if (!ok) break;
+                qk(1, [&](int kk) {
+                    if (kk == 0) tc_commit_if(lead, v_bar + kEmptyV);   // V tile j read by both PV
+                    if (kk == 1) next_v();
+                    if (kk == 2) poll(v_ready, v_bar, v_par);
+                    if (kk == D / 16 - 2) poll(p_ready[0], pfull[0], p_par[0]);
+                });
+                tc_commit_if(lead, k_bar + kEmptyK);   // K tile j+1 read by both QK^T
                 next_k();
-                int j = 0;
-                // steps whose two sub-tiles both go on: PV_0(j) QK_0(j+1) PV_1(j) QK_1(j+1)
-                uint32_t k_release = 0;   // K stage to give back in the next gap
-                for (; j + 1 < min(n0, n1); ++j) {
-                    if (!need(v_ready, v_bar, v_par) || !need(p_ready[0], pfull[0], p_par[0])) { ok = false; break; }
-                    tc_fence_after();
-                    ok = pv(0, j > 0 ? 1u : 0u, [&](int kk) {
-                        if (kk == 1 && k_release) tc_commit(k_release);
-                        if (kk == 5) poll(k_ready, k_bar, k_par);
-                    });
-                    if (!ok || !need(k_ready, k_bar, k_par)) { ok = false; break; }
-                    tc_fence_after();
-                    // overwrites S_0: issued after the PV that reads P_0
-                    qk(0, [&](int kk) {
-                        if (kk == D / 16 - 3) poll(p_ready[1], pfull[1], p_par[1]);
-                    });
-                    if (!need(p_ready[1], pfull[1], p_par[1])) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t v_done = v_bar + kEmptyV;
-                    ok = pv(1, j > 0 ? 1u : 0u, nothing);
-                    if (!ok) break;
-                    qk(1, [&](int kk) {
-                        if (kk == 0) tc_commit(v_done);   // V tile j read by both PV
-                        if (kk == 1) next_v();
-                        if (kk == 2) poll(v_ready, v_bar, v_par);
-                        if (kk == D / 16 - 2) poll(p_ready[0], pfull[0], p_par[0]);
-                    });
-                    k_release = k_bar + kEmptyK;   // K tile j+1 read by both QK^T
-                    next_k();
-                }
-                if (ok && k_release) {
-                    tc_commit(k_release);
-                    if (j + 1 == n) tc_commit(bar(B_QEMPTY));
-                }
-                // the last steps, of one sub-tile or without a QK^T
-                for (; j < n && ok; ++j) {
-                    ok = need(v_ready, v_bar, v_par);
+            }
+            if (ok && j > 0 && j + 1 == n) tc_commit_if(lead, bar(B_QEMPTY));
+            // the last steps, of one sub-tile or without a QK^T
+            for (; j < n && ok; ++j) {
+                ok = need(v_ready, v_bar, v_par);
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        const int nt = t ? n1 : n0;
-                        if (!ok || j >= nt) continue;
-                        ok = need(p_ready[t], pfull[t], p_par[t]);
-                        if (!ok) break;
-                        tc_fence_after();
-                        ok = pv(t, j > 0 ? 1u : 0u, nothing);
-                        if (!ok) break;
-                        if (j + 1 < nt) {
-                            if (!k_ready) ok = mbar_wait_spin(k_bar, k_par, &abort_flag);
-                            if (!ok) break;
-                            k_ready = true;
-                            tc_fence_after();
-                            qk(t, nothing);
-                        } else {
-                            tc_commit(bar(B_ODONE + t));
-                        }
-                    }
+                for (int t = 0; t < 2; ++t) {
+                    const int nt = t ? n1 : n0;
+                    if (!ok || j >= nt) continue;
+                    ok = need(p_ready[t], pfull[t], p_par[t]);
                     if (!ok) break;
-                    tc_commit(v_bar + kEmptyV);
-                    next_v();
-                    if (j + 1 < n) {
-                        tc_commit(k_bar + kEmptyK);
-                        next_k();
-                        k_ready = false;
-                        if (j + 2 == n) tc_commit(bar(B_QEMPTY));
+                    tc_fence_after();
+                    ok = pv(t, j > 0 ? 1u : 0u, nothing);
+                    if (!ok) break;
+                    if (j + 1 < nt) {
+                        if (!k_ready) ok = warp_wait_spin(k_bar, k_par, &abort_flag);
+                        if (!ok) break;
+                        k_ready = true;
+                        tc_fence_after();
+                        qk(t, nothing);
+                    } else {
+                        tc_commit_if(lead, bar(B_ODONE + t));
                     }
+                }
+                if (!ok) break;
+                tc_commit_if(lead, v_bar + kEmptyV);
+                next_v();
+                if (j + 1 < n) {
+                    tc_commit_if(lead, k_bar + kEmptyK);
+                    next_k();
+                    k_ready = false;
+                    if (j + 2 == n) tc_commit_if(lead, bar(B_QEMPTY));
                 }
             }
-            if (!ok) raise_abort(&abort_flag, p.err, kErrTimeout);
-            // every MMA of this CTA must finish before tensor memory is released
-            tc_commit(bar(B_DRAIN));
-            if (!mbar_wait(bar(B_DRAIN), 0, nullptr)) atomicOr(p.err, kErrTimeout);
         }
+        if (!ok && lead) raise_abort(&abort_flag, p.err, kErrTimeout);
+        // every MMA of this CTA must finish before tensor memory is released
+        tc_commit_if(lead, bar(B_DRAIN));
+        if (!mbar_wait(bar(B_DRAIN), 0, nullptr) && lead) atomicOr(p.err, kErrTimeout);
         __syncwarp();
       }
     } else {
@@ -549,7 +552,8 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                             fence_proxy_async_smem();
                         }
                         tc_fence_before();
-                        mbar_arrive(bar(B_PFULL + t));
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(B_PFULL + t));
                     }
                 }
                 float l0, l1;
@@ -558,7 +562,8 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 tmem_st32(t_row + col_s(t) + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(bar(B_PFULL + 2 + t));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_PFULL + 2 + t));
             }
             if (!ok) break;
             vbase += sh.n_tiles;
@@ -574,24 +579,52 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (tile.part >= 0 && tok_valid)
                 slot = static_cast<int64_t>(p.part_offset[tok * p.n_groups + tile.kv_head / p.heads_per_group]) +
                        tile.part;
+            if (tile.part < 0) {
+                // Four neighbouring lanes hold four rows; their 32-byte pieces are
+                // exchanged so that a store writes 128 consecutive bytes of 8 rows
+                // (a piece of 32 rows each: 80 cycles a store, 5000 an epilogue,
+                // with the MMA thread's requests queued behind them).
+                const int64_t mine = tok_valid ? (static_cast<int64_t>(tok) * p.num_heads_q + h) * D : -1;
+                int64_t at[4];   // rows of the four lanes
+#pragma unroll
+                for (int s = 0; s < 4; ++s) at[s] = __shfl_sync(0xffffffffu, mine, (lane & ~3) + s);
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t orr[32];
-                tmem_ld32(t_row + col_o(t) + c, orr);
-                tmem_wait_ld();
-                if (!tok_valid) continue;
-                if (tile.part < 0) {
-                    uint16_t *dst = p.out + (static_cast<int64_t>(tok) * p.num_heads_q + h) * D + c;
+                for (int c = 0; c < D; c += 64) {
+                    uint32_t orr[64], w[32];
+                    tmem_ld32(t_row + col_o(t) + c, *reinterpret_cast<uint32_t(*)[32]>(&orr[0]));
+                    tmem_ld32(t_row + col_o(t) + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&orr[32]));
+                    tmem_wait_ld();
 #pragma unroll
-                    for (int q8 = 0; q8 < 2; ++q8) {
-                        uint32_t w[8];
+                    for (int e = 0; e < 32; ++e)
+                        w[e] = pack_bf16x2(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            w[e] = pack_bf16x2(__uint_as_float(orr[q8 * 16 + 2 * e]) * inv,
-                                               __uint_as_float(orr[q8 * 16 + 2 * e + 1]) * inv);
-                        st_global_v8(dst + q8 * 16, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+                    for (int bit = 1; bit <= 2; bit *= 2) {
+                        const bool up = lane & bit;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (k & bit) continue;   // pieces k and k + bit
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                uint32_t &lo = w[8 * k + e], &hi = w[8 * (k + bit) + e];
+                                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? lo : hi, bit);
+                                if (up) lo = got;
+                                else hi = got;
+                            }
+                        }
                     }
-                } else {
+#pragma unroll
+                    for (int s = 0; s < 4; ++s)
+                        if (at[s] >= 0)
+                            st_global_v8(p.out + at[s] + c + 16 * (lane & 3), w[8 * s], w[8 * s + 1], w[8 * s + 2],
+                                         w[8 * s + 3], w[8 * s + 4], w[8 * s + 5], w[8 * s + 6], w[8 * s + 7]);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t orr[32];
+                    tmem_ld32(t_row + col_o(t) + c, orr);
+                    tmem_wait_ld();
+                    if (!tok_valid) continue;
                     float *dst = p.o_part + (slot * p.num_heads_q + h) * D + c;
 #pragma unroll
                     for (int q8 = 0; q8 < 4; ++q8)
