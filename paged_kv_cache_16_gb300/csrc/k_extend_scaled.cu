@@ -15,23 +15,24 @@
 //
 // Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 203 us at
 // 2070 MHz, 1692 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
-// 244.  A step of 128 keys has 2048 cycles of MMAs (and fills the shared-memory
-// bandwidth for as long) and takes ~2800: what the MMA warp does between two MMAs,
-// and the chain S -> softmax -> P of a sub-tile (~1500 cycles), which its own PV and
-// QK^T follow.  P is handed over in halves, so that PV begins under the second
-// half's exponentials (3%), by one arrival per warp (1.5%).  Between two tiles go
-// ~3 steps' time: the last softmax, the epilogue and the first QK^T in a row.
-// Measured and not kept, as parts of the time then: ring indices by division and
-// all commits at the groups' ends +8%; weights through shared memory, QK^T a step
-// ahead, +23% (every operand from shared memory fills its bandwidth); one S buffer
-// for both sub-tiles and QK^T a step ahead, +39% with one MMA thread, +11% with one
-// for QK^T and one for PV; an MMA thread per sub-tile, +25%, taking turns at the
-// pipe +2%; two threads per row +15%; the first half's weights against the old
-// reference, checked by their sum, beside the second half's maximum, S read again
-// where a row needs a new one, +3%; the blocks' factors read from shared memory
-// where they are used instead of held, +2%; stages given back by a softmax warp, or
-// tile descriptions in shared memory: no change; three K and two V stages: no
-// change.
+// 244.  A step of 128 keys has 2048 cycles of MMAs and takes ~2800 (tensor pipe
+// active 68%, issue 43%): what the MMA warp does between two MMAs, and the chain
+// S -> softmax -> P of a sub-tile (~1500 cycles), which its own PV and QK^T follow.
+// P is handed over in halves, so that PV begins under the second half's
+// exponentials (3%; after a quarter or three quarters 1% more than that), by one
+// arrival per warp (1.5%).  Between two tiles go ~3 steps' time: the last softmax,
+// the epilogue and the first QK^T in a row.  Measured and not kept, as parts of the
+// time then: ring indices by division and all commits at the groups' ends +8%;
+// weights through shared memory, QK^T a step ahead, +23% (every operand from shared
+// memory fills its bandwidth); one S buffer for both sub-tiles and QK^T a step
+// ahead, +39% with one MMA thread, +11% with one for QK^T and one for PV; an MMA
+// thread per sub-tile, +25%, taking turns at the pipe +2%; two threads per row +15%;
+// the first half's weights against the old reference, checked by their sum, beside
+// the second half's maximum, S read again where a row needs a new one, +3%; the
+// blocks' factors read from shared memory where they are used instead of held, +2%;
+// the next tile's first QK^T in a tile's last step +2%, one loop body for full and
+// last steps +23%; stages given back by a softmax warp, tile descriptions in shared
+// memory, three K and two V stages: no change.
 #include "dev.cuh"
 
 namespace pa {
