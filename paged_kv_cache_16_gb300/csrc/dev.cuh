@@ -163,6 +163,11 @@ __device__ __forceinline__ void tma_load_3d_hint(uint32_t dst, const CUtensorMap
         : "memory");
 }
 
+// Asks `bytes` bytes of global memory into L2 (address and size multiples of 16).
+__device__ __forceinline__ void bulk_prefetch_l2(const void *src, int bytes) {
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(__cvta_generic_to_global(src)), "r"(bytes) : "memory");
+}
+
 // Contiguous bulk load (both addresses 16-byte aligned, bytes a multiple of
 // 16) into shared memory, completing on `bar`.
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {

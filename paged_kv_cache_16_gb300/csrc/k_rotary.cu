@@ -181,9 +181,12 @@ __device__ __forceinline__ void rotate_rows(const float *tab, const RopeParams &
     }
 }
 
-// Bound by HBM (8192 tokens x 40 heads of 128: 28.6 us, 5.9 TB/s; 43.3 us with
+// Bound by HBM (8192 tokens x 40 heads of 128: 26.1 us, 6.4 TB/s; 43.3 us with
 // cos and sin read from shared memory per row, 8-byte pieces and one row of a thread
-// in flight) and by the launch for a decode step (64 tokens: 2.2 us).
+// in flight) and by the launch for a decode step (64 tokens: 2.2 us).  A CTA's rows
+// are asked into L2 before its table of cos and sin is made, from 1 MB of rows on
+// (28.7 us without; 512 tokens 3.4 and 4.0, 128 tokens 2.8 and 2.9, 64 tokens 2.3 and
+// 2.2; 1021 tokens x 7 heads of 64 2.0 and 1.8).
 template <int W>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RopeParams rope, const RotaryParams p) {
     extern __shared__ float4 smem4[];
@@ -192,6 +195,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
     grid_dep_wait();
     const int t0 = blockIdx.x << p.log_tokens, h0 = blockIdx.y * p.heads_per_cta;
     const int n = min(1 << p.log_tokens, p.num_tokens - t0), nh = min(p.heads_per_cta, p.num_heads - h0);
+    if (W == 8 && p.prefetch && static_cast<int>(threadIdx.x) < n)   // (16-byte pieces: aligned rows)
+        bulk_prefetch_l2(p.x + (t0 + static_cast<int>(threadIdx.x)) * p.x_stride + h0 * p.head_dim, nh * p.head_dim * 2);
     fill_table(tab, rope, n, [&](int j) { return __ldg(p.positions + t0 + j); });
     __syncthreads();
     rotate_rows<W, W == 8 ? 5 : 8>(tab, rope, p.x + t0 * p.x_stride + h0 * p.head_dim, p.x_stride,
@@ -544,16 +549,19 @@ cudaError_t launch_rotary(const RopeParams &rope, const RotaryParams &p0, cudaSt
     RotaryParams p = p0;
     if (p.num_tokens <= 0) return cudaSuccess;
     p.heads_per_cta = p.num_heads < 40 ? p.num_heads : 40;
-    // tokens of a CTA: as many as give its threads up to 10 units each, while
-    // there is a CTA for every SM and a thread for every unit of a row
+    // tokens of a CTA: as many as give its threads up to 5 units each, one batch of
+    // loads (10 units: 4096 tokens x 40 heads 15.4 us instead of 14.5, 8192 tokens
+    // the same), while there is a CTA for every SM and a thread for every unit of a
+    // row
     const bool wide = wide_units(rope, p.head_dim);
     const int upr = p.head_dim / (wide ? 16 : 8);
     p.log_tokens = 0;
-    while (p.log_tokens < 4 && (p.heads_per_cta * upr << (p.log_tokens + 1)) <= 10 * kThreads &&
+    while (p.log_tokens < 4 && (p.heads_per_cta * upr << (p.log_tokens + 1)) <= 5 * kThreads &&
            p.num_tokens >> (p.log_tokens + 1) >= 152 && kThreads >> (p.log_tokens + 1) >= upr)
         ++p.log_tokens;
     const dim3 grid((p.num_tokens + (1 << p.log_tokens) - 1) >> p.log_tokens,
                     (p.num_heads + p.heads_per_cta - 1) / p.heads_per_cta);
+    p.prefetch = static_cast<int64_t>(p.num_tokens) * p.num_heads * p.head_dim >= 1 << 19;
     const size_t smem = sizeof(float) * (rope.rotary_dim << p.log_tokens);
     return wide ? launch_pdl(rotary_kernel<8>, grid, dim3(kThreads), smem, stream, rope, p)
                 : launch_pdl(rotary_kernel<4>, grid, dim3(kThreads), smem, stream, rope, p);

@@ -272,6 +272,7 @@ struct RotaryParams {
     int64_t x_stride, out_stride;
     int32_t num_tokens, num_heads, head_dim;
     int32_t log_tokens, heads_per_cta;   // a CTA's tokens (log2) and heads
+    bool prefetch;                       // ask a CTA's rows into L2 first
 };
 
 // Element types of the cache an append writes.
