@@ -375,7 +375,8 @@ int split_sms(const StepModel &m, int num_sms, int max_tile_ctas, double *t_out)
 
 // Assigns tiles (steps in descending order) to CTAs so that none gets more than
 // cap steps, each tile to the fullest CTA that it fits; false if one fits nowhere.
-bool pack_tiles(const std::vector<std::pair<int64_t, int32_t>> &tiles, int ctas, int cap, std::vector<int32_t> &cta_of) {
+bool pack_tiles(const std::vector<std::pair<int64_t, int32_t>> &tiles, int ctas, int cap,
+                std::vector<int32_t> &cta_of) {
     // CTAs by load: a list per load, and a bit per load that some CTA has
     std::vector<int32_t> first(static_cast<size_t>(cap) + 1, -1), next(static_cast<size_t>(ctas));
     std::vector<uint64_t> any(static_cast<size_t>(cap) / 64 + 1, 0);
@@ -406,12 +407,14 @@ bool pack_tiles(const std::vector<std::pair<int64_t, int32_t>> &tiles, int ctas,
 // mean where a CTA gets three or four tiles of different lengths, and the grid
 // waits for its last CTA: where it is off by more than 1/32, the smallest load that
 // packing reaches, by halving (to 1/128).  Two chunks of 2048 tokens over 2304 and
-// 4864 (512 tiles of 19 to 55 steps, mean 126): 138 steps before, 130 after, the
+// 4864 (512 tiles of 21 to 56 steps, mean 130): 142 steps before, 133 after, the
 // tiles 235 -> 221 us on block-scaled codes and 261 -> 249 us on E4M3 with one scale,
-// for 12 us of planning.
-void balance_tiles(const std::vector<std::pair<int64_t, int32_t>> &tiles, int ctas, int64_t most, double total,
+// for 10 us of planning.
+void balance_tiles(const std::vector<std::pair<int64_t, int32_t>> &tiles, int ctas, int64_t most,
                    std::vector<int32_t> &cta_of) {
-    const int64_t mean = static_cast<int64_t>(std::ceil(total / ctas));
+    int64_t total = 0;
+    for (const auto &t : tiles) total += t.first;
+    const int64_t mean = (total + ctas - 1) / ctas;
     if (most - mean <= mean / 32 || most > kMaxPackedSteps) return;
     std::vector<int32_t> packed(cta_of.size());
     int64_t lo = mean;
@@ -717,7 +720,7 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
                 heap[i] = v;
             }
             cost.swap(by_cost);
-            balance_tiles(cost, static_cast<int>(tile_work_ctas), most, model.tile_units, cta_of);
+            balance_tiles(cost, static_cast<int>(tile_work_ctas), most, cta_of);
             for (int32_t c : cta_of) ++P->cta_tile_begin[static_cast<size_t>(c) + 1];
             for (size_t c = 1; c < P->cta_tile_begin.size(); ++c) P->cta_tile_begin[c] += P->cta_tile_begin[c - 1];
             P->cta_tiles.resize(cost.size());
