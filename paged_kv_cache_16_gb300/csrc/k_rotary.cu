@@ -27,18 +27,37 @@ __device__ __forceinline__ void cos_sin(uint64_t step, int32_t pos, float mag, f
 }
 
 // cos and sin of `n` tokens: tab[j * rd + i] = cos, tab[j * rd + rd / 2 + i] = sin
-// of pair i at the position of token j.
-template <typename PosOf>
-__device__ __forceinline__ void fill_table(float *tab, const RopeParams &rope, int n, PosOf pos_of) {
-    const int half = rope.rotary_dim / 2;
-    for (int e = threadIdx.x; e < n * half; e += kThreads) {
-        const int j = e / half, i = e - j * half;
-        float c, s;
-        cos_sin(rope.step[i], pos_of(j), rope.mag, c, s);
-        tab[j * rope.rotary_dim + i] = c;
-        tab[j * rope.rotary_dim + half + i] = s;
+// of pair i at the position of token j.  A thread keeps one pair, whose step it
+// reads once, through the generic address of the kernel's argument: 32 lanes in
+// one access, where constant loads of 32 addresses go one by one (a constant load
+// per entry: 64 tokens 2.2 us instead of 1.8, 8192 tokens x 8 heads 10.4 instead of
+// 7.6, an append of two chunks 19.6 instead of 18.5; once per thread, 2.0 and 18.4,
+// but a decode step's append 3.6 instead of 3.5).
+struct TableMaker {
+    int i, j0, tokens;   // pair, first token, tokens a pass (0: no part of the table)
+    uint64_t step;
+    __device__ __forceinline__ TableMaker(const RopeParams &rope, int n) : i(0), j0(0), tokens(0), step(0) {
+        const int half = rope.rotary_dim / 2;
+        if (half == 0) return;
+        j0 = static_cast<int>(threadIdx.x) / half;
+        i = static_cast<int>(threadIdx.x) - j0 * half;
+        tokens = kThreads / half;
+        const uint64_t *steps;   // (opaque, or the load would be a constant one)
+        asm("mov.u64 %0, %1;" : "=l"(steps) : "l"(rope.step));
+        if (j0 < min(tokens, n)) step = steps[i];
     }
-}
+    template <typename PosOf>
+    __device__ __forceinline__ void fill(float *tab, const RopeParams &rope, int n, PosOf pos_of) const {
+        if (j0 >= tokens) return;
+        float *at = tab + j0 * rope.rotary_dim + i;
+        for (int j = j0; j < n; j += tokens, at += tokens * rope.rotary_dim) {
+            float c, s;
+            cos_sin(step, pos_of(j), rope.mag, c, s);
+            at[0] = c;
+            at[rope.rotary_dim / 2] = s;
+        }
+    }
+};
 
 // A unit is 2 W elements of a row that one thread handles, as two groups of W
 // (8 or 16 bytes) at element offsets a and b.  Half layout: dims W u.. and their
@@ -181,23 +200,24 @@ __device__ __forceinline__ void rotate_rows(const float *tab, const RopeParams &
     }
 }
 
-// Bound by HBM (8192 tokens x 40 heads of 128: 26.1 us, 6.4 TB/s; 43.3 us with
+// Bound by HBM (8192 tokens x 40 heads of 128: 26.3 us, 6.4 TB/s; 43.3 us with
 // cos and sin read from shared memory per row, 8-byte pieces and one row of a thread
-// in flight) and by the launch for a decode step (64 tokens: 2.2 us).  A CTA's rows
+// in flight) and by the launch for a decode step (64 tokens: 1.8 us).  A CTA's rows
 // are asked into L2 before its table of cos and sin is made, from 1 MB of rows on
-// (28.7 us without; 512 tokens 3.4 and 4.0, 128 tokens 2.8 and 2.9, 64 tokens 2.3 and
-// 2.2; 1021 tokens x 7 heads of 64 2.0 and 1.8).
+// (28.8 us without; 512 tokens 3.2 and 3.7, 128 tokens 2.35 and 2.5, 64 tokens the
+// same; 1021 tokens x 7 heads of 64 1.76 and 1.65).
 template <int W>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RopeParams rope, const RotaryParams p) {
     extern __shared__ float4 smem4[];
     float *tab = reinterpret_cast<float *>(smem4);
     grid_launch_dependents();
-    grid_dep_wait();
     const int t0 = blockIdx.x << p.log_tokens, h0 = blockIdx.y * p.heads_per_cta;
     const int n = min(1 << p.log_tokens, p.num_tokens - t0), nh = min(p.heads_per_cta, p.num_heads - h0);
+    const TableMaker table(rope, n);
+    grid_dep_wait();
     if (W == 8 && p.prefetch && static_cast<int>(threadIdx.x) < n)   // (16-byte pieces: aligned rows)
         bulk_prefetch_l2(p.x + (t0 + static_cast<int>(threadIdx.x)) * p.x_stride + h0 * p.head_dim, nh * p.head_dim * 2);
-    fill_table(tab, rope, n, [&](int j) { return __ldg(p.positions + t0 + j); });
+    table.fill(tab, rope, n, [&](int j) { return __ldg(p.positions + t0 + j); });
     __syncthreads();
     rotate_rows<W, W == 8 ? 5 : 8>(tab, rope, p.x + t0 * p.x_stride + h0 * p.head_dim, p.x_stride,
                    p.out + t0 * p.out_stride + h0 * p.head_dim, p.out_stride, n, p.log_tokens, nh, p.head_dim);
@@ -411,11 +431,15 @@ __device__ __forceinline__ int log2_up(int n) { return n <= 1 ? 0 : 32 - __clz(n
 // or values of 8 kv heads (one per warp).  The queries, the longest parts, come
 // first in the grid.  K and V of a block are independent (each has scales of its
 // own): in CTAs of their own the dependent chain of a decode step is shorter
-// (64 requests, Hq 32, Hkv 8, int8: 3.6 us against 4.5 with both in one CTA; two
-// chunks of 2048 tokens into E4M3 codes 19.6 against 21.2, 4.4 TB/s of 12.7 us at
-// the copy rate; four into bf16 31.8 against 30.5, 5.7 TB/s).  Two CTAs per SM with
-// 8 rows of a thread in flight: bound by latency below a wave of CTAs (a decode
-// step: launch, starts and lengths, block id, scale), by HBM above.
+// (64 requests, Hq 32, Hkv 8, int8: 3.6 us against 4.5 with both in one CTA, before
+// the table's steps were read in one access; two chunks of 2048 tokens into E4M3
+// codes 19.6 against 21.2; four into bf16 31.8 against 30.5).  Now 3.5, 18.5 (4.7
+// TB/s; 12.7 us at the copy rate) and 31.6 us (5.8 TB/s): bound by latency below a
+// wave of CTAs (a decode step: launch, starts and lengths, block id, scale), by HBM
+// above, and by both where the queries' CTAs (~10 us each, two per SM) are followed
+// by the last keys and values (~4 us each).  Queries of 8 / 16 / 32 heads per CTA
+// 22.9 / 20.2 / 18.5, a segment's parts side by side in the grid 19.2, keys and
+// values first with 16 heads 19.3; rows asked into L2 first 19.4.
 template <int D, int KIND, int W>
 __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ RopeParams rope, const AppendParams p) {
     using H = HeadRows<D, W>;
@@ -431,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
     if (s.n == 0) return;
     auto pos_of = [&](int j) { return s.pos + j; };
     if (part >= 2 * kv_parts) {
-        fill_table(tab, rope, s.n, pos_of);
+        TableMaker(rope, s.n).fill(tab, rope, s.n, pos_of);
         __syncthreads();
         const int h0 = (part - 2 * kv_parts) * p.q_heads_per_cta;
         rotate_rows<W, 8>(tab, rope, p.q + s.t0 * p.q_stride + h0 * D, p.q_stride, p.q_out + s.t0 * p.q_out_stride + h0 * D,
@@ -460,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
             rb[it] = load_raw<W>(x + u.b);
         }
     }
-    if (half > 0) fill_table(tab, rope, s.n, pos_of);
+    if (half > 0) TableMaker(rope, s.n).fill(tab, rope, s.n, pos_of);
     __syncthreads();
     if (!block_ok(p, s, part == 0) || !mine) return;
     const int64_t row_stride = static_cast<int64_t>(p.num_heads_kv) * D;
