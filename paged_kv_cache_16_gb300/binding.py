@@ -602,10 +602,17 @@ _PLAIN_CACHES = {torch.bfloat16: PA_KV_BF16, torch.uint8: PA_KV_FP8_E4M3}
 _SCALED_CACHES = {torch.uint8: PA_KV_FP8_E4M3_BLOCK, torch.int8: PA_KV_INT8_BLOCK}
 
 
-def _here(t, name: str):
-    """Refuse a tensor that kernels on the current device cannot read."""
-    if t.get_device() < 0 or t.get_device() != (_raw_device or torch.cuda.current_device)():
-        raise ValueError(f"{name}: a tensor of the current CUDA device wanted")
+def _here(what: str, *tensors):
+    """Refuse tensors that kernels on the current device cannot read (one left
+    on the host among them)."""
+    device = tensors[0].get_device()   # (-1: the host)
+    if device >= 0 and device == (_raw_device or torch.cuda.current_device)():
+        for t in tensors:
+            if t.get_device() != device:
+                break
+        else:
+            return
+    raise ValueError(f"{what}: tensors of the current CUDA device wanted")
 
 
 def _rows(t, d: int, name: str) -> int:
@@ -624,7 +631,7 @@ def pa_rotary(rope: Rope, x, positions, out, stream=None):
     xs, os_ = _rows(x, D, "x"), _rows(out, D, "out")
     if out.shape != shape or positions.dtype is not _I32 or positions.numel() != T or not positions.is_contiguous():
         raise ValueError("out: x's shape wanted; positions: contiguous int32 [tokens]")
-    _here(x, "x")
+    _here("x, positions, out", x, positions, out)
     if T <= 1:   # a single row's stride is anything
         xs = os_ = H * D
     st = load().pa_rotary(rope.handle, x.data_ptr(), xs, positions.data_ptr(), T, H, D, out.data_ptr(), os_, _stream(stream))
@@ -670,7 +677,12 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
             raise ValueError(f"q, q_out: rows [{T}, heads, {d}] wanted")
     elif q is not q_out:
         raise ValueError("q and q_out come together")
-    _here(key_cache, "key_cache")
+    _here("rows, starts, lengths, block table, caches", key, value, query_start_loc, num_computed, block_table, key_cache,
+          value_cache)
+    if ksc:
+        _here("scales", key_scales, value_scales)
+    if qp:
+        _here("q, q_out", q, q_out)
     if T <= 1:   # a single row's stride is anything
         ks = vs = hkv * d
         qs = os_ = hq * d
@@ -687,13 +699,14 @@ def _scales(key_cache, key_scales, value_scales):
     if key_scales.dtype is not _F32 or value_scales.dtype is not _F32 or key_scales.shape != shape or \
             value_scales.shape != shape or not key_scales.is_contiguous() or not value_scales.is_contiguous():
         raise ValueError(f"scales: contiguous float {list(shape)} wanted")
-    _here(key_scales, "key_scales")
 
 
 def pa_attention_scaled(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace,
                         stream=None):
     """Attention over block-scaled 8-bit caches (see pa.h)."""
     _scales(key_cache, key_scales, value_scales)
+    _here("q, caches, scales, block table, out, workspace", q, key_cache, value_cache, key_scales, value_scales,
+          block_table, out, workspace)
     st = load().pa_attention_scaled(plan.handle, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                                     key_scales.data_ptr(), value_scales.data_ptr(), block_table.data_ptr(),
                                     out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))
@@ -705,6 +718,8 @@ def pa_attention_scaled_launch(plan: Plan, q, key_cache, value_cache, key_scales
                                workspace, stream=None):
     """Its kernels alone, after pa_upload_metadata (capturable in a CUDA graph)."""
     _scales(key_cache, key_scales, value_scales)
+    _here("q, caches, scales, block table, out, workspace", q, key_cache, value_cache, key_scales, value_scales,
+          block_table, out, workspace)
     st = load().pa_attention_scaled_launch(plan.handle, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                                            key_scales.data_ptr(), value_scales.data_ptr(), block_table.data_ptr(),
                                            out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))

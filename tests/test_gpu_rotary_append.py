@@ -252,6 +252,24 @@ def test_wrappers_refuse_tensors_of_other_devices():
         binding.pa_rotary(rope, x, torch.zeros(3, dtype=torch.int32), x)
 
 
+@pytest.mark.parametrize("left", ["positions", "out", "key", "query_start_loc", "num_computed", "block_table", "key_scales",
+                                  "q"])
+def test_wrappers_refuse_one_tensor_left_on_the_host(left):
+    x = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device=DEV)
+    rope = binding.pa_rope_create(rotary_dim=64)
+    a = dict(positions=i32([0, 1, 2]), out=x.clone(), key=x, value=x, query_start_loc=i32([0, 3]), num_computed=i32([0]),
+             block_table=i32([[0]]), key_cache=torch.zeros(1, 16, 2, 64, dtype=torch.int8, device=DEV),
+             value_cache=torch.zeros(1, 16, 2, 64, dtype=torch.int8, device=DEV), key_scales=torch.ones(1, 2, device=DEV),
+             value_scales=torch.ones(1, 2, device=DEV), q=x, q_out=x.clone())
+    a[left] = a[left].cpu()
+    positions, out = a.pop("positions"), a.pop("out")
+    with pytest.raises(ValueError, match="current CUDA device"):
+        if left in ("positions", "out"):
+            binding.pa_rotary(rope, x, positions, out)
+        else:
+            binding.pa_append_kv(rope, **a)
+
+
 def test_append_scaled_foreign_scales():
     """Old scales that are no powers of two: kept where large enough, codes
     re-coded by the true ratio where not."""

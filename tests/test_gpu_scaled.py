@@ -104,6 +104,17 @@ def test_one_key_is_its_value():
         assert np.array_equal(out[0].double().cpu().numpy(), np.repeat(v, 2, axis=0))
 
 
+@pytest.mark.parametrize("left", range(8))
+@pytest.mark.parametrize("call", ["pa_attention_scaled", "pa_attention_scaled_launch"])
+def test_one_tensor_left_on_the_host_is_refused(left, call):
+    """(q, caches, scales, block table, out, workspace)"""
+    g = oc.OnGpu(oc.Case(hq=4, hkv=2, d=64, q_lens=[1], seq_lens=[20], code="int8"))
+    args = list(g.args())
+    args[left] = args[left].cpu()
+    with pytest.raises(ValueError, match="current CUDA device"):
+        getattr(binding, call)(g.plan, *args)
+
+
 def test_matches_the_tensor_scale_kernel():
     """Equal scales everywhere: the E4M3 kernels with one scale per tensor on the
     same codes agree within both bounds (theirs: bf16 weights on the tiles,
