@@ -694,19 +694,30 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
         _check(st, "pa_append_kv")
 
 
-def _scales(key_cache, key_scales, value_scales):
-    shape = (key_cache.shape[0], key_cache.shape[2])
-    if key_scales.dtype is not _F32 or value_scales.dtype is not _F32 or key_scales.shape != shape or \
-            value_scales.shape != shape or not key_scales.is_contiguous() or not value_scales.is_contiguous():
-        raise ValueError(f"scales: contiguous float {list(shape)} wanted")
+def _attention_args(q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace):
+    # (element counts: a shape object costs as much as three other questions, and
+    # the smallest calls are bound by this thread)
+    blocks, _, heads, _ = key_cache.shape
+    n = blocks * heads
+    if key_scales.dtype is not _F32 or value_scales.dtype is not _F32 or key_scales.numel() != n or \
+            value_scales.numel() != n or not key_scales.is_contiguous() or not value_scales.is_contiguous():
+        raise ValueError(f"scales: contiguous float [{blocks}, {heads}] wanted")
+    if q.dtype is not _BF16 or out.dtype is not _BF16 or not q.is_contiguous() or not out.is_contiguous():
+        raise ValueError("q, out: contiguous bf16 wanted")
+    if block_table.dtype is not _I32 or not block_table.is_contiguous():
+        raise ValueError("block_table: contiguous int32 wanted")
+    codes = key_cache.dtype
+    if codes not in _SCALED_CACHES or value_cache.dtype is not codes or value_cache.numel() != key_cache.numel() or \
+            not key_cache.is_contiguous() or not value_cache.is_contiguous():
+        raise ValueError("caches: contiguous codes (uint8 or int8) of one shape wanted")
+    _here("q, caches, scales, block table, out, workspace", q, key_cache, value_cache, key_scales, value_scales,
+          block_table, out, workspace)
 
 
 def pa_attention_scaled(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace,
                         stream=None):
     """Attention over block-scaled 8-bit caches (see pa.h)."""
-    _scales(key_cache, key_scales, value_scales)
-    _here("q, caches, scales, block table, out, workspace", q, key_cache, value_cache, key_scales, value_scales,
-          block_table, out, workspace)
+    _attention_args(q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace)
     st = load().pa_attention_scaled(plan.handle, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                                     key_scales.data_ptr(), value_scales.data_ptr(), block_table.data_ptr(),
                                     out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))
@@ -717,9 +728,7 @@ def pa_attention_scaled(plan: Plan, q, key_cache, value_cache, key_scales, value
 def pa_attention_scaled_launch(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out,
                                workspace, stream=None):
     """Its kernels alone, after pa_upload_metadata (capturable in a CUDA graph)."""
-    _scales(key_cache, key_scales, value_scales)
-    _here("q, caches, scales, block table, out, workspace", q, key_cache, value_cache, key_scales, value_scales,
-          block_table, out, workspace)
+    _attention_args(q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace)
     st = load().pa_attention_scaled_launch(plan.handle, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                                            key_scales.data_ptr(), value_scales.data_ptr(), block_table.data_ptr(),
                                            out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))

@@ -196,3 +196,28 @@ def test_native_graph_refuses_scaled(lib):
         setattr(b, f, FAKE)
     h = ctypes.c_void_p()
     assert lib.pa_graph_create(ctypes.byref(d), ctypes.byref(fs), ctypes.byref(b), ctypes.byref(h)) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("call", ["pa_attention_scaled", "pa_attention_scaled_launch"])
+@pytest.mark.parametrize("change, message", [
+    (dict(q=torch.zeros(3, 4, 64)), "bf16"),
+    (dict(q=torch.zeros(3, 64, 4, dtype=torch.bfloat16).transpose(1, 2)), "contiguous bf16"),
+    (dict(out=torch.zeros(6, 4, 64, dtype=torch.bfloat16)[::2]), "contiguous bf16"),
+    (dict(table=torch.zeros(1, 2, dtype=torch.int64)), "int32"),
+    (dict(table=torch.zeros(2, 4, dtype=torch.int32)[:, ::2]), "contiguous int32"),
+    (dict(kc=torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16)), "codes"),
+    (dict(vc=torch.zeros(2, 16, 2, 64, dtype=torch.uint8)), "one shape"),
+    (dict(vc=torch.zeros(3, 16, 2, 64, dtype=torch.int8)), "one shape"),
+    (dict(kc=torch.zeros(2, 16, 4, 64, dtype=torch.int8)[:, :, ::2]), "contiguous codes"),
+    (dict(ks=torch.ones(2, 3)), "scales"),
+    (dict(vs=torch.ones(2, 2, dtype=torch.float64)), "scales"),
+    (dict(vs=torch.ones(2, 4)[:, ::2]), "scales"),
+    (dict(), "current CUDA device"),
+])
+def test_attention_wrappers_refuse(call, change, message):
+    a = dict(q=torch.zeros(3, 4, 64, dtype=torch.bfloat16), kc=torch.zeros(2, 16, 2, 64, dtype=torch.int8),
+             vc=torch.zeros(2, 16, 2, 64, dtype=torch.int8), ks=torch.ones(2, 2), vs=torch.ones(2, 2),
+             table=torch.zeros(1, 2, dtype=torch.int32), out=torch.zeros(3, 4, 64, dtype=torch.bfloat16),
+             workspace=torch.zeros(4096, dtype=torch.uint8))
+    with pytest.raises(ValueError, match=message):
+        getattr(binding, call)(None, *(a | change).values())
