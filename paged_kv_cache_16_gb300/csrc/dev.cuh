@@ -322,6 +322,15 @@ __device__ __forceinline__ float lg2(float x) {
 // A block scale as attention uses it: at least 2^-100 (a NaN stays one).
 __device__ __forceinline__ float used_scale(float s) { return s < 0x1p-100f ? 0x1p-100f : s; }
 
+// What a code product is multiplied by to be a score: a * b, at least 2^-149 where
+// that underflows to 0 (a masked score of -infinity times 0 would be NaN; the
+// scores of such a block are 0 up to 2^-20 either way).  A NaN stays one.
+__device__ __forceinline__ float score_factor(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a * b), "f"(0x1p-149f));
+    return y;
+}
+
 // Four codes (one word, lowest byte first) -> two f16x2 words, exact.  int8:
 // the byte plus 128 as the low mantissa bits of 1024 + byte, minus 1152.
 template <bool INT8>

@@ -217,7 +217,7 @@ struct Consumer {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) kf[k][n][e] = ks * rf[n][e];
+                    for (int e = 0; e < 2; ++e) kf[k][n][e] = score_factor(ks, rf[n][e]);
                 if (++slot == C::NS) {
                     slot = 0;
                     parity ^= 1u;

@@ -154,7 +154,7 @@ __global__ void expand_scaled_kernel(DequantParams p) {
             const float kf = dev::used_scale(__ldg(p.key_scales + static_cast<int64_t>(src) * p.num_heads_kv + h));
             const float vf = dev::used_scale(__ldg(p.value_scales + static_cast<int64_t>(src) * p.num_heads_kv + h));
             // (a NaN value scale shows in the scores, where masks can take it out)
-            fd[static_cast<int64_t>(h) * p.n_dst] = vf == vf ? make_float4(kf * p.scale_log2, dev::lg2(vf), 1.f / vf, 0.f)
+            fd[static_cast<int64_t>(h) * p.n_dst] = vf == vf ? make_float4(dev::score_factor(kf, p.scale_log2), dev::lg2(vf), 1.f / vf, 0.f)
                                                             : make_float4(vf, 0.f, 1.f, 0.f);
         }
     }
