@@ -109,8 +109,12 @@ struct Consumer {
         const int G = b.group;
         const int kvh = item.head_group * HG + warp;
         const int nrow = item.n_tok * G;
-        // q as f16, each row scaled by a power of two to magnitudes below 2
-        // (bf16's range does not fit f16's): the factor returns in the scores
+        // q as f16, each row scaled by a power of two to magnitudes below 2 (4 for
+        // the largest of bf16, whose range does not fit f16's): the factor returns
+        // in the scores.  Exact for elements down to 2^-17 of the row's largest
+        // magnitude; smaller ones are rounded to steps of 2^-24 of it, at most
+        // 2^-25 of it off (a score by 2^-25 of that magnitude times the sum of |k|).
+        // f16 and not bf16, because one conversion then serves the codes of K and V
         uint32_t qt[NT][D / 16][2];
         float rf[NT][2];
 #pragma unroll
@@ -133,7 +137,7 @@ struct Consumer {
                 }
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
             amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-            const int e2 = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100), 100);
+            const int e2 = min(max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -126), 126);
             const float down = __uint_as_float(static_cast<uint32_t>(127 - e2) << 23);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk)

@@ -81,3 +81,11 @@ def test_step_of_zero_queries_and_keys(code):
     c.table, c.nb = a.table, a.nb
     c.q, c.kc, c.vc, c.ks, c.vs = q.cpu(), kc.cpu(), vc.cpu(), ks.cpu(), vs.cpu()
     check(c)
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("q_size", [1e-36, 1e-30, 1e30, 1e35])
+def test_queries_at_the_ends_of_the_bf16_range(code, q_size):
+    """Magnitudes beyond 2^100 and below 2^-100 on the split-KV kernel (the softmax
+    scale undoes them)."""
+    check(oc.Case(hq=8, hkv=2, d=128, q_lens=[1, 3], seq_lens=[100, 50], code=code, q_size=q_size))
