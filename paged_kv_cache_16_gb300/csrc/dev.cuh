@@ -184,6 +184,19 @@ __device__ __forceinline__ void st_global_v8(void *p, uint32_t a0, uint32_t a1, 
                  : "memory");
 }
 
+// The same 32 bytes of an output row, whose address is a multiple of 32 (`wide`) or
+// of 16 alone, where one 32-byte store would be misaligned.
+__device__ __forceinline__ void st_row_v8(bool wide, void *p, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t a4, uint32_t a5, uint32_t a6, uint32_t a7) {
+    if (wide) {
+        st_global_v8(p, a0, a1, a2, a3, a4, a5, a6, a7);
+    } else {
+        uint4 *q = static_cast<uint4 *>(p);
+        q[0] = make_uint4(a0, a1, a2, a3);
+        q[1] = make_uint4(a4, a5, a6, a7);
+    }
+}
+
 __device__ __forceinline__ uint64_t policy_evict_first() {
     uint64_t p;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));

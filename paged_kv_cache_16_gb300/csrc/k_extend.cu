@@ -503,6 +503,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             ++ocnt;
             tc_fence_after();
             const float inv = l > 0.f ? p.out_scale / l : 0.f;
+            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
             const int tok = tile.t0 + i;
             const int h = tile.kv_head * G + gq;
             int64_t slot = -1;
@@ -524,7 +525,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                         for (int e = 0; e < 8; ++e)
                             w[e] = pack_bf16x2(__uint_as_float(orr[q8 * 16 + 2 * e]) * inv,
                                                __uint_as_float(orr[q8 * 16 + 2 * e + 1]) * inv);
-                        st_global_v8(dst + q8 * 16, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
+                        st_row_v8(wide, dst + q8 * 16, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
                     }
                 } else {
                     float *dst = p.o_part + (slot * p.num_heads_q + h) * D + c;

@@ -592,6 +592,7 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 // exchanged so that a store writes 128 consecutive bytes of 8 rows
                 // (a piece of 32 rows each: 80 cycles a store, 5000 an epilogue,
                 // with the MMA thread's requests queued behind them).
+                const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
                 const int64_t mine = tok_valid ? (static_cast<int64_t>(tok) * p.num_heads_q + h) * D : -1;
                 int64_t at[4];   // rows of the four lanes
 #pragma unroll
@@ -623,8 +624,8 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
                     for (int s = 0; s < 4; ++s)
                         if (at[s] >= 0)
-                            st_global_v8(p.out + at[s] + c + 16 * (lane & 3), w[8 * s], w[8 * s + 1], w[8 * s + 2],
-                                         w[8 * s + 3], w[8 * s + 4], w[8 * s + 5], w[8 * s + 6], w[8 * s + 7]);
+                            st_row_v8(wide, p.out + at[s] + c + 16 * (lane & 3), w[8 * s], w[8 * s + 1], w[8 * s + 2],
+                                      w[8 * s + 3], w[8 * s + 4], w[8 * s + 5], w[8 * s + 6], w[8 * s + 7]);
                 }
             } else {
 #pragma unroll 1
