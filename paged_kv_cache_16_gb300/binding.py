@@ -324,6 +324,9 @@ class Plan:
     handle: int
     workspace_bytes: int
     _keep: tuple  # host arrays referenced while pa_plan runs
+    # what the tensors of its calls have to be: (kv_cache_dtype, elements of q and
+    # out, num_blocks, kv heads, head_dim, elements of the block table, its width)
+    _step: tuple | None = None
 
     def info(self) -> dict:
         pi = PlanInfo()
@@ -368,13 +371,18 @@ def make_desc(*, num_heads_q, num_heads_kv, head_dim, num_blocks, query_start_lo
     return d, (qsl, sl, nc, bt)
 
 
+def _step_of(d: BatchDesc, rows: int) -> tuple:
+    return (d.kv_cache_dtype, rows * d.num_heads_q * d.head_dim, d.num_blocks, d.num_heads_kv, d.head_dim,
+            d.num_reqs * d.max_blocks_per_req, d.max_blocks_per_req)
+
+
 def pa_plan(**kw) -> Plan:
     """Validate the step's metadata and build its plan (see pa.h)."""
     d, keep = make_desc(**kw)
     handle = ctypes.c_void_p()
     ws = ctypes.c_size_t()
     _check(load().pa_plan(ctypes.byref(d), ctypes.byref(handle), ctypes.byref(ws)), "pa_plan")
-    return Plan(handle.value, ws.value, keep)
+    return Plan(handle.value, ws.value, keep, _step_of(d, int(keep[0][-1]) if len(keep[0]) else 0))
 
 
 def _fixed_shape(max_tokens, max_reqs, max_extend_tiles=0, max_dequant_blocks=0, max_partial_slots=0,
@@ -397,7 +405,7 @@ def pa_plan_fixed(*, max_tokens, max_reqs, max_extend_tiles=0, max_dequant_block
     ws = ctypes.c_size_t()
     _check(load().pa_plan_fixed(ctypes.byref(d), ctypes.byref(fs), ctypes.byref(handle), ctypes.byref(ws)),
            "pa_plan_fixed")
-    return Plan(handle.value, ws.value, keep)
+    return Plan(handle.value, ws.value, keep, _step_of(d, fs.max_tokens))
 
 
 def pa_plan_fixed_status(*, max_tokens, max_reqs, max_extend_tiles=0, max_dequant_blocks=0, max_partial_slots=0,
@@ -694,10 +702,10 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
         _check(st, "pa_append_kv")
 
 
-def _attention_args(q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace):
+def _attention_args(plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace):
     # (element counts: a shape object costs as much as three other questions, and
     # the smallest calls are bound by this thread)
-    blocks, _, heads, _ = key_cache.shape
+    blocks, _, heads, d = key_cache.shape
     n = blocks * heads
     if key_scales.dtype is not _F32 or value_scales.dtype is not _F32 or key_scales.numel() != n or \
             value_scales.numel() != n or not key_scales.is_contiguous() or not value_scales.is_contiguous():
@@ -710,6 +718,18 @@ def _attention_args(q, key_cache, value_cache, key_scales, value_scales, block_t
     if codes not in _SCALED_CACHES or value_cache.dtype is not codes or value_cache.numel() != key_cache.numel() or \
             not key_cache.is_contiguous() or not value_cache.is_contiguous():
         raise ValueError("caches: contiguous codes (uint8 or int8) of one shape wanted")
+    if plan is not None and plan._step is not None:
+        # the kernels go by the plan: tensors of another step, or codes of another
+        # type, would be read as what they are not, or past their ends
+        kind, rows, nb, hkv, dim, entries, width = plan._step
+        if _SCALED_CACHES[codes] != kind:
+            raise ValueError("caches: the type of codes that the plan was made for wanted")
+        if heads != hkv or d != dim or blocks < nb or key_cache.numel() != blocks * 16 * heads * d:
+            raise ValueError(f"caches: the plan's [{nb}, 16, {hkv}, {dim}] wanted")
+        if q.numel() < rows or out.numel() < rows:
+            raise ValueError(f"q, out: all of the plan's rows wanted ({rows} elements)")
+        if block_table.numel() < entries or block_table.shape[-1] != width:
+            raise ValueError(f"block_table: the plan's requests and its {width} blocks each wanted")
     _here("q, caches, scales, block table, out, workspace", q, key_cache, value_cache, key_scales, value_scales,
           block_table, out, workspace)
 
@@ -717,7 +737,7 @@ def _attention_args(q, key_cache, value_cache, key_scales, value_scales, block_t
 def pa_attention_scaled(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace,
                         stream=None):
     """Attention over block-scaled 8-bit caches (see pa.h)."""
-    _attention_args(q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace)
+    _attention_args(plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace)
     st = load().pa_attention_scaled(plan.handle, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                                     key_scales.data_ptr(), value_scales.data_ptr(), block_table.data_ptr(),
                                     out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))
@@ -728,7 +748,7 @@ def pa_attention_scaled(plan: Plan, q, key_cache, value_cache, key_scales, value
 def pa_attention_scaled_launch(plan: Plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out,
                                workspace, stream=None):
     """Its kernels alone, after pa_upload_metadata (capturable in a CUDA graph)."""
-    _attention_args(q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace)
+    _attention_args(plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace)
     st = load().pa_attention_scaled_launch(plan.handle, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
                                            key_scales.data_ptr(), value_scales.data_ptr(), block_table.data_ptr(),
                                            out.data_ptr(), workspace.data_ptr(), workspace.nbytes, _stream(stream))

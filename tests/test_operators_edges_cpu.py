@@ -1,0 +1,54 @@
+"""Refusals of the operators' wrappers and steps, and what their plans look
+like, on the CPU (no kernel runs)."""
+import numpy as np
+import pytest
+import torch
+
+import operators_common as oc
+from paged_kv_cache_16_gb300 import binding, build
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    build.build()
+    return binding.load()
+
+
+@pytest.mark.parametrize("call", ["pa_attention_scaled", "pa_attention_scaled_launch"])
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("change,message", [
+    (lambda a: dict(kc=a["kc"].view(torch.uint8 if a["kc"].dtype == torch.int8 else torch.int8),
+                    vc=a["vc"].view(torch.uint8 if a["vc"].dtype == torch.int8 else torch.int8)), "type of codes"),
+    (lambda a: dict(out=a["out"][:-1]), "rows"), (lambda a: dict(q=a["q"][:-1]), "rows"),
+    (lambda a: dict(table=a["table"][:-1]), "requests"), (lambda a: dict(table=a["table"][:, :-1].contiguous()), "blocks each"),
+    (lambda a: dict(kc=a["kc"][:-1], vc=a["vc"][:-1], ks=a["ks"][:-1], vs=a["vs"][:-1]), "caches"),
+    (lambda a: dict(kc=a["kc"].view(-1, 16, 4, 64), vc=a["vc"].view(-1, 16, 4, 64), ks=a["ks"].repeat(1, 2),
+                    vs=a["vs"].repeat(1, 2)), "caches"),
+    (lambda a: dict(kc=a["kc"].view(-1, 8, 2, 128), vc=a["vc"].view(-1, 8, 2, 128), ks=a["ks"].repeat(2, 1),
+                    vs=a["vs"].repeat(2, 1)), "caches")])
+def test_attention_refuses_what_its_plan_was_not_made_for(call, code, change, message):
+    """The kernels read and write by the plan's sizes: an output of fewer rows would
+    be written past its end, int8 codes read as E4M3 ones."""
+    c = oc.Case(hq=4, hkv=2, d=128, q_lens=[3, 1], seq_lens=[40, 90], code=code)
+    plan = binding.pa_plan(**c.desc(num_sms=4))
+    a = dict(q=c.q, kc=c.kc, vc=c.vc, ks=c.ks, vs=c.vs, table=torch.from_numpy(c.table), out=torch.empty_like(c.q),
+             workspace=torch.zeros(plan.workspace_bytes, dtype=torch.uint8))
+    with pytest.raises(ValueError, match=message):
+        getattr(binding, call)(plan, *(a | change(a)).values())
+    with pytest.raises(ValueError, match="current CUDA device"):     # the last check, reached by the plan's own tensors
+        getattr(binding, call)(plan, *a.values())
+    more = dict(a, q=torch.cat([c.q, c.q]), out=torch.empty(9, 4, 128, dtype=torch.bfloat16))
+    with pytest.raises(ValueError, match="current CUDA device"):     # rows behind the last are the caller's
+        getattr(binding, call)(plan, *more.values())
+
+
+def test_attention_of_a_fixed_shape_wants_its_capacity():
+    c = oc.Case(hq=4, hkv=2, d=64, q_lens=[1, 1], seq_lens=[40, 90], code="int8")
+    plan = binding.pa_plan_fixed(max_tokens=8, max_reqs=4, **c.desc(num_sms=4))
+    a = dict(q=c.q, kc=c.kc, vc=c.vc, ks=c.ks, vs=c.vs, table=torch.from_numpy(c.table), out=torch.empty_like(c.q),
+             workspace=torch.zeros(plan.workspace_bytes, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="rows"):
+        binding.pa_attention_scaled_launch(plan, *a.values())
+    a["q"] = a["out"] = torch.empty(8, 4, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="current CUDA device"):
+        binding.pa_attention_scaled_launch(plan, *a.values())
