@@ -705,7 +705,7 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
 def _attention_args(plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace):
     # (element counts: a shape object costs as much as three other questions, and
     # the smallest calls are bound by this thread)
-    blocks, _, heads, d = key_cache.shape
+    blocks, slots, heads, d = key_cache.shape
     n = blocks * heads
     if key_scales.dtype is not _F32 or value_scales.dtype is not _F32 or key_scales.numel() != n or \
             value_scales.numel() != n or not key_scales.is_contiguous() or not value_scales.is_contiguous():
@@ -715,16 +715,17 @@ def _attention_args(plan, q, key_cache, value_cache, key_scales, value_scales, b
     if block_table.dtype is not _I32 or not block_table.is_contiguous():
         raise ValueError("block_table: contiguous int32 wanted")
     codes = key_cache.dtype
-    if codes not in _SCALED_CACHES or value_cache.dtype is not codes or value_cache.numel() != key_cache.numel() or \
+    code_kind = _SCALED_CACHES.get(codes)
+    if code_kind is None or value_cache.dtype is not codes or value_cache.numel() != n * slots * d or \
             not key_cache.is_contiguous() or not value_cache.is_contiguous():
         raise ValueError("caches: contiguous codes (uint8 or int8) of one shape wanted")
     if plan is not None and plan._step is not None:
         # the kernels go by the plan: tensors of another step, or codes of another
         # type, would be read as what they are not, or past their ends
         kind, rows, nb, hkv, dim, entries, width = plan._step
-        if _SCALED_CACHES[codes] != kind:
+        if code_kind != kind:
             raise ValueError("caches: the type of codes that the plan was made for wanted")
-        if heads != hkv or d != dim or blocks < nb or key_cache.numel() != blocks * 16 * heads * d:
+        if heads != hkv or d != dim or blocks < nb or slots != 16:
             raise ValueError(f"caches: the plan's [{nb}, 16, {hkv}, {dim}] wanted")
         if q.numel() < rows or out.numel() < rows:
             raise ValueError(f"q, out: all of the plan's rows wanted ({rows} elements)")
