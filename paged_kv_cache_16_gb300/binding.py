@@ -685,18 +685,24 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
             raise ValueError(f"q, q_out: rows [{T}, heads, {d}] wanted")
     elif q is not q_out:
         raise ValueError("q and q_out come together")
+    word = _ptr(device_error_word)
+    if word is not None and word is not device_error_word and \
+            (device_error_word.dtype is not _I32 or device_error_word.numel() < 1):
+        raise ValueError("device_error_word: an int32 wanted")
     _here("rows, starts, lengths, block table, caches", key, value, query_start_loc, num_computed, block_table, key_cache,
           value_cache)
     if ksc:
         _here("scales", key_scales, value_scales)
     if qp:
         _here("q, q_out", q, q_out)
+    if word is not None and word is not device_error_word:
+        _here("device_error_word", device_error_word)
     if T <= 1:   # a single row's stride is anything
         ks = vs = hkv * d
         qs = os_ = hq * d
     a = AppendArgs(R, T, hq, hkv, d, bs, nb, mb, kind, k_scale, v_scale, query_start_loc.data_ptr(), num_computed.data_ptr(),
                    block_table.data_ptr(), key.data_ptr(), value.data_ptr(), ks, vs, qp, op, qs, os_, key_cache.data_ptr(),
-                   value_cache.data_ptr(), ksc, vsc, _ptr(device_error_word))
+                   value_cache.data_ptr(), ksc, vsc, word)
     st = load().pa_append_kv(rope.handle if rope is not None else None, a, _stream(stream))
     if st:
         _check(st, "pa_append_kv")

@@ -52,3 +52,21 @@ def test_attention_of_a_fixed_shape_wants_its_capacity():
     a["q"] = a["out"] = torch.empty(8, 4, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="current CUDA device"):
         binding.pa_attention_scaled_launch(plan, *a.values())
+
+
+def append_call(**over):
+    c = oc.AppendCase(hq=4, hkv=2, d=64, q_lens=[3, 1], computed=[5, 0], code="int8")
+    i32 = lambda a: torch.as_tensor(a, dtype=torch.int32)  # noqa: E731
+    a = dict(rope=None, key=c.key, value=c.value, query_start_loc=i32(c.qsl), num_computed=i32(c.nc),
+             block_table=i32(c.table), key_cache=c.kc, value_cache=c.vc, key_scales=c.ks, value_scales=c.vs)
+    return binding.pa_append_kv(**(a | over))
+
+
+@pytest.mark.parametrize("word", [torch.zeros(1, dtype=torch.uint8), torch.zeros(1, dtype=torch.int64),
+                                  torch.zeros(0, dtype=torch.int32)])
+def test_append_refuses_error_words_of_other_types(word):
+    """The kernel sets bits of four bytes there."""
+    with pytest.raises(ValueError, match="device_error_word"):
+        append_call(device_error_word=word)
+    with pytest.raises(ValueError, match="rows, starts"):
+        append_call(device_error_word=torch.zeros(1, dtype=torch.int32))
