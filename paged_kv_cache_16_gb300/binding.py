@@ -654,6 +654,8 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
     (see pa.h).  The cache's type follows from the tensors: bf16; uint8 E4M3
     codes with k_scale / v_scale; uint8 or int8 codes with key_scales and
     value_scales (float [num_blocks, Hkv])."""
+    if rope is not None and not rope.handle:   # (without a rotation keys would be stored as they are)
+        raise ValueError("rope: destroyed")
     shape = T, hkv, d = key.shape
     ks, vs = _rows(key, d, "key"), _rows(value, d, "value")
     pool, dtype = key_cache.shape, key_cache.dtype

@@ -70,3 +70,13 @@ def test_append_refuses_error_words_of_other_types(word):
         append_call(device_error_word=word)
     with pytest.raises(ValueError, match="rows, starts"):
         append_call(device_error_word=torch.zeros(1, dtype=torch.int32))
+
+
+def test_append_refuses_a_destroyed_rope():
+    """It must not pass for no rope at all, with which keys are stored unrotated."""
+    rope = binding.pa_rope_create(rotary_dim=64)
+    with pytest.raises(ValueError, match="rows, starts"):
+        append_call(rope=rope)
+    rope.destroy()
+    with pytest.raises(ValueError, match="destroyed"):
+        append_call(rope=rope)
