@@ -29,7 +29,8 @@ class DeviceStep:
     """Device-resident metadata, plan, workspace and output of one batch.
 
     ``rope`` (binding.pa_rope_create): run_append rotates queries and keys by
-    their positions on the way into the cache.  Block-scaled caches
+    their positions on the way into the cache (write, run and run_fused, which
+    do not rotate, refuse such a step).  Block-scaled caches
     ("fp8_block", "int8_block") go through run_append / append and attend, with
     their scales."""
 
@@ -72,7 +73,12 @@ class DeviceStep:
                                 b.block_size, stream)
         return self.slots[:b.num_tokens]
 
+    def _unrotated(self):
+        if self.rope is not None:
+            raise ValueError("a step with a rope stores and attends rotated rows: append (run_append)")
+
     def write(self, key, value, key_cache, value_cache, stream=None):
+        self._unrotated()
         if self.batch.kv_cache_dtype not in ("bf16", "fp8"):
             raise ValueError("block-scaled caches are written by append (run_append)")
         if self.batch.kv_cache_dtype == "fp8":
@@ -103,12 +109,14 @@ class DeviceStep:
 
     def run(self, q, key, value, key_cache, value_cache, stream=None):
         """slot mapping -> cache write -> attention; returns out [T, Hq, D]."""
+        self._unrotated()
         self.slot_mapping(stream)
         self.write(key, value, key_cache, value_cache, stream)
         return self.attend(q, key_cache, value_cache, stream)
 
     def run_fused(self, q, key, value, key_cache, value_cache, stream=None, plan=None):
         """Cache write and attention as one call (slots land in self.slots)."""
+        self._unrotated()
         binding.pa_attention_with_kv_update(plan or self.plan, q, key, value, key_cache, value_cache,
                                             self.block_table, self.out, self.workspace, self.slots, stream)
         return self.out[:self.batch.num_tokens]

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import operators_common as oc
-from paged_kv_cache_16_gb300 import binding, build
+from paged_kv_cache_16_gb300 import binding, build, workloads
+from paged_kv_cache_16_gb300.step import DeviceStep
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -80,3 +81,18 @@ def test_append_refuses_a_destroyed_rope():
     rope.destroy()
     with pytest.raises(ValueError, match="destroyed"):
         append_call(rope=rope)
+
+
+def small_batch(kind):
+    return workloads.make_batch(name="cpu", num_heads_q=4, num_heads_kv=2, head_dim=128, q_lens=[1, 3], seq_lens=[20, 33],
+                                num_blocks=8, kv_cache_dtype=kind)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "fp8"])
+@pytest.mark.parametrize("call", ["run", "run_fused", "write"])
+def test_step_with_a_rope_refuses_calls_that_do_not_rotate(kind, call):
+    b = small_batch(kind)
+    st = DeviceStep(b, "cpu", num_sms=4, rope=binding.pa_rope_create(rotary_dim=64))
+    args = (b.q, b.key, b.value, b.key_cache, b.value_cache)
+    with pytest.raises(ValueError, match="run_append"):
+        getattr(st, call)(*args[call == "write":])
