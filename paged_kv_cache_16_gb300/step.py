@@ -15,6 +15,13 @@ KV_DTYPES = {"bf16": binding.PA_KV_BF16, "fp8": binding.PA_KV_FP8_E4M3, "fp8_blo
              "int8_block": binding.PA_KV_INT8_BLOCK}
 
 
+def _check_scales(scaled: bool, key_scales, value_scales):
+    """Block-scaled steps come with both scales, others with none: the cache's type
+    follows from them, so that codes would be written as another type's."""
+    if (key_scales is not None, value_scales is not None) != (scaled, scaled):
+        raise ValueError("key_scales and value_scales wanted" if scaled else "a step of caches without block scales")
+
+
 def _append(rope, step, k_scale, v_scale, q, key, value, key_cache, value_cache, key_scales, value_scales, stream):
     """pa_append_kv with a step's metadata: the cache write with the rotation (if
     any) on the way; returns the queries to attend with."""
@@ -99,6 +106,7 @@ class DeviceStep:
     def append(self, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None, stream=None):
         """Cache write of the new rows into any cache type, keys rotated if the
         step has a rope; returns the (then rotated) queries."""
+        _check_scales(self.batch.kv_cache_dtype in ("fp8_block", "int8_block"), key_scales, value_scales)
         return _append(self.rope, self, self.batch.k_scale, self.batch.v_scale, q, key, value, key_cache, value_cache,
                        key_scales, value_scales, stream)
 
@@ -302,6 +310,7 @@ class GraphStep:
         (every launch sized by the capacities; capturable).  Fused: one
         pa_attention_with_kv_update_launch does all three.  With a rope or block
         scales: the append, then attention."""
+        _check_scales(self.scaled, key_scales, value_scales)
         if self.rope is not None or self.scaled:
             q = _append(self.rope, self, self.k_scale, self.v_scale, self.q, self.key, self.value, key_cache, value_cache,
                         key_scales, value_scales, stream)
@@ -329,6 +338,7 @@ class GraphStep:
     def capture(self, plan: binding.Plan, key_cache, value_cache, key_scales=None, value_scales=None):
         """Capture the upload of each metadata image followed by enqueue();
         the caches (and scales) are part of the graphs."""
+        _check_scales(self.scaled, key_scales, value_scales)
         if self.workspace is None:
             self.workspace = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device=self.device)
         binding.pa_upload_metadata(plan, self.workspace)   # prepares the kernels (not capturable)
@@ -375,6 +385,7 @@ class GraphStep:
 
     def run(self, batch: Batch, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None) -> torch.Tensor:
         """One step: plan, copy in, replay (capturing on first use)."""
+        _check_scales(self.scaled, key_scales, value_scales)
         plan = self.make_plan(batch)
         self.stage(batch, q, key, value)
         if self.graphs is None:

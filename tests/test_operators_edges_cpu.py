@@ -6,7 +6,7 @@ import torch
 
 import operators_common as oc
 from paged_kv_cache_16_gb300 import binding, build, workloads
-from paged_kv_cache_16_gb300.step import DeviceStep
+from paged_kv_cache_16_gb300.step import DeviceStep, GraphStep
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -96,3 +96,21 @@ def test_step_with_a_rope_refuses_calls_that_do_not_rotate(kind, call):
     args = (b.q, b.key, b.value, b.key_cache, b.value_cache)
     with pytest.raises(ValueError, match="run_append"):
         getattr(st, call)(*args[call == "write":])
+
+
+@pytest.mark.parametrize("kind", ["int8_block", "fp8_block", "fp8", "bf16"])
+def test_steps_refuse_scales_that_do_not_go_with_their_caches(kind):
+    """Codes of a block-scaled cache without its scales would be written as E4M3
+    codes with one scale, and the reverse."""
+    b = small_batch(kind)
+    scales = (torch.ones(8, 2), torch.ones(8, 2))
+    bad = [(None, None), (scales[0], None), (None, scales[1])] if "block" in kind else [scales, (scales[0], None)]
+    st = DeviceStep(b, "cpu", num_sms=4)
+    gs = GraphStep(num_heads_q=4, num_heads_kv=2, head_dim=128, num_blocks=8, max_blocks_per_req=3,
+                   softmax_scale=b.softmax_scale, max_tokens=8, max_reqs=4, kv_cache_dtype=kind, num_sms=4, device="cpu")
+    rows = (b.q, b.key, b.value, b.key_cache, b.value_cache)
+    for s in bad:
+        for call in (lambda: st.append(*rows, *s), lambda: st.run_append(*rows, *s), lambda: gs.run(b, *rows, *s),
+                     lambda: gs.capture(None, *rows[3:], *s), lambda: gs.enqueue(None, *rows[3:], None, *s)):
+            with pytest.raises(ValueError, match="scales"):
+                call()
