@@ -12,7 +12,6 @@ import os
 from dataclasses import dataclass
 
 import numpy as np
-import torch
 
 from . import build as _build
 
@@ -303,17 +302,32 @@ def _ptr(t) -> int | None:
     return int(t.data_ptr())
 
 
-_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+# What the calls that take tensors ask of torch, which the first of them imports:
+# plans, their metadata and rotations need none.
+_cuda = _raw_stream = _raw_device = _BF16 = _I32 = _F32 = None
+_PLAIN_CACHES, _SCALED_CACHES = {}, {}
+
+
+def _use_torch():
+    global _cuda, _raw_stream, _raw_device, _BF16, _I32, _F32
+    import torch
+    _PLAIN_CACHES.update({torch.bfloat16: PA_KV_BF16, torch.uint8: PA_KV_FP8_E4M3})
+    _SCALED_CACHES.update({torch.uint8: PA_KV_FP8_E4M3_BLOCK, torch.int8: PA_KV_INT8_BLOCK})
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    _raw_device = getattr(torch._C, "_cuda_getDevice", None)
+    _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+    _cuda = torch.cuda
 
 
 def _stream(stream) -> int | None:
     if stream is None:
+        if _cuda is None:
+            _use_torch()
         # the current stream's handle without a Stream object (0.2 us against
         # 2.9: as long as the C call itself)
-        if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
+        if _raw_stream is not None and _raw_device is not None and _cuda.is_initialized():
             return _raw_stream(_raw_device())
-        return int(torch.cuda.current_stream().cuda_stream)
+        return int(_cuda.current_stream().cuda_stream)
     if isinstance(stream, int):
         return stream
     return int(stream.cuda_stream)
@@ -605,16 +619,11 @@ def pa_rope_status(*, rotary_dim, layout=PA_ROPE_HALF, base=10000.0, scaling=PA_
     return st
 
 
-_BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
-_PLAIN_CACHES = {torch.bfloat16: PA_KV_BF16, torch.uint8: PA_KV_FP8_E4M3}
-_SCALED_CACHES = {torch.uint8: PA_KV_FP8_E4M3_BLOCK, torch.int8: PA_KV_INT8_BLOCK}
-
-
 def _here(what: str, *tensors):
     """Refuse tensors that kernels on the current device cannot read (one left
     on the host among them)."""
     device = tensors[0].get_device()   # (-1: the host)
-    if device >= 0 and device == (_raw_device or torch.cuda.current_device)():
+    if device >= 0 and device == (_raw_device or _cuda.current_device)():
         for t in tensors:
             if t.get_device() != device:
                 break
@@ -635,6 +644,8 @@ def _rows(t, d: int, name: str) -> int:
 def pa_rotary(rope: Rope, x, positions, out, stream=None):
     """out = x (bf16 [T, H, D], token stride free) rotated by positions (int32
     [T]); out may be x."""
+    if _cuda is None:
+        _use_torch()
     shape = T, H, D = x.shape
     xs, os_ = _rows(x, D, "x"), _rows(out, D, "out")
     if out.shape != shape or positions.dtype is not _I32 or positions.numel() != T or not positions.is_contiguous():
@@ -656,6 +667,8 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
     value_scales (float [num_blocks, Hkv])."""
     if rope is not None and not rope.handle:   # (without a rotation keys would be stored as they are)
         raise ValueError("rope: destroyed")
+    if _cuda is None:
+        _use_torch()
     shape = T, hkv, d = key.shape
     ks, vs = _rows(key, d, "key"), _rows(value, d, "value")
     pool, dtype = key_cache.shape, key_cache.dtype
@@ -711,6 +724,8 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
 
 
 def _attention_args(plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace):
+    if _cuda is None:
+        _use_torch()
     # (element counts: a shape object costs as much as three other questions, and
     # the smallest calls are bound by this thread)
     blocks, slots, heads, d = key_cache.shape

@@ -1,6 +1,9 @@
 """Refusals of the operators' wrappers and steps, and what their plans look
 like, on the CPU (no kernel runs)."""
-import numpy as np
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -114,3 +117,15 @@ def test_steps_refuse_scales_that_do_not_go_with_their_caches(kind):
                      lambda: gs.capture(None, *rows[3:], *s), lambda: gs.enqueue(None, *rows[3:], None, *s)):
             with pytest.raises(ValueError, match="scales"):
                 call()
+
+
+def test_binding_without_torch():
+    """Plans, their metadata and rotations do not need torch."""
+    code = ("import sys; sys.modules['torch'] = None\n"
+            "from paged_kv_cache_16_gb300 import binding\n"
+            "p = binding.pa_plan(num_heads_q=4, num_heads_kv=2, head_dim=64, num_blocks=9, query_start_loc=[0, 1],\n"
+            "                    seq_lens=[20], num_computed_tokens=[19], max_blocks_per_req=2, softmax_scale=0.1, num_sms=4)\n"
+            "assert p.info()['num_tokens'] == 1 and binding.pa_plan_metadata_bytes(p) > 0\n"
+            "assert binding.pa_rope_create(rotary_dim=8).frequencies()[1] == 1.0\n")
+    subprocess.run([sys.executable, "-c", code], check=True,
+                   cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
