@@ -15,6 +15,11 @@ KV_DTYPES = {"bf16": binding.PA_KV_BF16, "fp8": binding.PA_KV_FP8_E4M3, "fp8_blo
              "int8_block": binding.PA_KV_INT8_BLOCK}
 
 
+def kv_dtype(name: str) -> int:
+    """The cache type of a name; every other name ("auto", "bfloat16") is bf16."""
+    return KV_DTYPES.get(name, binding.PA_KV_BF16)
+
+
 def _check_scales(scaled: bool, key_scales, value_scales):
     """Block-scaled steps come with both scales, others with none: the cache's type
     follows from them, so that codes would be written as another type's."""
@@ -68,7 +73,7 @@ class DeviceStep:
                                num_common_prefix_blocks=b.num_common_prefix_blocks,
                                softmax_scale=b.softmax_scale, num_sms=self.num_sms,
                                block_size=b.block_size,
-                               kv_cache_dtype=KV_DTYPES[b.kv_cache_dtype], k_scale=b.k_scale, v_scale=b.v_scale)
+                               kv_cache_dtype=kv_dtype(b.kv_cache_dtype), k_scale=b.k_scale, v_scale=b.v_scale)
 
     @property
     def error_word(self) -> torch.Tensor:
@@ -227,7 +232,7 @@ class GraphStep:
         self.model = dict(num_heads_q=num_heads_q, num_heads_kv=num_heads_kv, head_dim=head_dim,
                           num_blocks=num_blocks, max_blocks_per_req=max_blocks_per_req,
                           softmax_scale=softmax_scale, num_sms=num_sms,
-                          kv_cache_dtype=KV_DTYPES[kv_cache_dtype],
+                          kv_cache_dtype=kv_dtype(kv_cache_dtype),
                           k_scale=k_scale, v_scale=v_scale)
         self.shape = dict(max_tokens=max_tokens, max_reqs=max_reqs, max_extend_tiles=max_extend_tiles,
                           max_dequant_blocks=max_dequant_blocks, max_partial_slots=max_partial_slots)
@@ -454,7 +459,7 @@ class NativeGraphStep:
                        decode_prefix_tokens=decode_prefix_tokens),
             host=host, buffers=bufs, num_reqs=0, fused=fused, num_heads_q=num_heads_q, num_heads_kv=num_heads_kv,
             head_dim=head_dim, num_blocks=num_blocks, softmax_scale=softmax_scale, num_sms=num_sms,
-            kv_cache_dtype=KV_DTYPES[kv_cache_dtype], k_scale=k_scale, v_scale=v_scale)
+            kv_cache_dtype=kv_dtype(kv_cache_dtype), k_scale=k_scale, v_scale=v_scale)
         self._last = None   # graph index of the last step launched
         self._keep = (key_cache, value_cache)
 

@@ -222,10 +222,11 @@ def make_batch(*, name: str, num_heads_q: int, num_heads_kv: int, head_dim: int,
     key_scales = value_scales = None
     if fp8:
         kc, vc = _to_e4m3(kc, k_scale), _to_e4m3(vc, v_scale)
-    elif kv_cache_dtype != "bf16":
+    elif kv_cache_dtype in ("fp8_block", "int8_block"):
         (kc, key_scales), (vc, value_scales) = (_to_block_codes(c, kv_cache_dtype, gen_pool) for c in (kc, vc))
         key_scales[poison_block] = value_scales[poison_block] = float("nan")
-    poison_fn = {"bf16": _poison_values, "int8_block": _poison_int8}.get(kv_cache_dtype, _poison_codes)
+    poison_fn = {"fp8": _poison_codes, "fp8_block": _poison_codes, "int8_block": _poison_int8}.get(kv_cache_dtype,
+                                                                                                _poison_values)
 
     # Poison: (a) the padding block, (b) every slot at or past num_computed in
     # a request's own (unshared) blocks -- the new tokens' destinations and

@@ -129,3 +129,15 @@ def test_binding_without_torch():
             "assert binding.pa_rope_create(rotary_dim=8).frequencies()[1] == 1.0\n")
     subprocess.run([sys.executable, "-c", code], check=True,
                    cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+@pytest.mark.parametrize("name", ["auto", "bfloat16"])
+def test_other_cache_type_names_are_bf16(name):
+    a, b = small_batch("bf16"), small_batch(name)
+    for x, y in ((a.key_cache, b.key_cache), (a.value_cache, b.value_cache)):
+        assert y.dtype == torch.bfloat16 and torch.equal(x, y)
+    assert b.key_scales is None and DeviceStep(b, "cpu", num_sms=4).plan.workspace_bytes == \
+        DeviceStep(a, "cpu", num_sms=4).plan.workspace_bytes
+    gs = GraphStep(num_heads_q=4, num_heads_kv=2, head_dim=128, num_blocks=8, max_blocks_per_req=3, softmax_scale=0.1,
+                   max_tokens=8, max_reqs=4, kv_cache_dtype=name, num_sms=4, device="cpu")
+    assert gs.model["kv_cache_dtype"] == binding.PA_KV_BF16
