@@ -5,8 +5,10 @@
 //   (x, y) -> mag * (x cos a - y sin a,  y cos a + x sin a).
 // Angles of far positions are exact to 2^-32 of a turn without 64-bit floating
 // point: the planner gives f_i as a fraction of a turn in 64-bit fixed point, so
-// p * step_i wraps to the fraction of a turn by itself, and its top 32 bits go
-// to sincospif.  cos and sin of the tokens of a CTA are computed once into
+// p * step_i wraps to the fraction of a turn by itself, whose top 32 bits are used:
+// 24 of them through sincospif, the rest as a turn of the result by that little
+// (without it the angle is off by up to 2^-26 of a turn: 9.4e-8, more than the
+// rounding of cos and sin).  cos and sin of the tokens of a CTA are computed once into
 // shared memory and used by all of its heads.  Arithmetic in fp32, one
 // rounding at the end.
 #include "dev.cuh"
@@ -20,10 +22,13 @@ constexpr int kThreads = 256;
 
 __device__ __forceinline__ void cos_sin(uint64_t step, int32_t pos, float mag, float &c, float &s) {
     const uint64_t turn = static_cast<uint64_t>(static_cast<int64_t>(pos)) * step;
-    const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-    sincospif(half_turns, &s, &c);
-    c *= mag;
-    s *= mag;
+    const int32_t t = static_cast<int32_t>((turn + 0x80000000u) >> 32);   // of 2^-31 half a turn, to nearest
+    const float head = __int2float_rz(t);                 // (towards 0: exact on the way back)
+    sincospif(head * 0x1p-31f, &s, &c);
+    const float rest = static_cast<float>(t - static_cast<int32_t>(head)) * 1.462918079e-9f;   // pi 2^-31
+    const float c1 = fmaf(-rest, s, c), s1 = fmaf(rest, c, s);
+    c = c1 * mag;
+    s = s1 * mag;
 }
 
 // cos and sin of `n` tokens: tab[j * rd + i] = cos, tab[j * rd + rd / 2 + i] = sin
