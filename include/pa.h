@@ -159,7 +159,7 @@ typedef struct {
     int32_t num_merge_rows;        /* tokens whose output is merged from partials     */
     int32_t kernels_per_call;      /* kernel launches one pa_attention call makes     */
     int32_t num_dequant_blocks;    /* 8-bit caches: blocks the tensor-core tiles read,
-                                      expanded to bf16 in the workspace each call   */
+                                      expanded to 16 bits in the workspace each call */
     int64_t decode_kv_bytes;       /* K+V bytes the decode kernel's rows must read    */
     int64_t prefix_kv_bytes;       /* K+V bytes of the shared prefix (read once)      */
     double  extend_flops;          /* 4*D*Hq * visible (query, key) pairs, extend     */
@@ -269,7 +269,9 @@ pa_status pa_write_kv_fp8(const void *key, const void *value, const int64_t *slo
  * The result depends only on the metadata and the logical contents: physical
  * block placement does not change a single bit of it.  Slots past seq_len in a
  * request's last block are never used (their contents may be anything,
- * including NaN).  Returns PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_INVALID_ARGUMENT
+ * including NaN).  A NaN or infinity among the values of a step's own rows may
+ * reach rows of the same request that stand up to 255 tokens before it in the step
+ * (a weight of 0 times it).  Returns PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_INVALID_ARGUMENT
  * (NULL or misaligned pointer) or PA_ERR_CUDA (launch failure).  Equivalent to
  * pa_upload_metadata then pa_attention_launch, plus the optional timing events.
  *
@@ -462,7 +464,8 @@ pa_status pa_attention_with_kv_update_launch_staged(const pa_plan_t *plan, const
  *   key_cache,
  *   value_cache      DEVICE, 16-byte aligned, [num_blocks][16][Hkv][D] of
  *                    kv_cache_dtype (any PA_KV_*; code 0 of a block-scaled
- *                    cache reads 0 under every scale, so scales stay)
+ *                    cache reads 0 under every finite scale, so scales stay; a
+ *                    NaN scale stays one until an append starts its block anew)
  * Returns PA_ERR_INVALID_ARGUMENT for a negative count or size, a NULL or
  * misaligned pointer, or an unknown kv_cache_dtype; PA_ERR_CUDA on a launch
  * failure.  Enqueue before the step's pa_write_kv.
@@ -527,9 +530,9 @@ pa_status pa_rope_frequencies(const pa_rope_t *rope, double *frequencies, double
 
 /*
  * out[t][h] = row x[t][h] rotated by positions[t], for t < num_tokens and
- * h < num_heads: products and sums in binary32, angles exact to 2^-32 of a
- * turn at every int32 position, one rounding to bf16 (elements that pass through
- * are bit copies up to the quieting of NaNs).
+ * h < num_heads: angles exact to 2^-32 of a turn at every int32 position, their
+ * cos and sin, products and sums in binary32, one rounding to bf16 (elements that
+ * pass through are bit copies up to the quieting of NaNs).
  *   x, out      DEVICE bf16, 16-byte aligned; heads head_dim apart, tokens
  *               x_stride / out_stride elements apart (>= num_heads * head_dim, a
  *               multiple of 8), so views of a packed projection output work,
@@ -615,10 +618,18 @@ pa_status pa_append_kv(const pa_rope_t *rope, const pa_append_args *args, void *
  *                  below 2^-100 is read as 2^-100); a NaN scale makes the
  *                  outputs that read the block NaN.  Only scales of blocks that
  *                  are read are looked at
- * Codes and scales are used exactly (scales in binary32; softmax weights rounded
- * to f16), whatever the scales' spread.  Rows on the tensor-core tiles read 16-bit
- * copies of the codes, made on the way in the workspace.  All other arguments,
- * errors and ordering as for pa_attention / pa_attention_launch.
+ * Codes are used exactly, scales in binary32.  What is rounded beside the output:
+ *   weights   a key's softmax weight times its block's value scale to f16: to
+ *             2^-11 of itself, or to 2^-24 of the row's largest such product where
+ *             it is below 2^-14 of that.  Keys whose product is below 2^-24 of the
+ *             largest add nothing to the sum of values; all count in the sum of
+ *             weights, as long as the value scales that a row reads lie within
+ *             2^100 of one another
+ *   queries   decode and verify rows, to f16 relative to the row's largest
+ *             magnitude: elements below 2^-17 of it to 2^-25 of it (chunk rows: not)
+ * Rows on the tensor-core tiles read 16-bit copies of the codes (K bf16, V f16,
+ * exact), made on the way in the workspace.  All other arguments, errors and
+ * ordering as for pa_attention / pa_attention_launch.
  */
 pa_status pa_attention_scaled(const pa_plan_t *plan, const void *q, const void *key_cache, const void *value_cache,
                               const float *key_scales, const float *value_scales, const int32_t *block_table,

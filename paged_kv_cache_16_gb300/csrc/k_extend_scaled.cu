@@ -13,8 +13,8 @@
 // kernel as one 16-byte record, travel with the V stage, which is not given back
 // before its weights have been used: a softmax warp waits for it under QK^T.
 //
-// Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 203 us at
-// 2070 MHz, 1692 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
+// Two chunks of 2048 tokens over 2304 and 4864 (Hq 32, Hkv 8, D 128): 204 us at
+// 2070 MHz, 1516 TFLOP/s, where the kernel of the E4M3 caches with one scale takes
 // 244.  A step of 128 keys has 2048 cycles of MMAs and takes ~2800 (tensor pipe
 // active 68%, issue 43%): what the MMA warp does between two MMAs, and the chain
 // S -> softmax -> P of a sub-tile (~1500 cycles), which its own PV and QK^T follow.

@@ -89,3 +89,15 @@ def test_queries_at_the_ends_of_the_bf16_range(code, q_size):
     """Magnitudes beyond 2^100 and below 2^-100 on the split-KV kernel (the softmax
     scale undoes them)."""
     check(oc.Case(hq=8, hkv=2, d=128, q_lens=[1, 3], seq_lens=[100, 50], code=code, q_size=q_size))
+
+
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("num_sms", [3, 152])
+def test_value_scales_far_apart(code, num_sms):
+    """Value scales of 2^-64 and 2^36 in one row: keys whose products with the small
+    scales are lost still count in the sum of the weights."""
+    c = oc.Case(hq=8, hkv=2, d=128, q_lens=[1, 4, 1, 60], seq_lens=[700, 90, 333, 200], code=code, seed=9)
+    used = torch.isfinite(c.vs)
+    small = torch.rand(c.vs.shape, generator=torch.Generator().manual_seed(1)) < 0.5
+    c.vs = torch.where(used, torch.where(small, 2.0 ** -64, 2.0 ** 36), c.vs)
+    check(c, num_sms=num_sms)
