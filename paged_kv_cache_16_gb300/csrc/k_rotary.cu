@@ -205,7 +205,7 @@ __device__ __forceinline__ void rotate_rows(const float *tab, const RopeParams &
     }
 }
 
-// Bound by HBM (8192 tokens x 40 heads of 128: 26.3 us, 6.4 TB/s; 43.3 us with
+// Bound by HBM (8192 tokens x 40 heads of 128: 26.5 us, 6.3 TB/s; 43.3 us with
 // cos and sin read from shared memory per row, 8-byte pieces and one row of a thread
 // in flight) and by the launch for a decode step (64 tokens: 1.8 us).  A CTA's rows
 // are asked into L2 before its table of cos and sin is made, from 1 MB of rows on
