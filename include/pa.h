@@ -19,6 +19,12 @@
  *                    every cache type (block-scaled 8-bit caches included);
  *   pa_attention_scaled
  *                    device: attention over block-scaled 8-bit caches;
+ *   pa_plan_window   host: a plan whose queries see a sliding window and a few
+ *                    first tokens, for every attention call;
+ *   pa_rotary_axes,
+ *   pa_append_kv_axes
+ *                    device: rotation and rotating cache write with positions on
+ *                    several axes (time, height, width);
  *   pa_attention_with_kv_update
  *                    device: the cache write and attention as one call (§6.1,
  *                    fused dispatch).
@@ -343,6 +349,37 @@ pa_status pa_plan_fixed(const pa_batch_desc *desc, const pa_fixed_shape *shape, 
                         size_t *workspace_bytes);
 
 /*
+ * pa_plan / pa_plan_fixed (shape not NULL) for layers whose queries see a sliding
+ * window and a few first tokens: the query at position p sees key j <= p where
+ *   p - j < window  or  j < sink_tokens
+ * (window 1: itself alone; one that reaches past position 0 hides nothing).  The
+ * attention calls take the plan as they take others, by its kv_cache_dtype: the
+ * window is a model field of the plan, and a layer with another window wants
+ * another plan (and another upload into its workspace).  Rows, slots and
+ * block_table are those of the whole context, with any blocks that no query of the
+ * step sees given back: of request r the blocks from
+ * ceil(min(sink_tokens, seq_lens[r]) / 16) up to
+ * (num_computed_tokens[r] - window + 1) / 16, rounded down, are never read, and
+ * their table entries neither read nor checked (any value).
+ * A hidden key plays no part, whatever it holds, with one exception: a NaN or an
+ * infinity among the values of a key that some rows of a request see may also
+ * reach rows of the same request within 255 tokens of one that sees it (a weight of
+ * 0 times it).
+ * Fixed shapes: window and sink_tokens count as model fields, as the kernels'
+ * arguments hold them.  max_dequant_blocks counts blocks that some query sees.
+ * Errors: as pa_plan / pa_plan_fixed, plus PA_ERR_INVALID_ARGUMENT for a NULL
+ * window, window <= 0 or sink_tokens < 0, and PA_ERR_UNSUPPORTED for
+ * num_common_prefix_blocks > 0 (a window leaves no prefix in common).
+ */
+typedef struct {
+    int32_t window;              /* > 0                                               */
+    int32_t sink_tokens;         /* >= 0                                              */
+} pa_window_desc;
+
+pa_status pa_plan_window(const pa_batch_desc *desc, const pa_window_desc *window, const pa_fixed_shape *shape,
+                         pa_plan_t **out, size_t *workspace_bytes);
+
+/*
  * Copy the plan's metadata into the workspace (stream ordered, from a pinned
  * host buffer the plan owns) and prepare the kernels the plan launches.  Not
  * for stream capture.  Arguments and errors as for pa_attention.
@@ -550,6 +587,46 @@ pa_status pa_rotary(const pa_rope_t *rope, const void *x, int64_t x_stride, cons
                     void *stream);
 
 /*
+ * Rotary positions on several axes (time, height and width of video and images,
+ * row and column of an image): a token has a position on each of num_axes axes, and
+ * pair i turns by the one on axis_of_pair[i],
+ *   a = p[axis_of_pair[i]] * f_i.
+ * PA_ROPE_AXES_SHARED: f_i as above, over all rotary_dim / 2 pairs (tokens that
+ * stand at one position on every axis turn as they do without axes).
+ * PA_ROPE_AXES_OWN: the k-th of an axis's m pairs has the f_k, scaling included, of
+ * a rotation of 2 m elements (m as for rotary_dim).
+ * Everything else is as pa_rope_create has it; pa_rope_destroy and
+ * pa_rope_frequencies take the result.  Rotations of more than one axis go with the
+ * calls that take positions per axis: pa_rotary and pa_append_kv refuse them.
+ * Errors: as pa_rope_create, plus PA_ERR_INVALID_ARGUMENT for NULL axes or
+ * axis_of_pair, num_axes < 1, an axis outside [0, num_axes) or an unknown
+ * `frequencies`; PA_ERR_UNSUPPORTED for num_axes > 4.
+ */
+#define PA_ROPE_AXES_SHARED 0
+#define PA_ROPE_AXES_OWN 1
+
+typedef struct {
+    int32_t num_axes;              /* 1 .. 4                                             */
+    int32_t frequencies;           /* PA_ROPE_AXES_*                                     */
+    const int32_t *axis_of_pair;   /* HOST [rotary_dim / 2], read during the call only   */
+} pa_rope_axes_desc;
+
+pa_status pa_rope_create_axes(const pa_rope_desc *desc, const pa_rope_axes_desc *axes, pa_rope_t **out);
+
+/*
+ * pa_rotary with positions on the rotation's axes (one axis included):
+ *   positions    DEVICE int32 [num_axes][axis_stride], token t of axis a at
+ *                a * axis_stride + t, negative ones too
+ *   axis_stride  >= num_tokens (a buffer of a larger capacity), or 0: one row of
+ *                positions that counts for every axis
+ * Other arguments and errors as for pa_rotary, plus PA_ERR_INVALID_ARGUMENT for
+ * another axis_stride.
+ */
+pa_status pa_rotary_axes(const pa_rope_t *rope, const void *x, int64_t x_stride, const int32_t *positions,
+                         int64_t axis_stride, int32_t num_tokens, int32_t num_heads, int32_t head_dim, void *out,
+                         int64_t out_stride, void *stream);
+
+/*
  * The step's cache write with the rotation on the way, one launch: token i of
  * request r at position p = num_computed[r] + i goes to slot p % 16 of block
  * block_table[r][p / 16] (pa_slot_mapping's slot), its key rotated by p, its
@@ -608,6 +685,19 @@ typedef struct {
  * rope), PA_ERR_UNSUPPORTED (block_size, head_dim, num_blocks * 16 >= 2^31),
  * PA_ERR_CUDA.  Enqueue before the step's attention on the same stream. */
 pa_status pa_append_kv(const pa_rope_t *rope, const pa_append_args *args, void *stream);
+
+/*
+ * pa_append_kv with keys and queries rotated by positions given per token and axis:
+ * token row t turns by positions[a * axis_stride + t] (as for pa_rotary_axes;
+ * axis_stride >= num_tokens or 0), while its slot goes by num_computed_tokens as
+ * before: the tokens of an image take more slots than positions.  rope must not be
+ * NULL; a rotation of one axis does too (positions other than the slots' then).
+ * Positions of rows from query_start_loc[num_reqs] on are not read.
+ * Errors: as pa_append_kv, plus PA_ERR_INVALID_ARGUMENT for a NULL rope, NULL or
+ * misaligned positions, or another axis_stride.
+ */
+pa_status pa_append_kv_axes(const pa_rope_t *rope, const pa_append_args *args, const int32_t *positions,
+                            int64_t axis_stride, void *stream);
 
 /*
  * pa_attention and pa_attention_launch for plans of block-scaled caches

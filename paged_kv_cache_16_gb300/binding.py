@@ -34,6 +34,8 @@ PA_ROPE_SCALE_NONE = 0
 PA_ROPE_SCALE_LINEAR = 1
 PA_ROPE_SCALE_WAVELENGTH = 2
 PA_ROPE_SCALE_YARN = 3
+PA_ROPE_AXES_SHARED = 0
+PA_ROPE_AXES_OWN = 1
 
 PA_DEVERR_SLOT_RANGE = 0x1
 PA_DEVERR_BLOCK_RANGE = 0x2
@@ -48,7 +50,8 @@ EXPORTED = ("pa_plan", "pa_plan_destroy", "pa_plan_get_info", "pa_slot_mapping",
             "pa_plan_copy_metadata", "pa_upload_metadata_from", "pa_graph_create", "pa_graph_step",
             "pa_graph_turn", "pa_graph_wait", "pa_graph_workspace", "pa_graph_slot_mapping", "pa_graph_destroy",
             "pa_attention_with_kv_update_launch_staged", "pa_rope_create", "pa_rope_destroy", "pa_rope_frequencies",
-            "pa_rotary", "pa_append_kv", "pa_attention_scaled", "pa_attention_scaled_launch")
+            "pa_rotary", "pa_append_kv", "pa_attention_scaled", "pa_attention_scaled_launch", "pa_plan_window",
+            "pa_rope_create_axes", "pa_rotary_axes", "pa_append_kv_axes")
 
 
 class PaError(RuntimeError):
@@ -150,6 +153,21 @@ class RopeDesc(ctypes.Structure):
         ("low", ctypes.c_double),
         ("high", ctypes.c_double),
         ("attention_factor", ctypes.c_double),
+    ]
+
+
+class RopeAxesDesc(ctypes.Structure):
+    _fields_ = [
+        ("num_axes", ctypes.c_int32),
+        ("frequencies", ctypes.c_int32),
+        ("axis_of_pair", ctypes.c_void_p),         # const int32_t * (host)
+    ]
+
+
+class WindowDesc(ctypes.Structure):
+    _fields_ = [
+        ("window", ctypes.c_int32),
+        ("sink_tokens", ctypes.c_int32),
     ]
 
 
@@ -276,6 +294,15 @@ def load(path: str | None = None, build_if_missing: bool = False) -> ctypes.CDLL
     lib.pa_attention_scaled.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
     lib.pa_attention_scaled_launch.restype = ctypes.c_int
     lib.pa_attention_scaled_launch.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.pa_plan_window.restype = ctypes.c_int
+    lib.pa_plan_window.argtypes = [ctypes.POINTER(BatchDesc), ctypes.POINTER(WindowDesc), ctypes.POINTER(FixedShape),
+                                   ctypes.POINTER(vp), ctypes.POINTER(sz)]
+    lib.pa_rope_create_axes.restype = ctypes.c_int
+    lib.pa_rope_create_axes.argtypes = [ctypes.POINTER(RopeDesc), ctypes.POINTER(RopeAxesDesc), ctypes.POINTER(vp)]
+    lib.pa_rotary_axes.restype = ctypes.c_int
+    lib.pa_rotary_axes.argtypes = [vp, vp, i64, vp, i64, i32, i32, i32, vp, i64, vp]
+    lib.pa_append_kv_axes.restype = ctypes.c_int
+    lib.pa_append_kv_axes.argtypes = [vp, ctypes.POINTER(AppendArgs), vp, i64, vp]
     if path is None:
         _LIB = lib
     return lib
@@ -341,6 +368,8 @@ class Plan:
     # what the tensors of its calls have to be: (kv_cache_dtype, elements of q and
     # out, num_blocks, kv heads, head_dim, elements of the block table, its width)
     _step: tuple | None = None
+    window: tuple | None = None   # (window, sink_tokens) of pa_plan_window
+    heads_q: int = 0              # with a window
 
     def info(self) -> dict:
         pi = PlanInfo()
@@ -436,6 +465,35 @@ def pa_plan_fixed_status(*, max_tokens, max_reqs, max_extend_tiles=0, max_dequan
     return st
 
 
+def _plan_window(window, sink_tokens, shape, kw):
+    d, keep = make_desc(**kw)
+    fs = _fixed_shape(**shape) if shape else None
+    handle = ctypes.c_void_p()
+    ws = ctypes.c_size_t()
+    st = load().pa_plan_window(ctypes.byref(d), ctypes.byref(WindowDesc(int(window), int(sink_tokens))),
+                               ctypes.byref(fs) if fs is not None else None, ctypes.byref(handle), ctypes.byref(ws))
+    rows = fs.max_tokens if fs is not None else int(keep[0][-1]) if len(keep[0]) else 0
+    return st, handle.value, lambda: Plan(handle.value, ws.value, keep, _step_of(d, rows), (int(window), int(sink_tokens)),
+                                     d.num_heads_q)
+
+
+def pa_plan_window(*, window, sink_tokens=0, shape: dict | None = None, **kw) -> Plan:
+    """A plan whose queries see the last ``window`` keys and the first
+    ``sink_tokens`` (see pa.h); ``shape``: the arguments of pa_plan_fixed for a
+    fixed-shape plan."""
+    st, _, plan = _plan_window(window, sink_tokens, shape, kw)
+    _check(st, "pa_plan_window")
+    return plan()
+
+
+def pa_plan_window_status(*, window, sink_tokens=0, shape: dict | None = None, **kw) -> int:
+    """Status code pa_plan_window returns (plan discarded)."""
+    st, handle, _ = _plan_window(window, sink_tokens, shape, kw)
+    if st == PA_OK:
+        load().pa_plan_destroy(handle)
+    return st
+
+
 def pa_plan_status(**kw) -> int:
     """Status code pa_plan returns for this descriptor (plan discarded)."""
     d, keep = make_desc(**kw)
@@ -472,7 +530,47 @@ def pa_write_kv_fp8(key, value, slot_mapping, key_cache, value_cache, k_scale: f
                                   _ptr(device_error_word), _stream(stream)), "pa_write_kv_fp8")
 
 
+def _check_window(plan, q, key_cache, value_cache, block_table, out, *more):
+    """Windowed plans: the kernels go by the plan, so tensors of another step, type or
+    device would be read as what they are not, or past their ends."""
+    if plan.window is None:
+        return
+    if _cuda is None:
+        _use_torch()
+    kind, rows, nb, hkv, dim, entries, width = plan._step
+    dtype = key_cache.dtype
+    if _PLAIN_CACHES.get(dtype) != kind or value_cache.dtype is not dtype or key_cache.shape[1:] != (16, hkv, dim) or \
+            key_cache.shape[0] < nb or value_cache.shape != key_cache.shape or not key_cache.is_contiguous() or \
+            not value_cache.is_contiguous():
+        raise ValueError(f"caches: the plan's type, contiguous [{nb}, 16, {hkv}, {dim}] wanted")
+    if q.dtype is not _BF16 or out.dtype is not _BF16 or q.numel() < rows or out.numel() < rows or \
+            not q.is_contiguous() or not out.is_contiguous():
+        raise ValueError(f"q, out: contiguous bf16, all of the plan's rows wanted ({rows} elements)")
+    if block_table.dtype is not _I32 or not block_table.is_contiguous() or block_table.numel() < entries or \
+            block_table.shape[-1] != width:
+        raise ValueError(f"block_table: contiguous int32, the plan's requests and its {width} blocks each wanted")
+    _here("q, caches, block table, out, workspace", q, key_cache, value_cache, block_table, out,
+          *(t for t in more if t is not None))
+
+
+def _check_new_rows(plan, key, value, slot_mapping):
+    """The new rows of a fused call with a windowed plan."""
+    if plan.window is None:
+        return
+    import torch
+    _, rows, _, hkv, dim, _, _ = plan._step
+    tokens = rows // (plan.heads_q * dim)
+    need = tokens * hkv * dim
+    for t in (key, value):
+        if t.dtype is not _BF16 or not t.is_contiguous() or t.numel() < need:
+            raise ValueError(f"key, value: contiguous bf16, all of the plan's rows wanted ({need} elements)")
+    if slot_mapping is not None and (slot_mapping.dtype is not torch.int64 or slot_mapping.numel() < tokens or
+                                     not slot_mapping.is_contiguous()):
+        raise ValueError("slot_mapping: contiguous int64, one per row of the plan wanted")
+
+
 def pa_attention(plan: Plan, q, key_cache, value_cache, block_table, out, workspace, stream=None):
+    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace)
     nbytes = workspace.numel() * workspace.element_size()
     _check(load().pa_attention(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(block_table),
                                _ptr(out), _ptr(workspace), nbytes, _stream(stream)), "pa_attention")
@@ -509,6 +607,7 @@ def pa_upload_metadata_from(host_src, nbytes: int, workspace, stream=None):
 
 def pa_attention_launch(plan: Plan, q, key_cache, value_cache, block_table, out, workspace, stream=None):
     """The attention kernels alone (capturable in a CUDA graph; see pa.h)."""
+    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace)
     nbytes = workspace.numel() * workspace.element_size()
     _check(load().pa_attention_launch(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(block_table),
                                       _ptr(out), _ptr(workspace), nbytes, _stream(stream)), "pa_attention_launch")
@@ -517,6 +616,8 @@ def pa_attention_launch(plan: Plan, q, key_cache, value_cache, block_table, out,
 def pa_attention_with_kv_update(plan: Plan, q, key, value, key_cache, value_cache, block_table, out, workspace,
                                 slot_mapping=None, stream=None):
     """Cache write + attention in one call (see pa.h)."""
+    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace, key, value, slot_mapping)
+    _check_new_rows(plan, key, value, slot_mapping)
     nbytes = workspace.numel() * workspace.element_size()
     _check(load().pa_attention_with_kv_update(plan.handle, _ptr(q), _ptr(key), _ptr(value), _ptr(key_cache),
                                               _ptr(value_cache), _ptr(block_table), _ptr(slot_mapping), _ptr(out),
@@ -526,6 +627,8 @@ def pa_attention_with_kv_update(plan: Plan, q, key, value, key_cache, value_cach
 
 def pa_attention_with_kv_update_launch(plan: Plan, q, key, value, key_cache, value_cache, block_table, out,
                                        workspace, slot_mapping=None, stream=None):
+    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace, key, value, slot_mapping)
+    _check_new_rows(plan, key, value, slot_mapping)
     nbytes = workspace.numel() * workspace.element_size()
     _check(load().pa_attention_with_kv_update_launch(plan.handle, _ptr(q), _ptr(key), _ptr(value), _ptr(key_cache),
                                                      _ptr(value_cache), _ptr(block_table), _ptr(slot_mapping),
@@ -540,6 +643,8 @@ def pa_attention_with_kv_update_launch_staged(plan: Plan, q, key, value, key_cac
     prefix on may still be written until late_rows (a torch.cuda.Event,
     already recorded) fires.  late_out_ready (a torch.cuda.Event) is recorded
     once out's rows from the prefix on are final."""
+    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace, key, value, slot_mapping)
+    _check_new_rows(plan, key, value, slot_mapping)
     nbytes = workspace.numel() * workspace.element_size()
     if late_out_ready is not None and not late_out_ready.cuda_event:
         late_out_ready.record()   # torch creates the CUDA event at its first record
@@ -563,6 +668,8 @@ def pa_attention_no_alloc(plan: Plan, q, key_cache, value_cache, block_table, ou
                           stream=None):
     """pa_attention with the library's fixed scratch array instead of a workspace
     (for callers that cannot allocate device memory; see pa.h)."""
+    _check_window(plan, q, key_cache, value_cache, block_table, out,
+                  None if isinstance(device_error_word, int) else device_error_word)
     _check(load().pa_attention_no_alloc(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache),
                                         _ptr(block_table), _ptr(out), _ptr(device_error_word), _stream(stream)),
            "pa_attention_no_alloc")
@@ -574,6 +681,7 @@ class Rope:
     number of calls, streams and captured graphs."""
     handle: int
     rotary_dim: int
+    num_axes: int = 1
 
     def frequencies(self):
         """(angles per position [rotary_dim / 2] as float64, factor on cos and sin)"""
@@ -619,6 +727,32 @@ def pa_rope_status(*, rotary_dim, layout=PA_ROPE_HALF, base=10000.0, scaling=PA_
     return st
 
 
+def _axes_desc(rotary_dim, num_axes, axis_of_pair, frequencies):
+    axis = np.ascontiguousarray(axis_of_pair, dtype=np.int32)
+    if axis.ndim != 1 or 2 * axis.size != rotary_dim:
+        raise ValueError("axis_of_pair: an axis for each of the rotary_dim / 2 pairs wanted")
+    return RopeAxesDesc(int(num_axes), int(frequencies), axis.ctypes.data), axis
+
+
+def pa_rope_create_axes(*, num_axes, axis_of_pair, rotary_dim, frequencies=PA_ROPE_AXES_SHARED, layout=PA_ROPE_HALF,
+                        base=10000.0, scaling=PA_ROPE_SCALE_NONE, factor=1.0, original_max_position=0, low=1.0, high=4.0,
+                        attention_factor=0.0) -> Rope:
+    """Build a rotation with positions on several axes (host only, see pa.h)."""
+    d = _rope_desc(rotary_dim, layout, base, scaling, factor, original_max_position, low, high, attention_factor)
+    axes, _keep = _axes_desc(rotary_dim, num_axes, axis_of_pair, frequencies)
+    h = ctypes.c_void_p()
+    _check(load().pa_rope_create_axes(ctypes.byref(d), ctypes.byref(axes), ctypes.byref(h)), "pa_rope_create_axes")
+    return Rope(h.value, int(rotary_dim), int(num_axes))
+
+
+def _axis_stride(rope: Rope, positions, num_tokens: int) -> int:
+    """Elements between the axes of positions (int32 [axes, tokens], tokens dense)."""
+    if positions.dtype is not _I32 or positions.shape != (rope.num_axes, num_tokens) or \
+            (num_tokens > 1 and positions.stride(1) != 1):
+        raise ValueError(f"positions: int32 [{rope.num_axes}, {num_tokens}] with dense rows wanted")
+    return num_tokens if rope.num_axes == 1 else positions.stride(0)
+
+
 def _here(what: str, *tensors):
     """Refuse tensors that kernels on the current device cannot read (one left
     on the host among them)."""
@@ -658,13 +792,28 @@ def pa_rotary(rope: Rope, x, positions, out, stream=None):
         _check(st, "pa_rotary")
 
 
-def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, block_table, key_cache, value_cache, *,
-                 key_scales=None, value_scales=None, k_scale: float = 1.0, v_scale: float = 1.0, q=None, q_out=None,
-                 device_error_word=None, stream=None):
-    """The cache write with the rotation of key (and q into q_out) on the way
-    (see pa.h).  The cache's type follows from the tensors: bf16; uint8 E4M3
-    codes with k_scale / v_scale; uint8 or int8 codes with key_scales and
-    value_scales (float [num_blocks, Hkv])."""
+def pa_rotary_axes(rope: Rope, x, positions, out, stream=None):
+    """out = x (bf16 [T, H, D], token stride free) rotated by positions on the
+    rotation's axes (int32 [axes, T]; a row expanded to them counts for all); out
+    may be x."""
+    if _cuda is None:
+        _use_torch()
+    shape = T, H, D = x.shape
+    xs, os_ = _rows(x, D, "x"), _rows(out, D, "out")
+    if out.shape != shape:
+        raise ValueError("out: x's shape wanted")
+    apart = _axis_stride(rope, positions, T)
+    _here("x, positions, out", x, positions, out)
+    if T <= 1:   # a single row's stride is anything
+        xs = os_ = H * D
+    st = load().pa_rotary_axes(rope.handle, x.data_ptr(), xs, positions.data_ptr(), apart, T, H, D, out.data_ptr(), os_,
+                               _stream(stream))
+    if st:
+        _check(st, "pa_rotary_axes")
+
+
+def _append_args(rope, key, value, query_start_loc, num_computed, block_table, key_cache, value_cache, key_scales,
+                 value_scales, k_scale, v_scale, q, q_out, device_error_word):
     if rope is not None and not rope.handle:   # (without a rotation keys would be stored as they are)
         raise ValueError("rope: destroyed")
     if _cuda is None:
@@ -715,12 +864,37 @@ def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, b
     if T <= 1:   # a single row's stride is anything
         ks = vs = hkv * d
         qs = os_ = hq * d
-    a = AppendArgs(R, T, hq, hkv, d, bs, nb, mb, kind, k_scale, v_scale, query_start_loc.data_ptr(), num_computed.data_ptr(),
-                   block_table.data_ptr(), key.data_ptr(), value.data_ptr(), ks, vs, qp, op, qs, os_, key_cache.data_ptr(),
-                   value_cache.data_ptr(), ksc, vsc, word)
+    return AppendArgs(R, T, hq, hkv, d, bs, nb, mb, kind, k_scale, v_scale, query_start_loc.data_ptr(), num_computed.data_ptr(),
+                      block_table.data_ptr(), key.data_ptr(), value.data_ptr(), ks, vs, qp, op, qs, os_, key_cache.data_ptr(),
+                      value_cache.data_ptr(), ksc, vsc, word)
+
+
+def pa_append_kv(rope: Rope | None, key, value, query_start_loc, num_computed, block_table, key_cache, value_cache, *,
+                 key_scales=None, value_scales=None, k_scale: float = 1.0, v_scale: float = 1.0, q=None, q_out=None,
+                 device_error_word=None, stream=None):
+    """The cache write with the rotation of key (and q into q_out) on the way
+    (see pa.h).  The cache's type follows from the tensors: bf16; uint8 E4M3
+    codes with k_scale / v_scale; uint8 or int8 codes with key_scales and
+    value_scales (float [num_blocks, Hkv])."""
+    a = _append_args(rope, key, value, query_start_loc, num_computed, block_table, key_cache, value_cache, key_scales,
+                     value_scales, k_scale, v_scale, q, q_out, device_error_word)
     st = load().pa_append_kv(rope.handle if rope is not None else None, a, _stream(stream))
     if st:
         _check(st, "pa_append_kv")
+
+
+def pa_append_kv_axes(rope: Rope, key, value, positions, query_start_loc, num_computed, block_table, key_cache,
+                      value_cache, *, key_scales=None, value_scales=None, k_scale: float = 1.0, v_scale: float = 1.0,
+                      q=None, q_out=None, device_error_word=None, stream=None):
+    """pa_append_kv with rows rotated by positions of their own (int32 [axes, T],
+    see pa.h)."""
+    a = _append_args(rope, key, value, query_start_loc, num_computed, block_table, key_cache, value_cache, key_scales,
+                     value_scales, k_scale, v_scale, q, q_out, device_error_word)
+    apart = _axis_stride(rope, positions, key.shape[0])
+    _here("rows, positions", key, positions)
+    st = load().pa_append_kv_axes(rope.handle, a, positions.data_ptr(), apart, _stream(stream))
+    if st:
+        _check(st, "pa_append_kv_axes")
 
 
 def _attention_args(plan, q, key_cache, value_cache, key_scales, value_scales, block_table, out, workspace):

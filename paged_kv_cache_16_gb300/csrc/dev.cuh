@@ -681,5 +681,37 @@ __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// Rows of a block whose keys some token of an item sees; the others (past the
+// context, or behind every token's window and not among the first tokens) may
+// hold anything.
+template <bool WIN>
+struct LiveRows {
+    int n;   // rows of the context
+    __device__ __forceinline__ LiveRows(int key0, int key_end, int, int) : n(key_end - key0) {}
+    __device__ __forceinline__ bool all() const { return n >= kBlockSize; }
+    __device__ __forceinline__ bool has(int row) const { return row < n; }
+};
+template <>
+struct LiveRows<true> {
+    uint32_t mask;   // bit r: row r
+    // keys in [dead_begin, dead_end) are seen by no token
+    __device__ __forceinline__ LiveRows(int key0, int key_end, int dead_begin, int dead_end) {
+        auto below = [](int n) { return n <= 0 ? 0u : n >= kBlockSize ? 0xFFFFu : (1u << n) - 1u; };
+        mask = below(key_end - key0);
+        if (dead_end > key0) mask &= ~(below(dead_end - key0) & ~below(dead_begin - key0));
+    }
+    __device__ __forceinline__ bool all() const { return mask == 0xFFFFu; }
+    __device__ __forceinline__ bool has(int row) const { return mask >> row & 1u; }
+};
+
+// An item in WindowView's numbers (WIN; else as it is).
+template <bool WIN>
+__device__ __forceinline__ WindowView own_numbers(const DecodeParams &p, DecodeItem &item) {
+    if constexpr (!WIN) return WindowView{0, 0};
+    const WindowView v = window_view(item.key_end - item.n_tok, item.key_end, p.window, p.sinks, 1);
+    item.key_end -= kBlockSize * v.skip;
+    return v;
+}
+
 }  // namespace dev
 }  // namespace pa

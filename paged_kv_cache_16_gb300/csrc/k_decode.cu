@@ -65,7 +65,7 @@ __device__ __forceinline__ int new_row_page(const DecodeItem &item) {
 
 template <int D, bool KV8>
 __device__ __forceinline__ void store_new_row(const DecodeParams &p, const DecodeItem &item, int lp, int kvh,
-                                              int lane) {
+                                              int lane) {   // lp: the logical block
     const int32_t blk = __ldg(p.block_table + static_cast<int64_t>(item.req) * p.max_blocks + lp);
     const int64_t slot = static_cast<int64_t>(blk) * kBlockSize + (item.key_end - 1) % kBlockSize;
     const bool ok = blk >= 0 && blk < p.num_blocks;   // else: not stored (the page load reports it)
@@ -86,7 +86,11 @@ __device__ __forceinline__ void store_new_row(const DecodeParams &p, const Decod
     fence_proxy_async_global();   // the stores before the async-proxy (TMA) load of the page
 }
 
-template <int D, int HG, bool KV8, bool FUSED>
+// WIN: with a sliding window and first tokens (items in WindowView's numbers, so
+// that the stream and the masks at the context's end are the same; the masks at
+// the window's beginning are applied to the few blocks that reach below the last
+// token's window).
+template <int D, int HG, bool KV8, bool FUSED, bool WIN>
 __global__ void __launch_bounds__((HG + 1) * 32, 1)
 decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
               const DecodeParams p) {
@@ -136,7 +140,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const uint64_t evict_first = policy_evict_first();
         bool ok = true;
         for (int it = item_begin; it < item_end && ok; ++it) {
-            const DecodeItem item = p.items[it];
+            DecodeItem item = p.items[it];
+            const WindowView view = own_numbers<WIN>(p, item);
             const int32_t *bt = p.block_table + static_cast<int64_t>(item.req) * p.max_blocks;
             const int h0 = item.head_group * HG;
             const int new_page = FUSED ? new_row_page(item) : -1;   // load only after its new rows are stored
@@ -145,7 +150,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             for (int pg = item.page_begin; pg < item.page_end; ++pg) {
                 if (pg - window >= 32) {
                     window = pg;
-                    blk_lane = pg + lane < item.page_end ? bt[pg + lane] : 0;
+                    blk_lane = pg + lane < item.page_end ? bt[view.at(pg + lane)] : 0;
                 }
                 const int s = issued % C::NS;
                 const int n = issued / C::NS;
@@ -217,7 +222,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         int consumed = 0;
         bool ok = true;
         for (int it = item_begin; it < item_end && ok; ++it) {
-            const DecodeItem item = p.items[it];
+            DecodeItem item = p.items[it];
+            const WindowView view = own_numbers<WIN>(p, item);
+            // windows begin below low_top, the item's first one at low_min
+            const int low_top = item.key_end - p.window, low_min = low_top - (item.n_tok - 1);
             const int kvh = item.head_group * HG + warp;
             const int nrow = item.n_tok * G;
             if (nrow <= 8) {
@@ -255,7 +263,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 if constexpr (FUSED) {
                     const int lp = new_row_page(item);
                     if (lp >= 0) {
-                        store_new_row<D, true>(p, item, lp, kvh, lane);
+                        store_new_row<D, true>(p, item, view.at(lp), kvh, lane);
                         __syncwarp();
                         if (lane == 0) mbar_arrive(row_ready);
                     }
@@ -273,15 +281,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 // O^T += V^T P^T for one block: lane (g, t) loads the value
                 // rows of keys 2t, 2t + 1, 2t + 8, 2t + 9 at the logical bytes
                 // 64h + 32jr + 4g (dims of rows g + 8jr of m-tiles 4h + i);
-                // MASKED zeroes the codes of rows at or past `valid`
-                auto pv_t = [&](auto masked, uint32_t vb, uint32_t b0, uint32_t b1, int valid) {
+                // MASKED zeroes the codes of rows that are not `live`
+                auto pv_t = [&](auto masked, uint32_t vb, uint32_t b0, uint32_t b1, const LiveRows<WIN> &live) {
                     const uint32_t r0 = vb + 256u * t4;
                     uint32_t mA = ~0u, mB = ~0u, mC = ~0u, mD = ~0u;
                     if constexpr (decltype(masked)::value) {
-                        mA = 2 * t4 < valid ? ~0u : 0u;
-                        mB = 2 * t4 + 1 < valid ? ~0u : 0u;
-                        mC = 2 * t4 + 8 < valid ? ~0u : 0u;
-                        mD = 2 * t4 + 9 < valid ? ~0u : 0u;
+                        mA = live.has(2 * t4) ? ~0u : 0u;
+                        mB = live.has(2 * t4 + 1) ? ~0u : 0u;
+                        mC = live.has(2 * t4 + 8) ? ~0u : 0u;
+                        mD = live.has(2 * t4 + 9) ? ~0u : 0u;
                     }
 #pragma unroll
                     for (int h = 0; h < D / 64; ++h) {
@@ -319,8 +327,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     qk_t(stage(s0) + warp * C::BOX, sa);
                     if constexpr (TWO) qk_t(stage(s1) + warp * C::BOX, sb);
                     const int loaded = TWO ? 2 * kBlockSize : kBlockSize;
-                    const int valid_keys = min(item.key_end - pg * kBlockSize, loaded);   // V rows past it may be anything
-                    if (!TWO || lim_lo - pg * kBlockSize < 2 * kBlockSize) {
+                    const int key0 = pg * kBlockSize;
+                    if (!TWO || lim_lo - key0 < 2 * kBlockSize) {
                         // keys past the context or a row's causal limit drop out
                         const int va = min(lim_a - pg * kBlockSize, loaded), vb = min(lim_b - pg * kBlockSize, loaded);
                         if (g >= va) sa[0] = -INFINITY;
@@ -332,6 +340,21 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                             if (g + 16 >= vb) sb[1] = -INFINITY;
                             if (g + 24 >= va) sb[2] = -INFINITY;
                             if (g + 24 >= vb) sb[3] = -INFINITY;
+                        }
+                    }
+                    if (WIN && key0 < low_top) {
+                        // keys behind a row's window that are not first tokens
+                        const int first = p.sinks - key0, la = lim_a - p.window - key0, lb = lim_b - p.window - key0;
+                        auto behind = [&](int k, int low) { return k >= first && k < low; };
+                        if (behind(g, la)) sa[0] = -INFINITY;
+                        if (behind(g, lb)) sa[1] = -INFINITY;
+                        if (behind(g + 8, la)) sa[2] = -INFINITY;
+                        if (behind(g + 8, lb)) sa[3] = -INFINITY;
+                        if constexpr (TWO) {
+                            if (behind(g + 16, la)) sb[0] = -INFINITY;
+                            if (behind(g + 16, lb)) sb[1] = -INFINITY;
+                            if (behind(g + 24, la)) sb[2] = -INFINITY;
+                            if (behind(g + 24, lb)) sb[3] = -INFINITY;
                         }
                     }
                     float mx0 = fmaxf(sa[0], sa[2]), mx1 = fmaxf(sa[1], sa[3]);
@@ -370,14 +393,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     uint32_t pa0, pa1;
                     weights(sa, pa0, pa1);
                     const uint32_t vb0 = stage(s0) + C::TSTAGE + warp * C::BOX;
-                    if (valid_keys < kBlockSize) pv_t(std::true_type{}, vb0, pa0, pa1, valid_keys);
-                    else pv_t(std::false_type{}, vb0, pa0, pa1, kBlockSize);
+                    const LiveRows<WIN> live0(key0, item.key_end, p.sinks, low_min);
+                    if (!live0.all()) pv_t(std::true_type{}, vb0, pa0, pa1, live0);
+                    else pv_t(std::false_type{}, vb0, pa0, pa1, live0);
                     if constexpr (TWO) {
                         uint32_t pb0, pb1;
                         weights(sb, pb0, pb1);
                         const uint32_t vb1 = stage(s1) + C::TSTAGE + warp * C::BOX;
-                        if (valid_keys < 2 * kBlockSize) pv_t(std::true_type{}, vb1, pb0, pb1, valid_keys - kBlockSize);
-                        else pv_t(std::false_type{}, vb1, pb0, pb1, kBlockSize);
+                        const LiveRows<WIN> live1(key0 + kBlockSize, item.key_end, p.sinks, low_min);
+                        if (!live1.all()) pv_t(std::true_type{}, vb1, pb0, pb1, live1);
+                        else pv_t(std::false_type{}, vb1, pb0, pb1, live1);
                     }
                     __syncwarp();
                     if (lane == 0) {
@@ -472,7 +497,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             if constexpr (FUSED) {
                 const int lp = new_row_page(item);
                 if (lp >= 0) {
-                    store_new_row<D, true>(p, item, lp, kvh, lane);
+                    store_new_row<D, true>(p, item, view.at(lp), kvh, lane);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(row_ready);
                 }
@@ -489,16 +514,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     mma_f16_16816(b, qf[kk], k2, k3);
                 }
             };
-            // O += P V for one block; MASKED zeroes the codes of rows at or
-            // past `valid` (0-weight x NaN would poison the MMA)
-            auto pv = [&](auto masked, uint32_t vb, const uint32_t (&pf)[4], int valid) {
+            // O += P V for one block; MASKED zeroes the codes of rows that are
+            // not `live` (0-weight x NaN would poison the MMA)
+            auto pv = [&](auto masked, uint32_t vb, const uint32_t (&pf)[4], const LiveRows<WIN> &live) {
                 const uint32_t ra = vb + va_lane, rb = vb + vb_lane;
                 uint32_t mA = ~0u, mB = ~0u, mC = ~0u, mD = ~0u;
                 if constexpr (decltype(masked)::value) {
-                    mA = 2 * t4 < valid ? ~0u : 0u;
-                    mB = 2 * t4 + 1 < valid ? ~0u : 0u;
-                    mC = 2 * t4 + 8 < valid ? ~0u : 0u;
-                    mD = 2 * t4 + 9 < valid ? ~0u : 0u;
+                    mA = live.has(2 * t4) ? ~0u : 0u;
+                    mB = live.has(2 * t4 + 1) ? ~0u : 0u;
+                    mC = live.has(2 * t4 + 8) ? ~0u : 0u;
+                    mD = live.has(2 * t4 + 9) ? ~0u : 0u;
                 }
 #pragma unroll
                 for (int a = 0; a < D / 32; ++a) {
@@ -538,14 +563,25 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 // keys past the context (their codes may be NaN) or past the
                 // blocks loaded drop out; raw scores, scaled inside ex2
                 const int loaded = TWO ? 2 * kBlockSize : kBlockSize;
-                const int valid_keys = min(item.key_end - pg * kBlockSize, loaded);   // V rows past it may be anything
-                if (!TWO || lim_min - pg * kBlockSize < 2 * kBlockSize) {
+                const int key0 = pg * kBlockSize;
+                if (!TWO || lim_min - key0 < 2 * kBlockSize) {
                     const int valid0 = min(lim0 - pg * kBlockSize, loaded), valid1 = min(lim1 - pg * kBlockSize, loaded);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (j * 8 + 2 * t4 + (e & 1) >= (e < 2 ? valid0 : valid1)) sc[j][e] = -INFINITY;
+                }
+                if (WIN && key0 < low_top) {
+                    // keys behind a row's window that are not first tokens
+                    const int first = p.sinks - key0, low0 = lim0 - p.window - key0, low1 = lim1 - p.window - key0;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int k = j * 8 + 2 * t4 + (e & 1);
+                            if (k >= first && k < (e < 2 ? low0 : low1)) sc[j][e] = -INFINITY;
+                        }
                 }
                 constexpr int NT = TWO ? 4 : 2;
                 float mx0 = fmaxf(sc[0][0], sc[0][1]), mx1 = fmaxf(sc[0][2], sc[0][3]);
@@ -582,12 +618,14 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     pa[b][3] = pack_f16x2(ex2(fmaf(sc[2 * b + 1][2], sl2, -r1)), ex2(fmaf(sc[2 * b + 1][3], sl2, -r1)));
                 }
                 const uint32_t vb0 = stage(s0) + C::TSTAGE + warp * C::BOX;
-                if (valid_keys < kBlockSize) pv(std::true_type{}, vb0, pa[0], valid_keys);
-                else pv(std::false_type{}, vb0, pa[0], kBlockSize);
+                const LiveRows<WIN> live0(key0, item.key_end, p.sinks, low_min);
+                if (!live0.all()) pv(std::true_type{}, vb0, pa[0], live0);
+                else pv(std::false_type{}, vb0, pa[0], live0);
                 if constexpr (TWO) {
                     const uint32_t vb1 = stage(s1) + C::TSTAGE + warp * C::BOX;
-                    if (valid_keys < 2 * kBlockSize) pv(std::true_type{}, vb1, pa[1], valid_keys - kBlockSize);
-                    else pv(std::false_type{}, vb1, pa[1], kBlockSize);
+                    const LiveRows<WIN> live1(key0 + kBlockSize, item.key_end, p.sinks, low_min);
+                    if (!live1.all()) pv(std::true_type{}, vb1, pa[1], live1);
+                    else pv(std::false_type{}, vb1, pa[1], live1);
                 }
                 __syncwarp();
                 if (lane == 0) {
@@ -665,7 +703,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         int consumed = 0;
         bool ok = true;
         for (int it = item_begin; it < item_end && ok; ++it) {
-            const DecodeItem item = p.items[it];
+            DecodeItem item = p.items[it];
+            const WindowView view = own_numbers<WIN>(p, item);
+            // windows begin below low_top, the item's first one at low_min
+            const int low_top = item.key_end - p.window, low_min = low_top - (item.n_tok - 1);
             const int kvh = item.head_group * HG + warp;
             const int nrow = item.n_tok * G;
             const int tok0 = g / G, tok1 = (g + 8) / G;
@@ -691,7 +732,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             if constexpr (FUSED) {
                 const int lp = new_row_page(item);
                 if (lp >= 0) {
-                    store_new_row<D, false>(p, item, lp, kvh, lane);
+                    store_new_row<D, false>(p, item, view.at(lp), kvh, lane);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(row_ready);
                 }
@@ -730,6 +771,16 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         const int key = j * 8 + 2 * t4 + (e & 1);
                         sc[j][e] = key < (e < 2 ? valid0 : valid1) ? sc[j][e] * p.scale_log2 : -INFINITY;
                     }
+                if (WIN && key0 < low_top) {
+                    // keys behind a row's window that are not first tokens
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const int key = j * 8 + 2 * t4 + (e & 1);
+                            if (key >= p.sinks - key0 && key < (e < 2 ? valid0 : valid1) - p.window) sc[j][e] = -INFINITY;
+                        }
+                }
                 float mx0 = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
                 float mx1 = fmaxf(fmaxf(sc[0][2], sc[0][3]), fmaxf(sc[1][2], sc[1][3]));
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
@@ -764,12 +815,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     ok = false;
                     break;
                 }
-                if (valid_keys < kBlockSize) {
-                    // rows past the context may hold anything (even NaN); zero
-                    // them so that 0-weight * row stays 0 inside the MMA
-                    const int bad = kBlockSize - valid_keys;
-                    for (int i = lane; i < bad * C::NH * 8; i += 32) {
-                        const int row = valid_keys + i / (C::NH * 8);
+                if (valid_keys < kBlockSize || (WIN && key0 < low_min && key0 + kBlockSize > p.sinks)) {
+                    // rows past the context, or behind every token's window, may
+                    // hold anything (even NaN); zero them so that 0-weight * row
+                    // stays 0 inside the MMA
+                    const LiveRows<WIN> live(key0, item.key_end, p.sinks, low_min);
+                    const int from = WIN ? 0 : valid_keys;
+                    for (int i = lane; i < (kBlockSize - from) * C::NH * 8; i += 32) {
+                        const int row = from + i / (C::NH * 8);
+                        if (WIN && live.has(row)) continue;
                         const int half = (i / 8) % C::NH;
                         const int ch = i % 8;
                         const uint32_t a = vb + half * C::SLICE + row * 128 + ch * 16;
@@ -831,11 +885,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     __syncthreads();
 }
 
-template <int D, int HG, bool KV8, bool FUSED>
+template <int D, int HG, bool KV8, bool FUSED, bool WIN>
 cudaError_t configure() {
     static bool configured = false;  // attribute is per function, set once per process
     if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, HG, KV8, FUSED>,
+        cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, HG, KV8, FUSED, WIN>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeCfg<D, HG, KV8>::SMEM);
         if (e != cudaSuccess) return e;
         configured = true;
@@ -843,22 +897,22 @@ cudaError_t configure() {
     return cudaSuccess;
 }
 
-template <int D, int HG, bool KV8>
+template <int D, int HG, bool KV8, bool WIN>
 cudaError_t configure_both() {
-    cudaError_t e = configure<D, HG, KV8, false>();
-    return e == cudaSuccess ? configure<D, HG, KV8, true>() : e;
+    cudaError_t e = configure<D, HG, KV8, false, WIN>();
+    return e == cudaSuccess ? configure<D, HG, KV8, true, WIN>() : e;
 }
 
-template <int D, int HG, bool KV8>
+template <int D, int HG, bool KV8, bool WIN>
 cudaError_t launch_t(int num_ctas, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                      const DecodeParams &p, cudaStream_t stream) {
     using C = DecodeCfg<D, HG, KV8>;
-    cudaError_t e = configure_both<D, HG, KV8>();
+    cudaError_t e = configure_both<D, HG, KV8, WIN>();
     if (e != cudaSuccess) return e;
     if (p.new_k != nullptr)
-        return launch_pdl(decode_kernel<D, HG, KV8, true>, dim3(num_ctas), dim3(C::THREADS),
+        return launch_pdl(decode_kernel<D, HG, KV8, true, WIN>, dim3(num_ctas), dim3(C::THREADS),
                           C::SMEM, stream, tm_k, tm_v, p);
-    return launch_pdl(decode_kernel<D, HG, KV8, false>, dim3(num_ctas), dim3(C::THREADS),
+    return launch_pdl(decode_kernel<D, HG, KV8, false, WIN>, dim3(num_ctas), dim3(C::THREADS),
                       C::SMEM, stream, tm_k, tm_v, p);
 }
 
@@ -868,9 +922,9 @@ cudaError_t launch_t(int num_ctas, const CUtensorMap &tm_k, const CUtensorMap &t
     X(64, 1, false) X(64, 2, false) X(64, 4, false) X(64, 8, false) X(128, 1, false) X(128, 2, false)      \
     X(128, 4, false) X(128, 8, false) X(128, 1, true) X(128, 2, true) X(128, 4, true) X(128, 8, true)
 
-cudaError_t prepare_decode(int head_dim, int hg, bool kv8) {
+cudaError_t prepare_decode(int head_dim, int hg, bool kv8, bool window) {
 #define X(d, h, f) \
-    if (head_dim == d && hg == h && kv8 == f) return configure_both<d, h, f>();
+    if (head_dim == d && hg == h && kv8 == f) return window ? configure_both<d, h, f, true>() : configure_both<d, h, f, false>();
     PA_DECODE_CASES(X)
 #undef X
     return cudaErrorInvalidValue;
@@ -880,7 +934,9 @@ cudaError_t launch_decode(int head_dim, int hg, bool kv8, int num_ctas, const CU
                                           const CUtensorMap &tm_v, const DecodeParams &p, cudaStream_t stream) {
     if (num_ctas <= 0) return cudaSuccess;
 #define X(d, h, f) \
-    if (head_dim == d && hg == h && kv8 == f) return launch_t<d, h, f>(num_ctas, tm_k, tm_v, p, stream);
+    if (head_dim == d && hg == h && kv8 == f)   \
+        return p.window > 0 ? launch_t<d, h, f, true>(num_ctas, tm_k, tm_v, p, stream) \
+                            : launch_t<d, h, f, false>(num_ctas, tm_k, tm_v, p, stream);
     PA_DECODE_CASES(X)
 #undef X
     return cudaErrorInvalidValue;

@@ -83,7 +83,8 @@ struct Piece {
     }
 };
 
-template <int D, int HG, bool INT8>
+// WIN: with a sliding window and first tokens (items in WindowView's numbers).
+template <int D, int HG, bool INT8, bool WIN>
 struct Consumer {
     using C = ScaledCfg<D, HG>;
     static constexpr int CH = D / 64;   // 16-byte chunks of a key row per lane of a quad
@@ -149,6 +150,8 @@ struct Consumer {
             for (int e = 0; e < 2; ++e) rf[n][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e));   // of row 8n + 2t + e
         }
         const int lim_lo = item.key_end - (item.n_tok - 1);
+        // windows begin below low_top, the item's first one at low_min
+        const int low_top = item.key_end - b.window, low_min = lim_lo - b.window;
         float ot[NT][D / 16][4], lt[NT][2], ref[NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -176,9 +179,9 @@ struct Consumer {
                 }
             }
         };
-        // O^T += V^T P^T of one block; codes of rows at or past `valid` (MASKED:
+        // O^T += V^T P^T of one block; codes of rows that are not `live` (MASKED:
         // they may be anything, also NaN) count as 0
-        auto pv = [&](auto masked, uint32_t vb, const uint32_t (&w)[NT][2], int valid) {
+        auto pv = [&](auto masked, uint32_t vb, const uint32_t (&w)[NT][2], const LiveRows<WIN> &live) {
             Piece<D> v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -186,7 +189,7 @@ struct Consumer {
                 v[i].load(vb, row, g);
                 if constexpr (decltype(masked)::value) {
 #pragma unroll
-                    for (int j = 0; j < D / 32; ++j) v[i].w[j] = row < valid ? v[i].w[j] : 0u;
+                    for (int j = 0; j < D / 32; ++j) v[i].w[j] = live.has(row) ? v[i].w[j] : 0u;
                 }
             }
 #pragma unroll
@@ -230,7 +233,6 @@ struct Consumer {
 #pragma unroll
             for (int k = 0; k < NB; ++k) qk(st[k], sc[k]);
             const int key0 = pg * kBlockSize;
-            const int valid = item.key_end - key0;   // V rows past it may be anything
             if (lim_lo - key0 < NB * kBlockSize) {
                 // token i of the item sees keys < key_end - (n_tok - 1 - i)
 #pragma unroll
@@ -243,6 +245,23 @@ struct Consumer {
                             if (16 * k + g >= lim) sc[k][n][e] = -INFINITY;
                             if (16 * k + g + 8 >= lim) sc[k][n][e + 2] = -INFINITY;
                             if (16 * k >= lim) kf[k][n][e] = 1.f;   // none of the block: its scale, NaN even, plays no part
+                        }
+                    }
+            }
+            if (WIN && key0 < low_top) {
+                // keys behind a row's window that are not first tokens
+                const int first = b.sinks - key0;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int low = min(item.key_end, lim_lo + (8 * n + 2 * t4 + e) / G) - b.window - key0;
+                        auto behind = [&](int i) { return i >= first && i < low; };
+#pragma unroll
+                        for (int k = 0; k < NB; ++k) {
+                            if (behind(16 * k + g)) sc[k][n][e] = -INFINITY;
+                            if (behind(16 * k + g + 8)) sc[k][n][e + 2] = -INFINITY;
+                            if (behind(16 * k) && behind(16 * k + 15)) kf[k][n][e] = 1.f;   // none of the block
                         }
                     }
             }
@@ -305,8 +324,9 @@ struct Consumer {
             }
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
-                if (valid < (k + 1) * kBlockSize) pv(std::true_type{}, st[k] + C::TSTAGE, w[k], valid - k * kBlockSize);
-                else pv(std::false_type{}, st[k] + C::TSTAGE, w[k], kBlockSize);
+                const LiveRows<WIN> live(key0 + k * kBlockSize, item.key_end, b.sinks, low_min);
+                if (!live.all()) pv(std::true_type{}, st[k] + C::TSTAGE, w[k], live);
+                else pv(std::false_type{}, st[k] + C::TSTAGE, w[k], live);
             }
             __syncwarp();
             if (lane == 0) {
@@ -363,7 +383,7 @@ struct Consumer {
     }
 };
 
-template <int D, int HG, bool INT8>
+template <int D, int HG, bool INT8, bool WIN>
 __global__ void __launch_bounds__((HG + 1) * 32, scaled_decode_ctas_per_sm(D, HG))
 scaled_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                      const ScaledDecodeParams sp) {
@@ -408,7 +428,8 @@ scaled_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         // lane l < 2 HG copies the scale of tensor l / HG, head l % HG
         const float *scales = lane / HG == 0 ? sp.key_scales : sp.value_scales;
         for (int it = item_begin; it < item_end && ok; ++it) {
-            const DecodeItem item = p.items[it];
+            DecodeItem item = p.items[it];
+            const WindowView view = own_numbers<WIN>(p, item);
             const int32_t *bt = p.block_table + static_cast<int64_t>(item.req) * p.max_blocks;
             const int h0 = item.head_group * HG;
             int32_t blk_lane = 0;       // block id of page (window + lane), 32 pages at a time
@@ -416,7 +437,7 @@ scaled_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             for (int pg = item.page_begin; pg < item.page_end; ++pg) {
                 if (pg - window >= 32) {
                     window = pg;
-                    blk_lane = pg + lane < item.page_end ? bt[pg + lane] : 0;
+                    blk_lane = pg + lane < item.page_end ? bt[view.at(pg + lane)] : 0;
                 }
                 const int s = issued % C::NS;
                 const int n = issued / C::NS;
@@ -455,10 +476,11 @@ scaled_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
         }
     } else {
         // ----------------------------------------------------- consumers --
-        Consumer<D, HG, INT8> c{sp, base, scale0, bar0, bar0 + 8u * C::NS, &abort_flag, warp, lane, lane >> 2, lane & 3};
+        Consumer<D, HG, INT8, WIN> c{sp, base, scale0, bar0, bar0 + 8u * C::NS, &abort_flag, warp, lane, lane >> 2, lane & 3};
         bool ok = true;
         for (int it = item_begin; it < item_end && ok; ++it) {
-            const DecodeItem item = p.items[it];
+            DecodeItem item = p.items[it];
+            own_numbers<WIN>(p, item);
             ok = item.n_tok * p.group <= 8 ? c.template run<1>(item) : c.template run<2>(item);
             if (!ok && lane == 0) raise_abort(&abort_flag, p.err, kErrTimeout);
         }
@@ -466,18 +488,18 @@ scaled_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
     __syncthreads();
 }
 
-template <int D, int HG, bool INT8>
+template <int D, int HG, bool INT8, bool WIN>
 cudaError_t configure() {
     // the attribute is per function and device; setting it again is harmless
-    return cudaFuncSetAttribute(scaled_decode_kernel<D, HG, INT8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(scaled_decode_kernel<D, HG, INT8, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 ScaledCfg<D, HG>::SMEM);
 }
 
-template <int D, int HG, bool INT8>
+template <int D, int HG, bool INT8, bool WIN>
 cudaError_t launch_t(int num_ctas, const CUtensorMap &tm_k, const CUtensorMap &tm_v, const ScaledDecodeParams &p,
                      cudaStream_t stream) {
     using C = ScaledCfg<D, HG>;
-    return launch_pdl(scaled_decode_kernel<D, HG, INT8>, dim3(num_ctas), dim3(C::THREADS), C::SMEM, stream, tm_k, tm_v, p);
+    return launch_pdl(scaled_decode_kernel<D, HG, INT8, WIN>, dim3(num_ctas), dim3(C::THREADS), C::SMEM, stream, tm_k, tm_v, p);
 }
 
 }  // namespace
@@ -487,9 +509,9 @@ cudaError_t launch_t(int num_ctas, const CUtensorMap &tm_k, const CUtensorMap &t
     X(128, 4, false) X(128, 8, false) X(64, 1, true) X(64, 2, true) X(64, 4, true) X(64, 8, true) X(128, 1, true) \
     X(128, 2, true) X(128, 4, true) X(128, 8, true)
 
-cudaError_t prepare_scaled_decode(int head_dim, int hg, bool int8) {
+cudaError_t prepare_scaled_decode(int head_dim, int hg, bool int8, bool window) {
 #define X(d, h, i) \
-    if (head_dim == d && hg == h && int8 == i) return configure<d, h, i>();
+    if (head_dim == d && hg == h && int8 == i) return window ? configure<d, h, i, true>() : configure<d, h, i, false>();
     PA_SCALED_CASES(X)
 #undef X
     return cudaErrorInvalidValue;
@@ -499,7 +521,9 @@ cudaError_t launch_scaled_decode(int head_dim, int hg, bool int8, int num_ctas, 
                                  const CUtensorMap &tm_v, const ScaledDecodeParams &p, cudaStream_t stream) {
     if (num_ctas <= 0) return cudaSuccess;
 #define X(d, h, i) \
-    if (head_dim == d && hg == h && int8 == i) return launch_t<d, h, i>(num_ctas, tm_k, tm_v, p, stream);
+    if (head_dim == d && hg == h && int8 == i)  \
+        return p.base.window > 0 ? launch_t<d, h, i, true>(num_ctas, tm_k, tm_v, p, stream) \
+                                 : launch_t<d, h, i, false>(num_ctas, tm_k, tm_v, p, stream);
     PA_SCALED_CASES(X)
 #undef X
     return cudaErrorInvalidValue;

@@ -110,7 +110,10 @@ __device__ __forceinline__ TileShape tile_shape(const ExtendTile &tile, int tpt)
     return sh;
 }
 
-template <int D>
+// WIN: with a sliding window and first tokens (tiles in WindowView's numbers: key
+// tiles of 128 keys run over the blocks with first tokens and on into those of the
+// tile's first window, whose lower masks reach over the first key tiles only).
+template <int D, bool WIN>
 __global__ void __launch_bounds__(384, 1)
 extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const ExtendParams p) {
@@ -209,7 +212,8 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 const int pages = min(8, (tile.key_end - kt0 + kBlockSize - 1) / kBlockSize);
                 if (pg0 + 8 > win0 + 32) {
                     win0 = pg0;
-                    win = pg0 + lane < pg_end ? bt[pg0 + lane] : 0;
+                    const int pg = WIN ? WindowView{tile.head, tile.skip}.at(pg0 + lane) : pg0 + lane;
+                    win = pg0 + lane < pg_end ? bt[pg] : 0;
                 }
                 const int32_t mine_blk = __shfl_sync(0xffffffffu, win, (pg0 - win0 + (lane & 7)) & 31);
                 int32_t blk = 0;
@@ -398,6 +402,8 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const int pos_lim = tile.causal ? tile.pos0 + i + 1 : 0x7fffffff;  // keys < pos_lim
             const int row_end = min(tile.key_end, pos_lim);
             const int n_mine = t ? sh.n_sub[1] : sh.n_sub[0];
+            // windows: this row's begins at low, the tile's first one at low_min
+            const int low = pos_lim - p.window, low_min = tile.pos0 + 1 - p.window;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < n_mine; ++j) {
                 if (!warp_wait(bar(B_SFULL + t), scnt & 1, &abort_flag)) { ok = false; break; }
@@ -416,6 +422,12 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
                     for (int c = 0; c < 128; ++c)
                         if (c >= lim) sr[c] = __float_as_uint(-INFINITY);
+                }
+                if (WIN && kt0 < low) {   // keys behind the row's window that are not first tokens
+                    const int from = p.sinks - kt0, to = low - kt0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c >= from && c < to) sr[c] = __float_as_uint(-INFINITY);
                 }
                 // row max: 3-input max, four chains
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
@@ -475,13 +487,17 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 // (unwritten slots, stale blocks, NaN): zero them so that
                 // 0 * row stays 0 inside the MMA.  Each sub-tile that reads
                 // the last V tile zeroes them before handing over its P, so
-                // the PV after it sees zeros (both write the same zeros).
+                // the PV after it sees zeros (both write the same zeros).  So it is
+                // for rows that no window of the tile reaches and that are not
+                // first tokens.  (V tiles before this one are full: S_t(j) stands
+                // behind the PVs of theirs.)
                 const int valid_keys = tile.key_end - kt0;
-                if (valid_keys < kTileKeys && j == sh.n_tiles - 1) {
+                const bool behind = WIN && kt0 < low_min && kt0 + kTileKeys > p.sinks;
+                if ((valid_keys < kTileKeys && j == sh.n_tiles - 1) || behind) {
                     const int vi = vbase + j;
                     const int s = vi % C::NSV;
                     if (!warp_wait(bar(B_VFULL + s), (vi / C::NSV) & 1, &abort_flag)) { ok = false; break; }
-                    if (row >= valid_keys) {
+                    if (row >= valid_keys || (behind && kt0 + row >= p.sinks && kt0 + row < low_min)) {
 #pragma unroll
                         for (int h = 0; h < C::NH; ++h)
 #pragma unroll
@@ -553,11 +569,11 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t configure() {
     static bool configured = false;  // attribute is per function, set once per process
     if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(extend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(extend_kernel<D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              ExtCfg<D>::SMEM);
         if (e != cudaSuccess) return e;
         configured = true;
@@ -565,28 +581,32 @@ cudaError_t configure() {
     return cudaSuccess;
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_t(int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                      const ExtendParams &p, cudaStream_t stream, bool pdl) {
     using C = ExtCfg<D>;
-    cudaError_t e = configure<D>();
+    cudaError_t e = configure<D, WIN>();
     if (e != cudaSuccess) return e;
-    return launch_ex(extend_kernel<D>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, pdl, tm_q, tm_k, tm_v, p);
+    return launch_ex(extend_kernel<D, WIN>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, pdl, tm_q, tm_k, tm_v, p);
 }
 
 }  // namespace
 
-cudaError_t prepare_extend(int head_dim) {
-    if (head_dim == 128) return configure<128>();
-    if (head_dim == 64) return configure<64>();
+cudaError_t prepare_extend(int head_dim, bool window) {
+    if (head_dim == 128) return window ? configure<128, true>() : configure<128, false>();
+    if (head_dim == 64) return window ? configure<64, true>() : configure<64, false>();
     return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_extend(int head_dim, int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const ExtendParams &p, cudaStream_t stream, bool pdl) {
     if (grid <= 0) return cudaSuccess;
-    if (head_dim == 128) return launch_t<128>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
-    if (head_dim == 64) return launch_t<64>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
+    if (head_dim == 128)
+        return p.window > 0 ? launch_t<128, true>(grid, tm_q, tm_k, tm_v, p, stream, pdl)
+                            : launch_t<128, false>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
+    if (head_dim == 64)
+        return p.window > 0 ? launch_t<64, true>(grid, tm_q, tm_k, tm_v, p, stream, pdl)
+                            : launch_t<64, false>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
     return cudaErrorInvalidValue;
 }
 

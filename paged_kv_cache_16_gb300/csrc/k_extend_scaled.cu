@@ -111,7 +111,10 @@ __device__ __forceinline__ TileShape tile_shape(const ExtendTile &tile, int tpt)
     return sh;
 }
 
-template <int D>
+// WIN: with a sliding window and first tokens (tiles in WindowView's numbers, the
+// head padded to whole key tiles: the copies of a head's blocks are consecutive,
+// and so are those from the window on).
+template <int D, bool WIN>
 __global__ void __launch_bounds__(384, 1)
 scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const ScaledExtendParams sp) {
@@ -210,15 +213,23 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // the producer 8% of the kernel's time).  Rows behind the key range
             // belong to other requests or to none: masked columns, and value
             // rows that the softmax warps zero
-            const int32_t dst0 = p.block_table[static_cast<int64_t>(tile.req) * p.max_blocks + tile.key_begin / kBlockSize];
+            const int32_t *copies = p.block_table + static_cast<int64_t>(tile.req) * p.max_blocks;
             const int pg_end = (tile.key_end - tile.key_begin + kBlockSize - 1) / kBlockSize;
-            if (dst0 < 0 || dst0 + pg_end > p.num_blocks) {   // (not from the planner)
+            // windowed: first the copies of the head (rows of its padding are other
+            // blocks'), then those from page `head` on; dst0 counts from page 0
+            const int32_t head = WIN ? tile.head : 0, head_end = head_blocks(p.sinks, p.sinks);
+            const int32_t dst0 = copies[tile.key_begin / kBlockSize + head + (WIN ? tile.skip : 0)] - head;
+            const int32_t head0 = head > 0 ? copies[0] : 0;
+            if (dst0 + head < 0 || dst0 + pg_end > p.num_blocks ||
+                head0 < 0 || (head > 0 && head0 + head_end > p.num_blocks)) {   // (not from the planner)
                 if (lane == 0) raise_abort(&abort_flag, p.err, kErrBlockRange);
                 break;
             }
             for (int j = 0; j < sh.n_tiles; ++j) {
                 const int pg0 = j * (kTileKeys / kBlockSize);
-                const int pages = min(kTileKeys / kBlockSize, pg_end - pg0);
+                const bool in_head = pg0 < head;
+                const int pages = min(kTileKeys / kBlockSize, (in_head ? head_end : pg_end) - pg0);
+                const int32_t at = (in_head ? head0 : dst0) + pg0;
 #pragma unroll
                 for (int tensor = 0; tensor < 2; ++tensor) {
                     const int ns = tensor ? C::NSV : C::NSK;
@@ -234,9 +245,9 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     __syncwarp();
                     if (lane < C::NH)
                         tma_load_3d((tensor ? v_s(s) : k_s(s)) + lane * C::HALF, tensor ? &tm_v : &tm_k, lane * 64,
-                                    tile.kv_head, (dst0 + pg0) * kBlockSize, bar(full + s));
+                                    tile.kv_head, at * kBlockSize, bar(full + s));
                     else if (tensor && lane == C::NH)
-                        bulk_load(f_s(s, 0), sp.factors + static_cast<int64_t>(tile.kv_head) * p.num_blocks + dst0 + pg0,
+                        bulk_load(f_s(s, 0), sp.factors + static_cast<int64_t>(tile.kv_head) * p.num_blocks + at,
                                   16u * pages, bar(full + s));
                     ++issued[tensor];
                 }
@@ -438,6 +449,8 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             const int pos_lim = tile.causal ? tile.pos0 + i + 1 : 0x7fffffff;  // keys < pos_lim
             const int row_end = min(tile.key_end, pos_lim);
             const int n_mine = t ? sh.n_sub[1] : sh.n_sub[0];
+            // windows: this row's begins at low, the tile's first one at low_min
+            const int low = pos_lim - p.window, low_min = tile.pos0 + 1 - p.window;
             float m = -INFINITY, l = 0.f;
             for (int j = 0; j < n_mine; ++j) {
                 const int kt0 = tile.key_begin + j * kTileKeys;
@@ -468,6 +481,16 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     for (int b = 0; b < 8; ++b)
                         if (kt0 + kBlockSize * b >= tile.key_end) { fs[b] = 1.f; lv[b] = 0.f; iv[b] = 0.f; }
                 }
+                // blocks without a key that some row of the tile sees (the head's
+                // padding, which has no factors, among them)
+                const bool behind = WIN && kt0 < low_min && kt0 + kTileKeys > p.sinks;
+                if (behind) {
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)
+                        if (kt0 + kBlockSize * b >= p.sinks && kt0 + kBlockSize * (b + 1) <= low_min) {
+                            fs[b] = 1.f; lv[b] = 0.f; iv[b] = 0.f;
+                        }
+                }
                 if (!s_first && !warp_wait(bar(B_SFULL + t), scnt & 1, &abort_flag)) { ok = false; break; }
                 ++scnt;
                 tc_fence_after();
@@ -486,6 +509,15 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
 #pragma unroll
                     for (int b = 0; b < 8; ++b)   // none of the block: its scale, NaN even, plays no part
                         if (kBlockSize * b >= lim) fs[b] = 1.f;
+                }
+                if (WIN && kt0 < low) {   // keys behind the row's window that are not first tokens
+                    const int from = p.sinks - kt0, to = low - kt0;
+#pragma unroll
+                    for (int c = 0; c < 128; ++c)
+                        if (c >= from && c < to) sr[c] = __float_as_uint(-INFINITY);
+#pragma unroll
+                    for (int b = 0; b < 8; ++b)
+                        if (kBlockSize * b >= from && kBlockSize * (b + 1) <= to) fs[b] = 1.f;
                 }
                 // row max of s + log2 vs
                 float mxs = -INFINITY;
@@ -547,11 +579,13 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                         // (unwritten slots, stale blocks, NaN): zero them so that
                         // 0 * row stays 0 inside the MMA.  Each sub-tile that reads
                         // the last V tile zeroes them before handing over its P, so
-                        // the PV after it sees zeros (both write the same zeros).
+                        // the PV after it sees zeros (both write the same zeros).  So
+                        // it is for rows that no window of the tile reaches and that
+                        // are not first tokens.
                         const int valid_keys = tile.key_end - kt0;
-                        if (valid_keys < kTileKeys && j == sh.n_tiles - 1) {
+                        if ((valid_keys < kTileKeys && j == sh.n_tiles - 1) || behind) {
                             const int s = vs_stage;   // (landed: waited for above)
-                            if (row >= valid_keys) {
+                            if (row >= valid_keys || (behind && kt0 + row >= p.sinks && kt0 + row < low_min)) {
 #pragma unroll
                                 for (int h = 0; h < C::NH; ++h)
 #pragma unroll
@@ -666,32 +700,36 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t configure() {
     // the attribute is per function and device; setting it again is harmless
-    return cudaFuncSetAttribute(scaled_extend_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScaledExtCfg<D>::SMEM);
+    return cudaFuncSetAttribute(scaled_extend_kernel<D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScaledExtCfg<D>::SMEM);
 }
 
-template <int D>
+template <int D, bool WIN>
 cudaError_t launch_t(int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                      const ScaledExtendParams &p, cudaStream_t stream, bool pdl) {
     using C = ScaledExtCfg<D>;
-    return launch_ex(scaled_extend_kernel<D>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, pdl, tm_q, tm_k, tm_v, p);
+    return launch_ex(scaled_extend_kernel<D, WIN>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, pdl, tm_q, tm_k, tm_v, p);
 }
 
 }  // namespace
 
-cudaError_t prepare_scaled_extend(int head_dim) {
-    if (head_dim == 128) return configure<128>();
-    if (head_dim == 64) return configure<64>();
+cudaError_t prepare_scaled_extend(int head_dim, bool window) {
+    if (head_dim == 128) return window ? configure<128, true>() : configure<128, false>();
+    if (head_dim == 64) return window ? configure<64, true>() : configure<64, false>();
     return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_scaled_extend(int head_dim, int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const ScaledExtendParams &p, cudaStream_t stream, bool pdl) {
     if (grid <= 0) return cudaSuccess;
-    if (head_dim == 128) return launch_t<128>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
-    if (head_dim == 64) return launch_t<64>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
+    if (head_dim == 128)
+        return p.base.window > 0 ? launch_t<128, true>(grid, tm_q, tm_k, tm_v, p, stream, pdl)
+                                 : launch_t<128, false>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
+    if (head_dim == 64)
+        return p.base.window > 0 ? launch_t<64, true>(grid, tm_q, tm_k, tm_v, p, stream, pdl)
+                                 : launch_t<64, false>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
     return cudaErrorInvalidValue;
 }
 

@@ -11,6 +11,10 @@
 // rounding of cos and sin).  cos and sin of the tokens of a CTA are computed once into
 // shared memory and used by all of its heads.  Arithmetic in fp32, one
 // rounding at the end.
+//
+// With positions on several axes (time, height, width) pair i turns by
+// p_axis(i) * f_i: the table is made from as many positions per token, a thread of
+// it keeps one pair and so one axis, and nothing else differs.
 #include "dev.cuh"
 
 namespace pa {
@@ -38,10 +42,19 @@ __device__ __forceinline__ void cos_sin(uint64_t step, int32_t pos, float mag, f
 // per entry: 64 tokens 2.2 us instead of 1.8, 8192 tokens x 8 heads 10.4 instead of
 // 7.6, an append of two chunks 19.6 instead of 18.5; once per thread, 2.0 and 18.4,
 // but a decode step's append 3.6 instead of 3.5).
+template <bool AXES>
+struct RopeArg_ { using type = RopeParams; };
+template <>
+struct RopeArg_<true> { using type = AxesRopeParams; };
+template <bool AXES>
+using RopeArg = typename RopeArg_<AXES>::type;
+
+template <bool AXES>
 struct TableMaker {
     int i, j0, tokens;   // pair, first token, tokens a pass (0: no part of the table)
+    int axis;            // of its positions
     uint64_t step;
-    __device__ __forceinline__ TableMaker(const RopeParams &rope, int n) : i(0), j0(0), tokens(0), step(0) {
+    __device__ __forceinline__ TableMaker(const RopeArg<AXES> &rope, int n) : i(0), j0(0), tokens(0), axis(0), step(0) {
         const int half = rope.rotary_dim / 2;
         if (half == 0) return;
         j0 = static_cast<int>(threadIdx.x) / half;
@@ -50,6 +63,11 @@ struct TableMaker {
         const uint64_t *steps;   // (opaque, or the load would be a constant one)
         asm("mov.u64 %0, %1;" : "=l"(steps) : "l"(rope.step));
         if (j0 < min(tokens, n)) step = steps[i];
+        if constexpr (AXES) {
+            const uint8_t *axes;
+            asm("mov.u64 %0, %1;" : "=l"(axes) : "l"(rope.axis));
+            if (j0 < min(tokens, n)) axis = axes[i];
+        }
     }
     template <typename PosOf>
     __device__ __forceinline__ void fill(float *tab, const RopeParams &rope, int n, PosOf pos_of) const {
@@ -57,7 +75,7 @@ struct TableMaker {
         float *at = tab + j0 * rope.rotary_dim + i;
         for (int j = j0; j < n; j += tokens, at += tokens * rope.rotary_dim) {
             float c, s;
-            cos_sin(step, pos_of(j), rope.mag, c, s);
+            cos_sin(step, pos_of(j, axis), rope.mag, c, s);
             at[0] = c;
             at[rope.rotary_dim / 2] = s;
         }
@@ -211,18 +229,18 @@ __device__ __forceinline__ void rotate_rows(const float *tab, const RopeParams &
 // are asked into L2 before its table of cos and sin is made, from 1 MB of rows on
 // (28.8 us without; 512 tokens 3.2 and 3.7, 128 tokens 2.35 and 2.5, 64 tokens the
 // same; 1021 tokens x 7 heads of 64 1.76 and 1.65).
-template <int W>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RopeParams rope, const RotaryParams p) {
+template <int W, bool AXES>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RopeArg<AXES> rope, const RotaryParams p) {
     extern __shared__ float4 smem4[];
     float *tab = reinterpret_cast<float *>(smem4);
     grid_launch_dependents();
     const int t0 = blockIdx.x << p.log_tokens, h0 = blockIdx.y * p.heads_per_cta;
     const int n = min(1 << p.log_tokens, p.num_tokens - t0), nh = min(p.heads_per_cta, p.num_heads - h0);
-    const TableMaker table(rope, n);
+    const TableMaker<AXES> table(rope, n);
     grid_dep_wait();
     if (W == 8 && p.prefetch && static_cast<int>(threadIdx.x) < n)   // (16-byte pieces: aligned rows)
         bulk_prefetch_l2(p.x + (t0 + static_cast<int>(threadIdx.x)) * p.x_stride + h0 * p.head_dim, nh * p.head_dim * 2);
-    table.fill(tab, rope, n, [&](int j) { return __ldg(p.positions + t0 + j); });
+    table.fill(tab, rope, n, [&](int j, int axis) { return __ldg(p.positions + (AXES ? axis * p.axis_stride : 0) + t0 + j); });
     __syncthreads();
     rotate_rows<W, W == 8 ? 5 : 8>(tab, rope, p.x + t0 * p.x_stride + h0 * p.head_dim, p.x_stride,
                    p.out + t0 * p.out_stride + h0 * p.head_dim, p.out_stride, n, p.log_tokens, nh, p.head_dim);
@@ -445,8 +463,8 @@ __device__ __forceinline__ int log2_up(int n) { return n <= 1 ? 0 : 32 - __clz(n
 // by the last keys and values (~4 us each).  Queries of 8 / 16 / 32 heads per CTA
 // 22.9 / 20.2 / 18.5, a segment's parts side by side in the grid 19.2, keys and
 // values first with 16 heads 19.3; rows asked into L2 first 19.4.
-template <int D, int KIND, int W>
-__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ RopeParams rope, const AppendParams p) {
+template <int D, int KIND, int W, bool AXES>
+__global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_constant__ RopeArg<AXES> rope, const AppendParams p) {
     using H = HeadRows<D, W>;
     constexpr bool BLOCK_SCALED = KIND == kCacheE4m3Block || KIND == kCacheInt8Block;
     constexpr bool INT8 = KIND == kCacheInt8Block;
@@ -458,9 +476,13 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
     const int part = (static_cast<int>(blockIdx.y) + 2 * kv_parts) % static_cast<int>(gridDim.y);
     const Segment s = find_segment(p, blockIdx.x);
     if (s.n == 0) return;
-    auto pos_of = [&](int j) { return s.pos + j; };
+    // (axes: a row turns by positions of its own, wherever it goes in the cache)
+    auto pos_of = [&](int j, int axis) {
+        if constexpr (AXES) return __ldg(p.positions + axis * p.axis_stride + s.t0 + j);
+        return s.pos + j;
+    };
     if (part >= 2 * kv_parts) {
-        TableMaker(rope, s.n).fill(tab, rope, s.n, pos_of);
+        TableMaker<AXES>(rope, s.n).fill(tab, rope, s.n, pos_of);
         __syncthreads();
         const int h0 = (part - 2 * kv_parts) * p.q_heads_per_cta;
         rotate_rows<W, 8>(tab, rope, p.q + s.t0 * p.q_stride + h0 * D, p.q_stride, p.q_out + s.t0 * p.q_out_stride + h0 * D,
@@ -489,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
             rb[it] = load_raw<W>(x + u.b);
         }
     }
-    if (half > 0) TableMaker(rope, s.n).fill(tab, rope, s.n, pos_of);
+    if (half > 0) TableMaker<AXES>(rope, s.n).fill(tab, rope, s.n, pos_of);
     __syncthreads();
     if (!block_ok(p, s, part == 0) || !mine) return;
     const int64_t row_stride = static_cast<int64_t>(p.num_heads_kv) * D;
@@ -559,22 +581,21 @@ __global__ void __launch_bounds__(kThreads, 2) append_kernel(const __grid_consta
 // units of 2 x 8 elements where every group of a row is 16-byte aligned
 bool wide_units(const RopeParams &rope, int head_dim) { return rope.rotary_dim % 16 == 0 && head_dim % 16 == 0; }
 
-template <int D, int W>
-cudaError_t launch_append_d(int kind, const RopeParams &rope, const AppendParams &p, dim3 grid, cudaStream_t stream) {
+template <int D, int W, bool AXES>
+cudaError_t launch_append_d(int kind, const RopeArg<AXES> &rope, const AppendParams &p, dim3 grid, cudaStream_t stream) {
     switch (kind) {
-        case kCacheBf16: return launch_pdl(append_kernel<D, kCacheBf16, W>, grid, dim3(kThreads), 0, stream, rope, p);
-        case kCacheE4m3: return launch_pdl(append_kernel<D, kCacheE4m3, W>, grid, dim3(kThreads), 0, stream, rope, p);
+        case kCacheBf16: return launch_pdl(append_kernel<D, kCacheBf16, W, AXES>, grid, dim3(kThreads), 0, stream, rope, p);
+        case kCacheE4m3: return launch_pdl(append_kernel<D, kCacheE4m3, W, AXES>, grid, dim3(kThreads), 0, stream, rope, p);
         case kCacheE4m3Block:
-            return launch_pdl(append_kernel<D, kCacheE4m3Block, W>, grid, dim3(kThreads), 0, stream, rope, p);
+            return launch_pdl(append_kernel<D, kCacheE4m3Block, W, AXES>, grid, dim3(kThreads), 0, stream, rope, p);
         case kCacheInt8Block:
-            return launch_pdl(append_kernel<D, kCacheInt8Block, W>, grid, dim3(kThreads), 0, stream, rope, p);
+            return launch_pdl(append_kernel<D, kCacheInt8Block, W, AXES>, grid, dim3(kThreads), 0, stream, rope, p);
     }
     return cudaErrorInvalidValue;
 }
 
-}  // namespace
-
-cudaError_t launch_rotary(const RopeParams &rope, const RotaryParams &p0, cudaStream_t stream) {
+template <bool AXES>
+cudaError_t launch_rotary_t(const RopeArg<AXES> &rope, const RotaryParams &p0, cudaStream_t stream) {
     RotaryParams p = p0;
     if (p.num_tokens <= 0) return cudaSuccess;
     p.heads_per_cta = p.num_heads < 40 ? p.num_heads : 40;
@@ -592,11 +613,12 @@ cudaError_t launch_rotary(const RopeParams &rope, const RotaryParams &p0, cudaSt
                     (p.num_heads + p.heads_per_cta - 1) / p.heads_per_cta);
     p.prefetch = static_cast<int64_t>(p.num_tokens) * p.num_heads * p.head_dim >= 1 << 19;
     const size_t smem = sizeof(float) * (rope.rotary_dim << p.log_tokens);
-    return wide ? launch_pdl(rotary_kernel<8>, grid, dim3(kThreads), smem, stream, rope, p)
-                : launch_pdl(rotary_kernel<4>, grid, dim3(kThreads), smem, stream, rope, p);
+    return wide ? launch_pdl(rotary_kernel<8, AXES>, grid, dim3(kThreads), smem, stream, rope, p)
+                : launch_pdl(rotary_kernel<4, AXES>, grid, dim3(kThreads), smem, stream, rope, p);
 }
 
-cudaError_t launch_append(int head_dim, int kind, const RopeParams &rope, const AppendParams &p0, cudaStream_t stream) {
+template <bool AXES>
+cudaError_t launch_append_t(int head_dim, int kind, const RopeArg<AXES> &rope, const AppendParams &p0, cudaStream_t stream) {
     AppendParams p = p0;
     if (p.num_tokens <= 0 || p.num_reqs <= 0) return cudaSuccess;
     p.q_heads_per_cta = p.num_heads_q < 32 ? p.num_heads_q : 32;
@@ -604,10 +626,30 @@ cudaError_t launch_append(int head_dim, int kind, const RopeParams &rope, const 
     const dim3 grid(p.num_tokens / kBlockSize + 2 * p.num_reqs, 2 * ((p.num_heads_kv + 7) / 8) + q_parts);
     const bool wide = wide_units(rope, head_dim);
     if (head_dim == 128)
-        return wide ? launch_append_d<128, 8>(kind, rope, p, grid, stream) : launch_append_d<128, 4>(kind, rope, p, grid, stream);
+        return wide ? launch_append_d<128, 8, AXES>(kind, rope, p, grid, stream)
+                    : launch_append_d<128, 4, AXES>(kind, rope, p, grid, stream);
     if (head_dim == 64)
-        return wide ? launch_append_d<64, 8>(kind, rope, p, grid, stream) : launch_append_d<64, 4>(kind, rope, p, grid, stream);
+        return wide ? launch_append_d<64, 8, AXES>(kind, rope, p, grid, stream)
+                    : launch_append_d<64, 4, AXES>(kind, rope, p, grid, stream);
     return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t launch_rotary(const RopeParams &rope, const RotaryParams &p, cudaStream_t stream) {
+    return launch_rotary_t<false>(rope, p, stream);
+}
+
+cudaError_t launch_rotary_axes(const AxesRopeParams &rope, const RotaryParams &p, cudaStream_t stream) {
+    return launch_rotary_t<true>(rope, p, stream);
+}
+
+cudaError_t launch_append(int head_dim, int kind, const RopeParams &rope, const AppendParams &p, cudaStream_t stream) {
+    return launch_append_t<false>(head_dim, kind, rope, p, stream);
+}
+
+cudaError_t launch_append_axes(int head_dim, int kind, const AxesRopeParams &rope, const AppendParams &p, cudaStream_t stream) {
+    return launch_append_t<true>(head_dim, kind, rope, p, stream);
 }
 
 }  // namespace pa

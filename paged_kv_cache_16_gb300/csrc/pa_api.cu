@@ -140,7 +140,7 @@ int heads_per_group(int hkv) {
     return 1;
 }
 
-pa_status validate(const pa_batch_desc *d) {
+pa_status validate(const pa_batch_desc *d, const pa_window_desc *win = nullptr) {
     if (d->num_reqs < 0 || d->num_heads_q <= 0 || d->num_heads_kv <= 0 || d->num_blocks <= 0 ||
         d->max_blocks_per_req <= 0 || d->block_size <= 0 || d->head_dim <= 0)
         return PA_ERR_INVALID_ARGUMENT;
@@ -166,7 +166,14 @@ pa_status validate(const pa_batch_desc *d) {
             const int32_t *row = d->block_table_host + static_cast<int64_t>(r) * d->max_blocks_per_req;
             const uint32_t nb = static_cast<uint32_t>(d->num_blocks);
             uint32_t bad = 0;
-            for (int64_t b = 0; b < need; ++b) bad |= static_cast<uint32_t>(row[b]) >= nb ? 1u : 0u;
+            int64_t low = 0;
+            if (win) {   // ids of blocks that no query sees may be anything
+                if (q_len == 0) continue;
+                low = window_low(d->num_computed_tokens[r], win->window) / kBlockSize;
+                const int64_t head = std::min<int64_t>(head_blocks(d->seq_lens[r], win->sink_tokens), low);
+                for (int64_t b = 0; b < head; ++b) bad |= static_cast<uint32_t>(row[b]) >= nb ? 1u : 0u;
+            }
+            for (int64_t b = low; b < need; ++b) bad |= static_cast<uint32_t>(row[b]) >= nb ? 1u : 0u;
             if (bad) return PA_ERR_INVALID_ARGUMENT;
         }
     }
@@ -208,6 +215,8 @@ pa_status validate(const pa_batch_desc *d) {
 // unit reads keys [0, key_end), key_end = one past its last token's position.
 struct DecodeUnit {
     int32_t r, t0, n_tok, key_end;
+    int32_t skip;   // blocks below key_end that it does not read (WindowView)
+    int32_t keys() const { return key_end - kBlockSize * skip; }   // with the gap left out
 };
 
 // Cut the concatenated decode runs into ncta equal contiguous shares.
@@ -246,7 +255,7 @@ void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector
     int64_t total = 0;
     for (int grp = 0; grp < P->n_groups; ++grp)
         for (size_t u = 0; u < units.size(); ++u) {
-            const int32_t pe = (units[u].key_end + kBlockSize - 1) / kBlockSize;
+            const int32_t pe = (units[u].keys() + kBlockSize - 1) / kBlockSize;
             if (pe <= kb) continue;
             runs.push_back({static_cast<int32_t>(u), grp, kb, pe});
             total += pe - kb;
@@ -430,8 +439,11 @@ void balance_tiles(const std::vector<std::pair<int64_t, int32_t>> &tiles, int ct
     }
 }
 
-pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape *shape) {
+pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape *shape,
+                     const pa_window_desc *win = nullptr) {
     P->fixed = shape != nullptr;
+    P->window = win ? win->window : 0;
+    P->sinks = win ? win->sink_tokens : 0;
     P->R = d->num_reqs;
     P->Hq = d->num_heads_q;
     P->Hkv = d->num_heads_kv;
@@ -539,6 +551,16 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
                 t.pos0 = d->num_computed_tokens[r] + m0;
                 t.key_begin = kb_keys;
                 t.key_end = std::min(d->seq_lens[r], t.pos0 + t.n_tok);
+                if (win) {
+                    // block-scaled tiles read whole key tiles of consecutive copies:
+                    // their head is padded to one
+                    const WindowView v = window_view(t.pos0, t.key_end, P->window, P->sinks,
+                                                     P->scaled ? kTileKeys / kBlockSize : 1);
+                    t.head = v.head;
+                    t.skip = v.skip;
+                    t.pos0 -= v.skip * kBlockSize;
+                    t.key_end -= v.skip * kBlockSize;
+                }
                 t.kv_head = h;
                 t.part = cascade ? P->prefix_splits : -1;
                 t.causal = 1;
@@ -560,7 +582,8 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
     // E4M3 caches: the tiles read bf16 copies of the blocks they touch, one
     // scratch block-table row per request the tiles read through
     if (P->kv8 && !P->tiles.empty()) {
-        std::vector<int32_t> row_of(static_cast<size_t>(P->R), -1), lo, hi, reqs;
+        // (windowed: blocks of first tokens [0, first), then [lo, hi))
+        std::vector<int32_t> row_of(static_cast<size_t>(P->R), -1), lo, hi, reqs, first;
         for (const ExtendTile &t : P->tiles) {
             int32_t &row = row_of[t.req];
             if (row < 0) {
@@ -568,13 +591,17 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
                 reqs.push_back(t.req);
                 lo.push_back(INT32_MAX);
                 hi.push_back(0);
+                first.push_back(0);
             }
-            lo[row] = std::min(lo[row], t.key_begin / kBlockSize);
-            hi[row] = std::max(hi[row], (t.key_end + kBlockSize - 1) / kBlockSize);
+            const int32_t end = t.key_end + t.skip * kBlockSize;
+            lo[row] = std::min(lo[row], t.key_begin / kBlockSize + t.head + t.skip);
+            hi[row] = std::max(hi[row], (end + kBlockSize - 1) / kBlockSize);
+            first[row] = std::max(first[row], head_blocks(end, P->sinks));
         }
         P->scratch_table.assign(reqs.size() * static_cast<size_t>(P->max_blocks), 0);
         for (size_t row = 0; row < reqs.size(); ++row)
-            for (int32_t b = lo[row]; b < hi[row]; ++b) {   // consecutive copies (block-scaled tiles rely on it)
+            for (int32_t b = first[row] > 0 ? 0 : lo[row]; b < hi[row]; ++b) {   // consecutive copies (block-scaled tiles rely on it)
+                if (b >= first[row] && b < lo[row]) continue;   // no tile's window reaches it
                 DequantItem di{};
                 di.req = reqs[row];
                 di.block = b;
@@ -592,8 +619,9 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
         const int32_t q_len = qsl[r + 1] - qsl[r];
         if (!on_decode[r]) continue;
         for (int32_t j = 0; j < q_len; j += tg) {
-            const int32_t n = std::min(tg, q_len - j);
-            units.push_back({r, qsl[r] + j, n, d->num_computed_tokens[r] + j + n});
+            const int32_t n = std::min(tg, q_len - j), p0 = d->num_computed_tokens[r] + j;
+            const int32_t skip = win ? window_view(p0, p0 + n, P->window, P->sinks, 1).skip : 0;
+            units.push_back({r, qsl[r] + j, n, p0 + n, skip});
         }
     }
     // staged inputs: the decode stream may read rows below the shape's
@@ -632,7 +660,7 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
         }
         const int64_t row_bytes = static_cast<int64_t>(P->Hkv) * P->D * (P->kv8 ? 1 : 2) * 2;
         for (const DecodeUnit &u : units)
-            model.decode_bytes += static_cast<double>(std::max(0, u.key_end - kb_keys)) * row_bytes;
+            model.decode_bytes += static_cast<double>(std::max(0, u.keys() - kb_keys)) * row_bytes;
         model.sm_rate = P->kv8 ? kSmFp8BytesPerUs : kSmBf16BytesPerUs;
         if (P->kv8) {
             model.side_step = kTileStepSideFp8Us;
@@ -909,15 +937,53 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
                          (P->cap_dequant > 0 ? 1 : 0);
     I.num_dequant_blocks = P->num_scratch_blocks;
     const int64_t row_bytes = static_cast<int64_t>(P->Hkv) * P->D * 2 * (P->kv8 ? 1 : 2);   // K and V
-    for (const DecodeUnit &u : units) I.decode_kv_bytes += std::max(0, u.key_end - kb_keys) * row_bytes;
+    for (const DecodeUnit &u : units) {
+        const int32_t low = win ? window_low(u.key_end - u.n_tok, P->window) : 0;
+        I.decode_kv_bytes += std::max(0, std::min(P->sinks, low) + u.key_end - low - kb_keys) * row_bytes;
+    }
     I.prefix_kv_bytes = cascade ? kb_keys * row_bytes : 0;
     double pairs = 0.0;   // sum over the row's queries i of (num_computed + i + 1 - prefix keys)
     for (int32_t r : extend_rows) {
         const double q_len = qsl[r + 1] - qsl[r];
+        if (win) {
+            for (int32_t p = d->num_computed_tokens[r]; p < d->seq_lens[r]; ++p) {
+                const int32_t low = window_low(p, P->window);
+                pairs += std::min(P->sinks, low) + p + 1 - low;
+            }
+            continue;
+        }
         pairs += q_len * (d->num_computed_tokens[r] + 1 - kb_keys) + q_len * (q_len - 1) / 2;
     }
     I.extend_flops = 4.0 * P->D * P->Hq * pairs;
     I.prefix_flops = cascade ? 4.0 * P->D * P->Hq * static_cast<double>(P->T) * kb_keys : 0.0;
+    return PA_OK;
+}
+
+// The three planning calls: `shape` null for a plain plan, `win` null for one
+// without a window.
+pa_status make_plan(const pa_batch_desc *desc, const pa_fixed_shape *shape, const pa_window_desc *win, pa_plan_t **out,
+                    size_t *workspace_bytes) {
+    if (shape && (shape->max_tokens <= 0 || shape->max_reqs <= 0 || shape->max_extend_tiles < 0 ||
+                  shape->max_dequant_blocks < 0 || shape->max_partial_slots < 0 || shape->decode_prefix_tokens < 0))
+        return PA_ERR_INVALID_ARGUMENT;
+    pa_status st = validate(desc, win);
+    if (st != PA_OK) return st;
+    if (win && desc->num_common_prefix_blocks > 0) return PA_ERR_UNSUPPORTED;
+    if (shape && desc->kv_cache_dtype != PA_KV_BF16 && shape->max_extend_tiles > 0 && shape->max_dequant_blocks == 0)
+        return PA_ERR_INVALID_ARGUMENT;   // tiles over 8-bit caches read 16-bit copies: they need room
+    pa_plan_s *P = new (std::nothrow) pa_plan_s();
+    if (!P) return PA_ERR_INVALID_ARGUMENT;
+    try {
+        st = build_plan(P, desc, shape, win);
+    } catch (const std::bad_alloc &) {   // (nothing throws across the ABI)
+        st = PA_ERR_INVALID_ARGUMENT;
+    }
+    if (st != PA_OK) {
+        delete P;
+        return st;
+    }
+    *out = P;
+    *workspace_bytes = P->ws_bytes;
     return PA_OK;
 }
 
@@ -973,10 +1039,11 @@ SideStream *side_stream() {
 
 pa_status prepare_plan(pa_plan_s *P) {
     if (P->prepared) return PA_OK;
-    if (P->ncta > 0 && (P->scaled ? prepare_scaled_decode(P->D, P->HG, P->int8) : prepare_decode(P->D, P->HG, P->kv8)) !=
-                           cudaSuccess)
+    const bool window = P->window > 0;
+    if (P->ncta > 0 && (P->scaled ? prepare_scaled_decode(P->D, P->HG, P->int8, window)
+                                  : prepare_decode(P->D, P->HG, P->kv8, window)) != cudaSuccess)
         return PA_ERR_CUDA;
-    if (P->cap_tiles > 0 && (P->scaled ? prepare_scaled_extend(P->D) : prepare_extend(P->D)) != cudaSuccess)
+    if (P->cap_tiles > 0 && (P->scaled ? prepare_scaled_extend(P->D, window) : prepare_extend(P->D, window)) != cudaSuccess)
         return PA_ERR_CUDA;
     if (P->fork && side_stream() == nullptr) return PA_ERR_CUDA;
     P->prepared = true;
@@ -1121,6 +1188,8 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
         ep.heads_per_group = P->HG;
         ep.scale_log2 = P->scale_log2;
         ep.out_scale = P->out_scale;
+        ep.window = P->window;
+        ep.sinks = P->sinks;
         if (rec(1, true, tile_stream) != cudaSuccess) return PA_ERR_CUDA;
         const ScaledExtendParams sep{ep, reinterpret_cast<const float4 *>(ws + P->off_factors)};
         if ((P->scaled ? launch_scaled_extend(P->D, P->ext_ctas, tm_q, tm_tk, tm_tv, sep, tile_stream, !fork)
@@ -1159,6 +1228,8 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
         dp.num_heads_kv = P->Hkv;
         dp.k_scale = P->k_scale;
         dp.v_scale = P->v_scale;
+        dp.window = P->window;
+        dp.sinks = P->sinks;
         if (rec(0, true, stream) != cudaSuccess) return PA_ERR_CUDA;
         if ((P->scaled ? launch_scaled_decode(P->D, P->HG, P->int8, P->ncta, tm_dk, tm_dv,
                                               ScaledDecodeParams{dp, scales.key, scales.value}, stream)
@@ -1207,18 +1278,7 @@ const char *pa_status_string(pa_status s) {
 pa_status pa_plan(const pa_batch_desc *desc, pa_plan_t **out, size_t *workspace_bytes) {
     if (out) *out = nullptr;
     if (desc == nullptr || out == nullptr || workspace_bytes == nullptr) return PA_ERR_INVALID_ARGUMENT;
-    pa_status st = validate(desc);
-    if (st != PA_OK) return st;
-    pa_plan_s *P = new (std::nothrow) pa_plan_s();
-    if (!P) return PA_ERR_INVALID_ARGUMENT;
-    st = build_plan(P, desc, nullptr);
-    if (st != PA_OK) {
-        delete P;
-        return st;
-    }
-    *out = P;
-    *workspace_bytes = P->ws_bytes;
-    return PA_OK;
+    return make_plan(desc, nullptr, nullptr, out, workspace_bytes);
 }
 
 pa_status pa_plan_fixed(const pa_batch_desc *desc, const pa_fixed_shape *shape, pa_plan_t **out,
@@ -1226,23 +1286,16 @@ pa_status pa_plan_fixed(const pa_batch_desc *desc, const pa_fixed_shape *shape, 
     if (out) *out = nullptr;
     if (desc == nullptr || shape == nullptr || out == nullptr || workspace_bytes == nullptr)
         return PA_ERR_INVALID_ARGUMENT;
-    if (shape->max_tokens <= 0 || shape->max_reqs <= 0 || shape->max_extend_tiles < 0 ||
-        shape->max_dequant_blocks < 0 || shape->max_partial_slots < 0 || shape->decode_prefix_tokens < 0)
+    return make_plan(desc, shape, nullptr, out, workspace_bytes);
+}
+
+pa_status pa_plan_window(const pa_batch_desc *desc, const pa_window_desc *window, const pa_fixed_shape *shape,
+                         pa_plan_t **out, size_t *workspace_bytes) {
+    if (out) *out = nullptr;
+    if (desc == nullptr || window == nullptr || out == nullptr || workspace_bytes == nullptr ||
+        window->window <= 0 || window->sink_tokens < 0)
         return PA_ERR_INVALID_ARGUMENT;
-    pa_status st = validate(desc);
-    if (st != PA_OK) return st;
-    if (desc->kv_cache_dtype != PA_KV_BF16 && shape->max_extend_tiles > 0 && shape->max_dequant_blocks == 0)
-        return PA_ERR_INVALID_ARGUMENT;   // tiles over 8-bit caches read 16-bit copies: they need room
-    pa_plan_s *P = new (std::nothrow) pa_plan_s();
-    if (!P) return PA_ERR_INVALID_ARGUMENT;
-    st = build_plan(P, desc, shape);
-    if (st != PA_OK) {
-        delete P;
-        return st;
-    }
-    *out = P;
-    *workspace_bytes = P->ws_bytes;
-    return PA_OK;
+    return make_plan(desc, shape, window, out, workspace_bytes);
 }
 
 void pa_plan_destroy(pa_plan_t *P) {

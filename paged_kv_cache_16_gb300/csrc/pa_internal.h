@@ -60,12 +60,42 @@ constexpr int kErrSlotRange = 0x1;
 constexpr int kErrBlockRange = 0x2;
 constexpr int kErrTimeout = 0x4;
 
+// Which blocks the query tokens at positions [first, end) of a request read
+// under a sliding window with `sinks` first tokens that stay visible (a query at
+// position p sees key j <= p where p - j < window or j < sinks): the head, blocks
+// with first tokens, and every block from the window of the first query on.  The
+// work lists number them without the gap between: block n of that numbering is
+// logical block at(n), and key v of it is logical key v + 16 skip from the head
+// on.  In those numbers a query that sees keys below `lim` sees v < lim with v <
+// sinks or v >= lim - window, gap or no gap.  `unit`: the head is padded to whole
+// units of blocks (its spare blocks are hidden, like first-token slots from `sinks`
+// on).
+struct WindowView {
+    int32_t head;   // blocks of the head (0: no first tokens, or no gap behind them)
+    int32_t skip;   // logical minus own number, from the head on (below 1 only by padding)
+    __host__ __device__ constexpr int32_t at(int32_t n) const { return n < head ? n : n + skip; }
+};
+__host__ __device__ constexpr int32_t window_low(int32_t first, int32_t window) {
+    return first - window + 1 > 0 ? first - window + 1 : 0;   // first key of the window
+}
+__host__ __device__ constexpr int32_t head_blocks(int32_t end, int32_t sinks) {
+    const int32_t n = sinks < end ? sinks : end;
+    return n / kBlockSize + (n % kBlockSize != 0 ? 1 : 0);
+}
+__host__ __device__ constexpr WindowView window_view(int32_t first, int32_t end, int32_t window, int32_t sinks,
+                                                     int32_t unit) {
+    const int32_t low = window_low(first, window) / kBlockSize, head = head_blocks(end, sinks);
+    if (low <= head) return WindowView{0, 0};   // one run of blocks
+    const int32_t padded = (head + unit - 1) / unit * unit;
+    return WindowView{padded, low - padded};
+}
+
 // One contiguous run of one request's key blocks for one group of kv heads,
 // processed by one persistent CTA of the split-KV decode kernel.
 struct DecodeItem {
     int32_t token;       // query row (q / out row)
     int32_t req;         // block-table row
-    int32_t page_begin;  // first logical block of the run
+    int32_t page_begin;  // first logical block of the run (windowed plans: WindowView's numbers)
     int32_t page_end;    // one past the last logical block of the run
     int32_t key_end;     // keys >= key_end are masked (one past the last token's position)
     int32_t head_group;  // kv heads [head_group*HG, head_group*HG + HG)
@@ -87,7 +117,10 @@ struct ExtendTile {
     int32_t kv_head;
     int32_t part;        // partial index (-1: write bf16 output)
     int32_t causal;      // 0: every key of the range is visible (shared prefix)
-    int32_t pad[3];
+    // windowed plans: pos0, key_begin and key_end are in WindowView's numbers
+    int32_t head;        // its fields
+    int32_t skip;
+    int32_t pad;
 };
 
 // The query heads [hq_begin, hq_begin + hq_count) of one token whose output
@@ -133,6 +166,7 @@ struct DecodeParams {
     int64_t *slots_out;         // optional [T]
     int32_t num_heads_kv;
     float k_scale, v_scale;     // E4M3 quantisation scales of the write
+    int32_t window, sinks;      // window > 0: see WindowView
 };
 
 // The same over block-scaled 8-bit caches (base.out_scale is 1, the fused
@@ -161,6 +195,7 @@ struct ExtendParams {
     int32_t heads_per_group;    // kv heads per head group (indexes part_offset)
     float scale_log2;           // softmax_scale * k_scale * log2(e)
     float out_scale;            // v_scale (1 for bf16 caches)
+    int32_t window, sinks;      // window > 0: see WindowView
 };
 
 // The same over block-scaled 8-bit caches (base.out_scale is unused): the K
@@ -265,10 +300,17 @@ struct RopeParams {
     int32_t interleaved;        // pairs (2i, 2i + 1), else (i, i + rotary_dim / 2)
 };
 
+// The same with positions on several axes: pair i turns by its own one.
+constexpr int kMaxAxes = 4;
+struct AxesRopeParams : RopeParams {
+    uint8_t axis[kMaxRotaryDim / 2];
+};
+
 struct RotaryParams {
     const uint16_t *x;          // bf16 rows [T][H][D], token stride in elements
     uint16_t *out;
-    const int32_t *positions;   // [T]
+    const int32_t *positions;   // [T]; axes: [axes][axis_stride]
+    int64_t axis_stride;
     int64_t x_stride, out_stride;
     int32_t num_tokens, num_heads, head_dim;
     int32_t log_tokens, heads_per_cta;   // a CTA's tokens (log2) and heads
@@ -296,6 +338,8 @@ struct AppendParams {
     int32_t num_reqs, num_tokens, num_heads_q, num_heads_kv;
     int32_t num_blocks, max_blocks;
     int32_t q_heads_per_cta;
+    const int32_t *positions;   // axes: [axes][axis_stride], by token row
+    int64_t axis_stride;
 };
 
 // Launch with programmatic stream serialisation when `pdl` (the kernel calls
@@ -340,7 +384,8 @@ cudaError_t launch_write_kv_fp8(const void *key, const void *value, const int64_
 // capacity is as correct as an exact one.
 cudaError_t launch_dequant(int grid, const DequantParams &p, cudaStream_t stream, bool pdl = true);
 // Decode kernel: head_dim D, heads per CTA hg, E4M3 caches (kv8).  Returns
-// cudaErrorInvalidValue for an unsupported combination.
+// cudaErrorInvalidValue for an unsupported combination.  The attention
+// launchers run the variant with a window where p.window > 0.
 cudaError_t launch_decode(int head_dim, int hg, bool kv8, int num_ctas, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const DecodeParams &p, cudaStream_t stream);
 cudaError_t launch_scaled_decode(int head_dim, int hg, bool int8, int num_ctas, const CUtensorMap &tm_k,
@@ -361,14 +406,17 @@ cudaError_t launch_write_runs(int grid, const WriteParams &p, cudaStream_t strea
 // as they are).
 cudaError_t launch_rotary(const RopeParams &rope, const RotaryParams &p, cudaStream_t stream);
 cudaError_t launch_append(int head_dim, int kind, const RopeParams &rope, const AppendParams &p, cudaStream_t stream);
+// The same with positions on several axes, given per token.
+cudaError_t launch_rotary_axes(const AxesRopeParams &rope, const RotaryParams &p, cudaStream_t stream);
+cudaError_t launch_append_axes(int head_dim, int kind, const AxesRopeParams &rope, const AppendParams &p, cudaStream_t stream);
 // Zero the K and V entries of the listed blocks (ids < 0 skipped).
 cudaError_t launch_zero_blocks(const int32_t *ids, int32_t num_ids, int32_t num_blocks, int64_t block_bytes,
                                void *key_cache, void *value_cache, int32_t *err, cudaStream_t stream);
 // One-time per-process kernel attributes (dynamic shared memory sizes) of the
 // kernels a plan launches, so that later launches can be captured.
-cudaError_t prepare_decode(int head_dim, int hg, bool kv8);
-cudaError_t prepare_scaled_decode(int head_dim, int hg, bool int8);
-cudaError_t prepare_extend(int head_dim);
-cudaError_t prepare_scaled_extend(int head_dim);
+cudaError_t prepare_decode(int head_dim, int hg, bool kv8, bool window);
+cudaError_t prepare_scaled_decode(int head_dim, int hg, bool int8, bool window);
+cudaError_t prepare_extend(int head_dim, bool window);
+cudaError_t prepare_scaled_extend(int head_dim, bool window);
 
 }  // namespace pa

@@ -4,6 +4,8 @@ Thin glue over the C ABI; torch only allocates memory and supplies streams.
 """
 from __future__ import annotations
 
+import functools
+
 import numpy as np
 import torch
 
@@ -27,13 +29,28 @@ def _check_scales(scaled: bool, key_scales, value_scales):
         raise ValueError("key_scales and value_scales wanted" if scaled else "a step of caches without block scales")
 
 
-def _append(rope, step, k_scale, v_scale, q, key, value, key_cache, value_cache, key_scales, value_scales, stream):
+def _check_positions(rope, positions):
+    """Rotations of several axes come with positions (one axis may), steps without a
+    rotation with none."""
+    if positions is None and rope is not None and rope.num_axes > 1:
+        raise ValueError(f"positions [{rope.num_axes}, tokens] wanted")
+    if positions is not None and rope is None:
+        raise ValueError("positions without a rope")
+
+
+def _append(rope, step, k_scale, v_scale, q, key, value, key_cache, value_cache, key_scales, value_scales, stream,
+            positions=None):
     """pa_append_kv with a step's metadata: the cache write with the rotation (if
     any) on the way; returns the queries to attend with."""
     rotated = {} if rope is None else dict(q=q, q_out=step.q_rot[:q.shape[0]])
-    binding.pa_append_kv(rope, key, value, step.qsl, step.num_computed, step.block_table, key_cache, value_cache,
-                         key_scales=key_scales, value_scales=value_scales, k_scale=k_scale, v_scale=v_scale,
-                         device_error_word=step.error_word, stream=stream, **rotated)
+    args = (step.qsl, step.num_computed, step.block_table, key_cache, value_cache)
+    more = dict(key_scales=key_scales, value_scales=value_scales, k_scale=k_scale, v_scale=v_scale,
+                device_error_word=step.error_word, stream=stream, **rotated)
+    _check_positions(rope, positions)
+    if positions is None:
+        binding.pa_append_kv(rope, key, value, *args, **more)
+    else:
+        binding.pa_append_kv_axes(rope, key, value, positions, *args, **more)
     return q if rope is None else step.q_rot[:q.shape[0]]
 
 
@@ -42,13 +59,16 @@ class DeviceStep:
 
     ``rope`` (binding.pa_rope_create): run_append rotates queries and keys by
     their positions on the way into the cache (write, run and run_fused, which
-    do not rotate, refuse such a step).  Block-scaled caches
-    ("fp8_block", "int8_block") go through run_append / append and attend, with
-    their scales."""
+    do not rotate, refuse such a step); with a rope of several axes
+    (binding.pa_rope_create_axes) it takes the positions.  ``window``: (window,
+    sink_tokens) of a layer whose queries see a sliding window and first tokens.
+    Block-scaled caches ("fp8_block", "int8_block") go through run_append / append
+    and attend, with their scales."""
 
-    def __init__(self, batch: Batch, device="cuda", num_sms: int = 0, plan: bool = True, rope=None):
+    def __init__(self, batch: Batch, device="cuda", num_sms: int = 0, plan: bool = True, rope=None, window=None):
         self.batch = batch
         self.rope = rope
+        self.window = window
         dev = torch.device(device)
         self.device = dev
         self.qsl = torch.as_tensor(batch.query_start_loc, device=dev)
@@ -66,14 +86,17 @@ class DeviceStep:
 
     def make_plan(self) -> binding.Plan:
         b = self.batch
-        return binding.pa_plan(num_heads_q=b.num_heads_q, num_heads_kv=b.num_heads_kv, head_dim=b.head_dim,
-                               num_blocks=b.num_blocks, query_start_loc=b.query_start_loc,
-                               seq_lens=b.seq_lens, num_computed_tokens=b.num_computed,
-                               block_table_host=b.block_table,
-                               num_common_prefix_blocks=b.num_common_prefix_blocks,
-                               softmax_scale=b.softmax_scale, num_sms=self.num_sms,
-                               block_size=b.block_size,
-                               kv_cache_dtype=kv_dtype(b.kv_cache_dtype), k_scale=b.k_scale, v_scale=b.v_scale)
+        make = binding.pa_plan
+        if self.window is not None:
+            make = functools.partial(binding.pa_plan_window, window=self.window[0], sink_tokens=self.window[1])
+        return make(num_heads_q=b.num_heads_q, num_heads_kv=b.num_heads_kv, head_dim=b.head_dim,
+                    num_blocks=b.num_blocks, query_start_loc=b.query_start_loc,
+                    seq_lens=b.seq_lens, num_computed_tokens=b.num_computed,
+                    block_table_host=b.block_table,
+                    num_common_prefix_blocks=b.num_common_prefix_blocks,
+                    softmax_scale=b.softmax_scale, num_sms=self.num_sms,
+                    block_size=b.block_size,
+                    kv_cache_dtype=kv_dtype(b.kv_cache_dtype), k_scale=b.k_scale, v_scale=b.v_scale)
 
     @property
     def error_word(self) -> torch.Tensor:
@@ -108,16 +131,19 @@ class DeviceStep:
                                         self.block_table, self.out, self.workspace, stream)
         return self.out[:self.batch.num_tokens]
 
-    def append(self, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None, stream=None):
+    def append(self, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None, stream=None,
+               positions=None):
         """Cache write of the new rows into any cache type, keys rotated if the
-        step has a rope; returns the (then rotated) queries."""
+        step has a rope (by positions [axes, T] if given, else by their place in the
+        context); returns the (then rotated) queries."""
         _check_scales(self.batch.kv_cache_dtype in ("fp8_block", "int8_block"), key_scales, value_scales)
         return _append(self.rope, self, self.batch.k_scale, self.batch.v_scale, q, key, value, key_cache, value_cache,
-                       key_scales, value_scales, stream)
+                       key_scales, value_scales, stream, positions)
 
-    def run_append(self, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None, stream=None):
+    def run_append(self, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None, stream=None,
+                   positions=None):
         """append -> attention; returns out [T, Hq, D]."""
-        q = self.append(q, key, value, key_cache, value_cache, key_scales, value_scales, stream)
+        q = self.append(q, key, value, key_cache, value_cache, key_scales, value_scales, stream, positions)
         return self.attend(q, key_cache, value_cache, stream, None, key_scales, value_scales)
 
     def run(self, q, key, value, key_cache, value_cache, stream=None):
@@ -217,17 +243,24 @@ class GraphStep:
     output back to page-locked memory, so a replay goes from host memory to
     host memory.  With a ``rope``, and for block-scaled caches (whose scales
     capture and run take), the graphs hold pa_append_kv and the attention
-    launch instead.
+    launch instead; with a rope of several axes they rotate by a static buffer of
+    positions that run fills.  ``window``: (window, sink_tokens) of a layer whose
+    queries see a sliding window and first tokens.
     """
 
     def __init__(self, *, num_heads_q, num_heads_kv, head_dim, num_blocks, max_blocks_per_req, softmax_scale,
                  max_tokens, max_reqs, max_extend_tiles=0, max_dequant_blocks=0, max_partial_slots=0,
                  kv_cache_dtype="bf16", k_scale=1.0, v_scale=1.0, num_sms=0, device="cuda", fused=True,
-                 host_io=False, rope=None):
+                 host_io=False, rope=None, window=None):
         dev = torch.device(device)
         self.device = dev
         self.fused = fused
         self.rope = rope
+        self.window = window
+        axes = rope.num_axes if rope is not None else 1
+        if axes > 1 and host_io:
+            raise ValueError("host_io: the input image holds no positions")
+        self.positions = torch.zeros(axes, max_tokens, dtype=torch.int32, device=dev) if axes > 1 else None
         self.scaled = kv_cache_dtype in ("fp8_block", "int8_block")
         self.model = dict(num_heads_q=num_heads_q, num_heads_kv=num_heads_kv, head_dim=head_dim,
                           num_blocks=num_blocks, max_blocks_per_req=max_blocks_per_req,
@@ -272,24 +305,33 @@ class GraphStep:
             padded = np.zeros((bt.shape[0], mb), dtype=np.int32)
             padded[:, :bt.shape[1]] = bt
             bt = padded
-        return binding.pa_plan_fixed(**self.shape, query_start_loc=batch.query_start_loc, seq_lens=batch.seq_lens,
-                                     num_computed_tokens=batch.num_computed, block_table_host=bt,
-                                     num_common_prefix_blocks=batch.num_common_prefix_blocks, **self.model)
+        make = functools.partial(binding.pa_plan_fixed, **self.shape)
+        if self.window is not None:
+            make = functools.partial(binding.pa_plan_window, window=self.window[0], sink_tokens=self.window[1],
+                                     shape=self.shape)
+        return make(query_start_loc=batch.query_start_loc, seq_lens=batch.seq_lens,
+                    num_computed_tokens=batch.num_computed, block_table_host=bt,
+                    num_common_prefix_blocks=batch.num_common_prefix_blocks, **self.model)
 
     @property
     def error_word(self) -> torch.Tensor:
         return self.workspace[:4].view(torch.int32)
 
-    def load(self, batch: Batch, plan: binding.Plan, q=None, key=None, value=None, stream=None):
+    def load(self, batch: Batch, plan: binding.Plan, q=None, key=None, value=None, stream=None, positions=None):
         """Copy a step's metadata (and, if given, its new q / key / value rows)
         into the static buffers and upload the plan's metadata (not captured)."""
-        self.stage(batch, q, key, value)
+        self.stage(batch, q, key, value, positions)
         if self.workspace is None:
             self.workspace = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device=self.device)
         binding.pa_upload_metadata(plan, self.workspace, stream)
 
-    def stage(self, batch: Batch, q=None, key=None, value=None):
-        """Copy a step's request metadata and new rows into the static buffers."""
+    def stage(self, batch: Batch, q=None, key=None, value=None, positions=None):
+        """Copy a step's request metadata and new rows (and their positions on several
+        axes) into the static buffers."""
+        if positions is not None:
+            if self.positions is None or positions.shape != (self.positions.shape[0], batch.num_tokens):
+                raise ValueError("positions: [axes, tokens] of a rope of several axes wanted")
+            self.positions[:, :batch.num_tokens].copy_(positions)
         _fill({"q": self.q, "key": self.key, "value": self.value, "qsl": self.qsl,
                "num_computed": self.num_computed, "block_table": self.block_table}, batch, q, key, value)
 
@@ -318,7 +360,7 @@ class GraphStep:
         _check_scales(self.scaled, key_scales, value_scales)
         if self.rope is not None or self.scaled:
             q = _append(self.rope, self, self.k_scale, self.v_scale, self.q, self.key, self.value, key_cache, value_cache,
-                        key_scales, value_scales, stream)
+                        key_scales, value_scales, stream, self.positions)
             if self.scaled:
                 binding.pa_attention_scaled_launch(plan, q, key_cache, value_cache, key_scales, value_scales,
                                                    self.block_table, self.out, self.workspace, stream)
@@ -388,11 +430,14 @@ class GraphStep:
         self.prepare_replay(plan)
         self.launch_replay()
 
-    def run(self, batch: Batch, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None) -> torch.Tensor:
+    def run(self, batch: Batch, q, key, value, key_cache, value_cache, key_scales=None, value_scales=None,
+            positions=None) -> torch.Tensor:
         """One step: plan, copy in, replay (capturing on first use)."""
         _check_scales(self.scaled, key_scales, value_scales)
+        if (positions is not None) != (self.positions is not None):
+            raise ValueError("positions wanted exactly with a rope of several axes")
         plan = self.make_plan(batch)
-        self.stage(batch, q, key, value)
+        self.stage(batch, q, key, value, positions)
         if self.graphs is None:
             self.capture(plan, key_cache, value_cache, key_scales, value_scales)
         elif self.caches != self._addresses(key_cache, value_cache, key_scales, value_scales):
