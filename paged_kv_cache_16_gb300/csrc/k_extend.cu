@@ -33,12 +33,13 @@
 // (P_t in the first 64 columns of S_t), O_0 [256,256+D), O_1 [384,384+D).
 // Shared memory tiles are 128-byte-swizzled [rows][64 elements] halves:
 // Q_t (A, K-major), K (B, K-major), V (B, MN-major).
-#include "dev.cuh"
+#include "tiles.cuh"
 
 namespace pa {
 namespace {
 
 using namespace dev;
+using namespace tiles;
 
 template <int D>
 struct ExtCfg {
@@ -63,52 +64,6 @@ struct ExtCfg {
     static constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true);
 };
 
-
-__device__ __forceinline__ uint32_t col_s(int t) { return static_cast<uint32_t>(t) * 128u; }
-__device__ __forceinline__ uint32_t col_o(int t) { return 256u + static_cast<uint32_t>(t) * 128u; }
-
-// barrier indices.  K and V stages are released separately: a K stage as
-// soon as the QK^T MMAs reading it finish, a V stage after the PV MMAs, so the
-// next K tile is loaded while the current tile's softmax and PV still run.
-// The CTA is persistent: rings, barriers and tensor memory carry over from one
-// tile to the next, and the next tile's Q is loaded as soon as the current
-// tile's last QK^T has read Q (QEMPTY), under the tile's last PV, softmax and
-// epilogue.
-enum : int {
-    B_QFULL = 0,
-    B_QEMPTY = 1,
-    B_KFULL = 2,    // +stage (2)
-    B_VFULL = 4,    // +stage (3)
-    B_KEMPTY = 7,   // +stage (2)
-    B_VEMPTY = 9,   // +stage (3)
-    B_SFULL = 12,   // +sub-tile
-    B_PFULL = 14,   // +sub-tile
-    B_ODONE = 16,   // +sub-tile
-    B_DRAIN = 18,
-    NUM_BARS = 19
-};
-
-// key tiles each sub-tile of a CTA tile needs (0 for an empty sub-tile)
-struct TileShape {
-    int n_sub[2];
-    int n_tiles;
-};
-__device__ __forceinline__ TileShape tile_shape(const ExtendTile &tile, int tpt) {
-    TileShape sh;
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        const int first = t * tpt;
-        if (first >= tile.n_tok) {
-            sh.n_sub[t] = 0;
-            continue;
-        }
-        const int last = min(tile.n_tok, first + tpt);   // one past the sub-tile's last token
-        const int kend = tile.causal ? min(tile.key_end, tile.pos0 + last) : tile.key_end;
-        sh.n_sub[t] = (kend - tile.key_begin + kTileKeys - 1) / kTileKeys;
-    }
-    sh.n_tiles = max(sh.n_sub[0], sh.n_sub[1]);
-    return sh;
-}
 
 // WIN: with a sliding window and first tokens (tiles in WindowView's numbers: key
 // tiles of 128 keys run over the blocks with first tokens and on into those of the
@@ -135,7 +90,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const int tile_begin = p.cta_tile_begin[blockIdx.x];
     const int tile_end = p.cta_tile_begin[blockIdx.x + 1];
     if (tile_begin >= tile_end) return;
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (uniform to the compiler)
     const int lane = threadIdx.x & 31;
     const int G = p.group;
     const int tpt = kTileRows / G;                    // tokens per 128-row sub-tile
@@ -154,7 +109,8 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(bar(B_SFULL + t), 1);
-            mbar_init(bar(B_PFULL + t), 128);
+            mbar_init(bar(B_PFULL + t), 4);       // a warp each
+            mbar_init(bar(B_PFULL + 2 + t), 4);
             mbar_init(bar(B_ODONE + t), 1);
         }
         mbar_init(bar(B_DRAIN), 1);
@@ -265,122 +221,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer --
-        if (lane == 0) {
-            int kc = 0, vc = 0;          // K and V tiles consumed (over all tiles)
-            int pc[2] = {0, 0};          // P tiles consumed per sub-tile
-            int n_q = 0;                 // Q tiles consumed
-            bool ok = true;
-            // operand descriptors built once; each MMA only moves the start
-            // address (the issuing thread shares its issue slots with two
-            // softmax warps, so every instruction here counts)
-            const uint64_t q_desc[2] = {sdesc_sw128(q_s(0), 16, 1024), sdesc_sw128(q_s(1), 16, 1024)};
-            const uint64_t k_desc0 = sdesc_sw128(k_s(0), 16, 1024);
-            const uint64_t v_desc0 = sdesc_sw128(v_s(0), C::HALF, 1024);
-            // readiness of the barriers the thread needs next, polled (one
-            // test each) between MMAs, where the pipe still holds queued work
-            bool p_ready[2] = {false, false}, k_ready = false, v_ready = false;
-            auto poll = [&](bool &flag, int b, int parity) {
-                if (!flag) flag = mbar_test_wait(bar(b), static_cast<uint32_t>(parity));
-            };
-            auto qk = [&](int t, int s, auto mid) {
-                const uint64_t a0 = q_desc[t];
-                const uint64_t b0 = sdesc_advance(k_desc0, static_cast<uint32_t>(s) * C::KVB);
-                const uint32_t d = tmem + col_s(t);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk / 4) * C::HALF + (kk % 4) * 32;
-                    tc_mma(d, sdesc_advance(a0, off), sdesc_advance(b0, off), C::IDESC_QK, kk > 0 ? 1u : 0u);
-                    if (kk == D / 32 - 1) mid();
-                }
-                tc_commit(bar(B_SFULL + t));
-            };
-            auto pv = [&](int t, int sv, bool first, auto mid) -> bool {
-                if (!p_ready[t] && !mbar_wait_spin(bar(B_PFULL + t), pc[t] & 1, &abort_flag)) return false;
-                p_ready[t] = false;
-                ++pc[t];
-                tc_fence_after();
-                const uint64_t b0 = sdesc_advance(v_desc0, static_cast<uint32_t>(sv) * C::KVB);
-                const uint32_t d = tmem + col_o(t), a = tmem + col_s(t);
-#pragma unroll
-                for (int kk = 0; kk < kTileKeys / 16; ++kk) {
-                    tc_mma_ts(d, a + kk * 8, sdesc_advance(b0, kk * 2048), C::IDESC_PV, (!first || kk > 0) ? 1u : 0u);
-                    if (kk == 3) mid();
-                }
-                return true;
-            };
-            auto nothing = [] {};
-            for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
-                const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-                const TileShape sh = tile_shape(tile, tpt);
-                ok = mbar_wait_spin(bar(B_QFULL), n_q & 1, &abort_flag);
-                ++n_q;
-                if (!ok || sh.n_tiles == 0) {
-                    if (ok) tc_commit(bar(B_QEMPTY));
-                    continue;
-                }
-                // QK^T still to issue in this tile; Q is released after the last
-                int q_left = sh.n_sub[0] + sh.n_sub[1];
-                ok = mbar_wait_spin(bar(B_KFULL + kc % C::NSK), (kc / C::NSK) & 1, &abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    if (sh.n_sub[t] > 0) {
-                        qk(t, kc % C::NSK, nothing);
-                        if (--q_left == 0) tc_commit(bar(B_QEMPTY));
-                    }
-                tc_commit(bar(B_KEMPTY + kc % C::NSK));   // K tile 0 read by both QK^T
-                ++kc;
-                for (int j = 0; j < sh.n_tiles && ok; ++j) {
-                    const int sv = vc % C::NSV;
-                    const int t_last = j < sh.n_sub[1] ? 1 : 0;   // last sub-tile that reads V tile j
-                    const bool k_next = j + 1 < sh.n_tiles;
-                    bool k_used = false;
-                    if (!v_ready) ok = mbar_wait_spin(bar(B_VFULL + sv), (vc / C::NSV) & 1, &abort_flag);
-                    v_ready = false;
-#pragma unroll
-                    for (int t = 0; t < 2 && ok; ++t) {
-                        if (j >= sh.n_sub[t]) continue;
-                        // during PV_0: the next K tile; during PV_1: the next V tile
-                        if (t == 0)
-                            ok = pv(0, sv, j == 0, [&] { if (k_next) poll(k_ready, B_KFULL + kc % C::NSK, (kc / C::NSK) & 1); });
-                        else
-                            ok = pv(1, sv, j == 0, [&] { poll(v_ready, B_VFULL + (vc + 1) % C::NSV, ((vc + 1) / C::NSV) & 1); });
-                        if (!ok) break;
-                        if (t == t_last) tc_commit(bar(B_VEMPTY + sv));   // V tile j read by both PV
-                        if (j + 1 < sh.n_sub[t]) {
-                            if (!k_ready) {
-                                ok = mbar_wait_spin(bar(B_KFULL + kc % C::NSK), (kc / C::NSK) & 1, &abort_flag);
-                                if (!ok) break;
-                                k_ready = true;
-                            }
-                            k_used = true;
-                            tc_fence_after();
-                            // overwrites S_t: issued after the PV that reads P_t.
-                            // During QK_0 poll P_1 of this step, during QK_1 P_0 of the next
-                            if (t == 0)
-                                qk(0, kc % C::NSK, [&] { if (j < sh.n_sub[1]) poll(p_ready[1], B_PFULL + 1, pc[1] & 1); });
-                            else
-                                qk(1, kc % C::NSK, [&] { poll(p_ready[0], B_PFULL + 0, pc[0] & 1); });
-                            if (--q_left == 0) tc_commit(bar(B_QEMPTY));
-                        } else {
-                            tc_commit(bar(B_ODONE + t));
-                        }
-                    }
-                    if (ok && k_used) {
-                        tc_commit(bar(B_KEMPTY + kc % C::NSK));   // K tile j+1 read by both QK^T
-                        ++kc;
-                        k_ready = false;
-                    }
-                    ++vc;
-                }
-            }
-            if (!ok) raise_abort(&abort_flag, p.err, kErrTimeout);
-            // every MMA of this CTA must finish before tensor memory is released
-            tc_commit(bar(B_DRAIN));
-            if (!mbar_wait(bar(B_DRAIN), 0, nullptr)) atomicOr(p.err, kErrTimeout);
-        }
-        __syncwarp();
+        issue_mmas<D, C>(p, smem_u32(bars), q_s(0), k_s(0), v_s(0), tmem, tile_begin, tile_end, tpt, lane, &abort_flag);
       }
     } else {
         // ------------------------------------------- softmax + epilogue --
@@ -453,23 +294,23 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 // scale-and-shift and the row sum run on packed fp32 pairs
                 const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2), shift2 = f32x2(nref, nref);
                 uint64_t la = f32x2(0.f, 0.f), lb = la;
+                auto weights = [&](int from) {   // 64 columns from there on
 #pragma unroll
-                for (int e = 0; e < 64; ++e) {
-                    float x0, x1;
-                    f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), scale2,
-                                          shift2),
-                                x0, x1);
-                    const float p0 = ex2(x0), p1 = ex2(x1);
-                    if (e & 1) lb = add_f32x2(lb, f32x2(p0, p1));
-                    else la = add_f32x2(la, f32x2(p0, p1));
-                    sr[e] = pack_bf16x2(p0, p1);
-                }
-                float a0, a1, b0, b1;
-                f32x2_split(la, a0, a1);
-                f32x2_split(lb, b0, b1);
-                l += (a0 + b0) + (a1 + b1);
-                tmem_st32(t_row + col_s(t) + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-                tmem_st32(t_row + col_s(t) + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+                    for (int i = 0; i < 32; ++i) {
+                        const int e = from / 2 + i;
+                        float x0, x1;
+                        f32x2_split(fma_f32x2(f32x2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), scale2,
+                                              shift2),
+                                    x0, x1);
+                        const float p0 = ex2(x0), p1 = ex2(x1);
+                        if (e & 1) lb = add_f32x2(lb, f32x2(p0, p1));
+                        else la = add_f32x2(la, f32x2(p0, p1));
+                        sr[e] = pack_bf16x2(p0, p1);
+                    }
+                    tmem_st32(t_row + col_s(t) + from / 2, *reinterpret_cast<uint32_t(*)[32]>(&sr[from / 2]));
+                };
+                // the first half of P, under which its PV can begin
+                weights(0);
                 if (j >= 1 && __any_sync(0xffffffffu, need)) {
                     // O_t holds the tiles before j (their PV completed before S_t(j) did)
 #pragma unroll 1
@@ -509,7 +350,17 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                     fence_proxy_async_smem();
                 }
                 tc_fence_before();
-                mbar_arrive(bar(B_PFULL + t));
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_PFULL + t));
+                weights(64);
+                float a0, a1, b0, b1;
+                f32x2_split(la, a0, a1);
+                f32x2_split(lb, b0, b1);
+                l += (a0 + b0) + (a1 + b1);
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(B_PFULL + 2 + t));
             }
             if (!ok) break;
             vbase += sh.n_tiles;
@@ -519,44 +370,13 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             ++ocnt;
             tc_fence_after();
             const float inv = l > 0.f ? p.out_scale / l : 0.f;
-            const bool wide = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;
             const int tok = tile.t0 + i;
             const int h = tile.kv_head * G + gq;
             int64_t slot = -1;
             if (tile.part >= 0 && tok_valid)
                 slot = static_cast<int64_t>(p.part_offset[tok * p.n_groups + tile.kv_head / p.heads_per_group]) +
                        tile.part;
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-                uint32_t orr[32];
-                tmem_ld32(t_row + col_o(t) + c, orr);
-                tmem_wait_ld();
-                if (!tok_valid) continue;
-                if (tile.part < 0) {
-                    uint16_t *dst = p.out + (static_cast<int64_t>(tok) * p.num_heads_q + h) * D + c;
-#pragma unroll
-                    for (int q8 = 0; q8 < 2; ++q8) {
-                        uint32_t w[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            w[e] = pack_bf16x2(__uint_as_float(orr[q8 * 16 + 2 * e]) * inv,
-                                               __uint_as_float(orr[q8 * 16 + 2 * e + 1]) * inv);
-                        st_row_v8(wide, dst + q8 * 16, w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]);
-                    }
-                } else {
-                    float *dst = p.o_part + (slot * p.num_heads_q + h) * D + c;
-#pragma unroll
-                    for (int q8 = 0; q8 < 4; ++q8)
-                        st_global_v8(dst + q8 * 8, __float_as_uint(__uint_as_float(orr[q8 * 8 + 0]) * inv),
-                                     __float_as_uint(__uint_as_float(orr[q8 * 8 + 1]) * inv),
-                                     __float_as_uint(__uint_as_float(orr[q8 * 8 + 2]) * inv),
-                                     __float_as_uint(__uint_as_float(orr[q8 * 8 + 3]) * inv),
-                                     __float_as_uint(__uint_as_float(orr[q8 * 8 + 4]) * inv),
-                                     __float_as_uint(__uint_as_float(orr[q8 * 8 + 5]) * inv),
-                                     __float_as_uint(__uint_as_float(orr[q8 * 8 + 6]) * inv),
-                                     __float_as_uint(__uint_as_float(orr[q8 * 8 + 7]) * inv));
-                }
-            }
+            store_output<D>(p, t_row + col_o(t), tok_valid, tile.part, tok, h, slot, inv, lane);
             if (tok_valid && tile.part >= 0) p.ml_part[slot * p.num_heads_q + h] = make_float2(m, l);
             tc_fence_before();
         }
