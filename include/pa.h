@@ -367,6 +367,11 @@ pa_status pa_plan_fixed(const pa_batch_desc *desc, const pa_fixed_shape *shape, 
  * 0 times it).
  * Fixed shapes: window and sink_tokens count as model fields, as the kernels'
  * arguments hold them.  max_dequant_blocks counts blocks that some query sees.
+ * Tiles that leave SMs idle are cut along their keys where that ends the step sooner
+ * (pa_plan_info.num_extend_tiles counts the pieces; joined by the merge); a fixed shape
+ * cuts them like pa_plan_window without a shape does, if its max_extend_tiles and
+ * max_partial_slots have room for all pieces, else (and with decode_prefix_tokens) not
+ * at all: its results then differ from the plain plan's within rounding.
  * Errors: as pa_plan / pa_plan_fixed, plus PA_ERR_INVALID_ARGUMENT for a NULL
  * window, window <= 0 or sink_tokens < 0, and PA_ERR_UNSUPPORTED for
  * num_common_prefix_blocks > 0 (a window leaves no prefix in common).

@@ -681,6 +681,12 @@ __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
+// (m, l) of a partial for the merge, which leaves out partials without weights: a
+// NaN among them takes it over.
+__device__ __forceinline__ float2 partial_weight(float m, float l) {
+    return l != l ? make_float2(3.0e38f, 1.f) : make_float2(m, l);
+}
+
 // Rows of a block whose keys some token of an item sees; the others (past the
 // context, or behind every token's window and not among the first tokens) may
 // hold anything.

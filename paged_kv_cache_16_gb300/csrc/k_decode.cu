@@ -463,8 +463,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                                                 ot[4 * h + 2][2 * jr + 1] * inv1, ot[4 * h + 3][2 * jr + 1] * inv1);
                         }
                     if (g == 0) {
-                        if (has0) p.ml_part[slotA * p.num_heads_q + headA] = make_float2(ma, lt[0]);
-                        if (has1) p.ml_part[slotB * p.num_heads_q + headB] = make_float2(mb, lt[1]);
+                        if (has0) p.ml_part[slotA * p.num_heads_q + headA] = partial_weight(ma, lt[0]);
+                        if (has1) p.ml_part[slotB * p.num_heads_q + headB] = partial_weight(mb, lt[1]);
                     }
                 }
                 continue;
@@ -688,8 +688,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     }
                 }
                 if (t4 == 0) {
-                    if (has0) p.ml_part[slot0 * p.num_heads_q + head0] = make_float2(m0, l0);
-                    if (has1) p.ml_part[slot1 * p.num_heads_q + head1] = make_float2(m1, l1);
+                    if (has0) p.ml_part[slot0 * p.num_heads_q + head0] = partial_weight(m0, l0);
+                    if (has1) p.ml_part[slot1 * p.num_heads_q + head1] = partial_weight(m1, l1);
                 }
             }
         }
@@ -876,8 +876,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     if (has1) *reinterpret_cast<float2 *>(op1 + d) = make_float2(o[j][2] * inv1, o[j][3] * inv1);
                 }
                 if (t4 == 0) {
-                    if (has0) p.ml_part[slot0 * p.num_heads_q + head0] = make_float2(m0, l0);
-                    if (has1) p.ml_part[slot1 * p.num_heads_q + head1] = make_float2(m1, l1);
+                    if (has0) p.ml_part[slot0 * p.num_heads_q + head0] = partial_weight(m0, l0);
+                    if (has1) p.ml_part[slot1 * p.num_heads_q + head1] = partial_weight(m1, l1);
                 }
             }
         }

@@ -377,7 +377,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 slot = static_cast<int64_t>(p.part_offset[tok * p.n_groups + tile.kv_head / p.heads_per_group]) +
                        tile.part;
             store_output<D>(p, t_row + col_o(t), tok_valid, tile.part, tok, h, slot, inv, lane);
-            if (tok_valid && tile.part >= 0) p.ml_part[slot * p.num_heads_q + h] = make_float2(m, l);
+            if (tok_valid && tile.part >= 0) p.ml_part[slot * p.num_heads_q + h] = partial_weight(m, l);
             tc_fence_before();
         }
         if (!ok) raise_abort(&abort_flag, p.err, kErrTimeout);

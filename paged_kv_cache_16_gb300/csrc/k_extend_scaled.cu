@@ -169,21 +169,23 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // belong to other requests or to none: masked columns, and value
             // rows that the softmax warps zero
             const int32_t *copies = p.block_table + static_cast<int64_t>(tile.req) * p.max_blocks;
+            const int pg_begin = tile.key_begin / kBlockSize;
             const int pg_end = (tile.key_end - tile.key_begin + kBlockSize - 1) / kBlockSize;
             // windowed: first the copies of the head (rows of its padding are other
-            // blocks'), then those from page `head` on; dst0 counts from page 0
-            const int32_t head = WIN ? tile.head : 0, head_end = head_blocks(p.sinks, p.sinks);
-            const int32_t dst0 = copies[tile.key_begin / kBlockSize + head + (WIN ? tile.skip : 0)] - head;
-            const int32_t head0 = head > 0 ? copies[0] : 0;
-            if (dst0 + head < 0 || dst0 + pg_end > p.num_blocks ||
-                head0 < 0 || (head > 0 && head0 + head_end > p.num_blocks)) {   // (not from the planner)
+            // blocks'), then those from page `head` on; all counted from the tile's
+            // first page
+            const int head = WIN ? tile.head - pg_begin : 0, head_end = head_blocks(p.sinks, p.sinks) - pg_begin;
+            const int32_t dst0 = WIN ? copies[tile.head + tile.skip] - head : copies[pg_begin];
+            const int32_t head0 = head > 0 ? copies[0] + pg_begin : 0;
+            if (dst0 + max(head, 0) < 0 || dst0 + pg_end > p.num_blocks ||
+                head0 < 0 || (head > 0 && head0 + min(head_end, pg_end) > p.num_blocks)) {   // (not from the planner)
                 if (lane == 0) raise_abort(&abort_flag, p.err, kErrBlockRange);
                 break;
             }
             for (int j = 0; j < sh.n_tiles; ++j) {
                 const int pg0 = j * (kTileKeys / kBlockSize);
                 const bool in_head = pg0 < head;
-                const int pages = min(kTileKeys / kBlockSize, (in_head ? head_end : pg_end) - pg0);
+                const int pages = min(kTileKeys / kBlockSize, (in_head ? min(head_end, pg_end) : pg_end) - pg0);
                 const int32_t at = (in_head ? head0 : dst0) + pg0;
 #pragma unroll
                 for (int tensor = 0; tensor < 2; ++tensor) {

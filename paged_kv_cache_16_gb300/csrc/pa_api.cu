@@ -439,8 +439,92 @@ void balance_tiles(const std::vector<std::pair<int64_t, int32_t>> &tiles, int ct
     }
 }
 
-pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape *shape,
-                     const pa_window_desc *win = nullptr) {
+// A windowed plan's query rows of one CTA tile, for every kv head.
+struct TileBlock {
+    ExtendTile tile;     // kv_head and part unset
+    int32_t steps;       // its 128-key steps
+    int32_t first_steps; // those of its first sub-tile
+    int32_t pieces = 1;
+};
+
+// Costs in steps (1.55 us): a tile's Q load and epilogue as the assignment to CTAs
+// counts them, one more for a piece's fp32 output, and the merge that joins pieces
+// (its launch, the partials written and read back, a row's partials one after
+// another).  Fitted: 512 tokens of 32 heads over 1024 / 2048 / 4096 keys, cut in
+// two 27.7 / 33.9 / 44.8 us, whole 19.8 / 30.5 / 53.9; one token of 32 heads over
+// 8192 keys in 17 / 33 pieces 15.1 / 18.4 us, whole 89.6.
+constexpr int kTileExtra = 2, kPieceExtra = 3;
+constexpr double kMergeLaunch = 1.5, kMergeBytesPerStep = 2.9e6, kMergePerPiece = 0.1;
+constexpr int kMaxPieces = 32;   // (the merge kernel's lanes)
+
+// Steps of the longest CTA when tiles of the given steps (descending) go to the
+// least loaded one each.
+int64_t longest_cta(const std::vector<int32_t> &steps, int ctas) {
+    std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> load;
+    for (int c = 0; c < ctas; ++c) load.push(0);
+    int64_t most = 0;
+    for (int32_t s : steps) {
+        const int64_t v = load.top() + s;
+        load.pop();
+        load.push(v);
+        most = std::max(most, v);
+    }
+    return most;
+}
+
+// Cut the keys of a windowed plan's tiles where that ends the step sooner: when the
+// tiles are fewer than the CTAs (a short chunk, a single token of more than 16 heads
+// per kv head), or leave the last round of CTAs mostly empty.  Partials are
+// joined by the merge kernel; a block's tiles of all kv heads are cut alike, as the
+// merge joins all heads of a token.  row_bytes: a token's partial.
+void cut_blocks(std::vector<TileBlock> &blocks, int hkv, int64_t row_bytes, int ctas) {
+    const int64_t n = static_cast<int64_t>(blocks.size()) * hkv;
+    if (n == 0 || n > 8LL * ctas) return;   // many rounds of CTAs hide an uneven last one
+    // longest first; the first `cut` of them may be cut: all, or those of the last round
+    std::vector<int32_t> order(blocks.size());
+    for (size_t i = 0; i < order.size(); ++i) order[i] = static_cast<int32_t>(i);
+    std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return blocks[a].steps > blocks[b].steps; });
+    const size_t cut = n < ctas ? blocks.size() : static_cast<size_t>((n % ctas + hkv - 1) / hkv);
+    const int32_t longest = blocks[order[0]].steps;
+    auto pieces_of = [&](size_t i, int32_t most) { return i < cut ? (blocks[order[i]].steps + most - 1) / most : 1; };
+    double best = longest + kTileExtra, best_merge = 0;
+    int32_t piece = 0;
+    for (int k = 2; k <= std::min(kMaxPieces, longest / 2) && cut > 0; ++k) {
+        const int32_t most = (longest + k - 1) / k;
+        int64_t tiles = 0, rows = 0;
+        for (size_t i = 0; i < cut; ++i) {
+            const int32_t j = pieces_of(i, most);
+            tiles += static_cast<int64_t>(j) * hkv;
+            if (j > 1) rows += static_cast<int64_t>(j) * blocks[order[i]].tile.n_tok;
+        }
+        const double merge = kMergeLaunch + rows * row_bytes / kMergeBytesPerStep + k * kMergePerPiece;
+        const double t = static_cast<double>((tiles + ctas - 1) / ctas) * (most + kPieceExtra) + merge;
+        if (t < best) {
+            best = t;
+            best_merge = merge;
+            piece = most;
+        }
+    }
+    if (piece == 0) return;
+    if (n >= ctas) {   // whole tiles beside the pieces: as they would be dealt out
+        std::vector<int32_t> before, after;
+        for (size_t i = 0; i < order.size(); ++i) {
+            const int32_t steps = blocks[order[i]].steps, k = pieces_of(i, piece);
+            for (int h = 0; h < hkv; ++h) {
+                before.push_back(steps + kTileExtra);
+                for (int32_t j = 0; j < k; ++j)
+                    after.push_back(steps * (j + 1) / k - steps * j / k + (k > 1 ? kPieceExtra : kTileExtra));
+            }
+        }
+        std::sort(after.begin(), after.end(), std::greater<int32_t>());
+        if (longest_cta(after, ctas) + best_merge >= longest_cta(before, ctas)) return;
+    }
+    for (size_t i = 0; i < cut; ++i) blocks[order[i]].pieces = pieces_of(i, piece);
+}
+
+// cut: windowed plans may cut the keys of tiles (cut_blocks)
+pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape *shape, const pa_window_desc *win,
+                     bool cut) {
     P->fixed = shape != nullptr;
     P->window = win ? win->window : 0;
     P->sinks = win ? win->sink_tokens : 0;
@@ -540,9 +624,10 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
         for (int32_t r : extend_rows) n += static_cast<size_t>(P->Hkv) * ((qsl[r + 1] - qsl[r] + tpt - 1) / tpt);
         P->tiles.reserve(n);
     }
+    std::vector<TileBlock> blocks;   // windowed
     for (int32_t r : extend_rows) {
         const int32_t q_len = qsl[r + 1] - qsl[r];
-        for (int h = 0; h < P->Hkv; ++h)
+        for (int h = 0; h < (win ? 1 : P->Hkv); ++h)
             for (int32_t m0 = 0; m0 < q_len; m0 += tpt) {
                 ExtendTile t{};
                 t.t0 = qsl[r] + m0;
@@ -560,12 +645,40 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
                     t.skip = v.skip;
                     t.pos0 -= v.skip * kBlockSize;
                     t.key_end -= v.skip * kBlockSize;
+                    t.part = -1;
+                    t.causal = 1;
+                    const int32_t first_end = std::min(t.key_end, t.pos0 + std::min(t.n_tok, tpt / 2));
+                    blocks.push_back({t, (t.key_end + kTileKeys - 1) / kTileKeys, (first_end + kTileKeys - 1) / kTileKeys});
+                    continue;
                 }
                 t.kv_head = h;
                 t.part = cascade ? P->prefix_splits : -1;
                 t.causal = 1;
                 P->tiles.push_back(t);
             }
+    }
+    std::vector<int32_t> tile_pieces;   // windowed: of each token's tiles
+    if (win) {
+        // staged inputs: rows from the decode prefix on may not be merged
+        if (cut && !(P->fixed && shape->decode_prefix_tokens > 0))
+            cut_blocks(blocks, P->Hkv, static_cast<int64_t>(P->Hq) * P->D * sizeof(float), P->num_sms);
+        tile_pieces.assign(static_cast<size_t>(P->T), 0);
+        for (const TileBlock &b : blocks)
+            for (int h = 0; h < P->Hkv; ++h)
+                for (int32_t j = 0; j < b.pieces; ++j) {
+                    ExtendTile t = b.tile;
+                    t.kv_head = h;
+                    if (b.pieces > 1) {
+                        // (every sub-tile has keys in every piece: the last one begins
+                        // before the first sub-tile's end)
+                        auto cut_at = [&](int32_t k) { return std::min(b.steps * k / b.pieces, b.first_steps - 1) * kTileKeys; };
+                        t.part = j;
+                        t.key_begin = cut_at(j);
+                        if (j + 1 < b.pieces) t.key_end = cut_at(j + 1);
+                        for (int32_t i = 0; i < t.n_tok; ++i) tile_pieces[static_cast<size_t>(t.t0 + i)] = b.pieces;
+                    }
+                    P->tiles.push_back(t);
+                }
     }
     // longest key ranges first: the last wave is made of short tiles (a
     // stable order: keys (INT32_MAX - range, index) sorted, then one move)
@@ -594,7 +707,7 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
                 first.push_back(0);
             }
             const int32_t end = t.key_end + t.skip * kBlockSize;
-            lo[row] = std::min(lo[row], t.key_begin / kBlockSize + t.head + t.skip);
+            lo[row] = std::min(lo[row], (win ? 0 : t.key_begin / kBlockSize) + t.head + t.skip);
             hi[row] = std::max(hi[row], (end + kBlockSize - 1) / kBlockSize);
             first[row] = std::max(first[row], head_blocks(end, P->sinks));
         }
@@ -791,6 +904,10 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
             for (int32_t t = units[u].t0; t < units[u].t0 + units[u].n_tok; ++t)
                 count[static_cast<size_t>(t) * P->n_groups + grp] = cascade ? P->prefix_splits + k : (k > 1 ? k : 0);
         }
+    if (win)
+        for (size_t t = 0; t < tile_pieces.size(); ++t)
+            for (int grp = 0; grp < P->n_groups && tile_pieces[t] > 0; ++grp)
+                count[t * P->n_groups + grp] = tile_pieces[t];
     if (cascade)
         for (int32_t r : extend_rows)
             for (int32_t t = qsl[r]; t < qsl[r + 1]; ++t)
@@ -971,16 +1088,19 @@ pa_status make_plan(const pa_batch_desc *desc, const pa_fixed_shape *shape, cons
     if (win && desc->num_common_prefix_blocks > 0) return PA_ERR_UNSUPPORTED;
     if (shape && desc->kv_cache_dtype != PA_KV_BF16 && shape->max_extend_tiles > 0 && shape->max_dequant_blocks == 0)
         return PA_ERR_INVALID_ARGUMENT;   // tiles over 8-bit caches read 16-bit copies: they need room
-    pa_plan_s *P = new (std::nothrow) pa_plan_s();
-    if (!P) return PA_ERR_INVALID_ARGUMENT;
-    try {
-        st = build_plan(P, desc, shape, win);
-    } catch (const std::bad_alloc &) {   // (nothing throws across the ABI)
-        st = PA_ERR_INVALID_ARGUMENT;
-    }
-    if (st != PA_OK) {
+    pa_plan_s *P = nullptr;
+    // a fixed shape without room for the pieces of cut tiles takes them whole
+    for (const bool cut : {true, false}) {
+        P = new (std::nothrow) pa_plan_s();
+        if (!P) return PA_ERR_INVALID_ARGUMENT;
+        try {
+            st = build_plan(P, desc, shape, win, cut);
+        } catch (const std::bad_alloc &) {   // (nothing throws across the ABI)
+            st = PA_ERR_INVALID_ARGUMENT;
+        }
+        if (st == PA_OK) break;
         delete P;
-        return st;
+        if (!cut || !win || st != PA_ERR_CAPACITY) return st;
     }
     *out = P;
     *workspace_bytes = P->ws_bytes;

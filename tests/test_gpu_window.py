@@ -60,6 +60,45 @@ def test_tile_rows(code, window, sinks, layout):
                            window=window, sinks=sinks, seed=d + window))
 
 
+@pytest.mark.parametrize("code", wc.KINDS)
+@pytest.mark.parametrize("q_lens,seq,window,sinks", [([9], [1500], 1400, 0), ([40], [2300], 2000, 20), ([300], [1900], 1024, 700),
+                                                     ([20, 1, 130], [1200, 700, 1700], 1100, 140), ([256], [900], 2000, 0)])
+@pytest.mark.parametrize("layout", [(8, 2, 128), (2, 2, 64), (32, 1, 128), (6, 2, 64)])
+def test_tiles_cut_along_their_keys(code, q_lens, seq, window, sinks, layout):
+    """Few tiles over long windows: pieces on idle SMs, some without a key for some
+    rows, joined by the merge; and whole in a shape without room for the pieces."""
+    hq, hkv, d = heads(code, [layout])[0]
+    c = wc.WindowCase(hq=hq, hkv=hkv, d=d, q_lens=q_lens, seq_lens=seq, code=code, window=window, sinks=sinks, seed=hq)
+    g = wc.check(c)
+    G = hq // hkv
+    whole = hkv * sum(-(-q // (2 * (128 // G))) for q in q_lens if q > (0 if G > 16 else max(8, 16 // G)))
+    assert g.plan.info()["num_extend_tiles"] > whole or whole == 0 or q_lens == [256]
+    blocks = 400 if code != "bf16" else 0
+    for tiles in (300, whole):                  # room for the pieces, or for whole tiles only
+        shape = dict(max_tokens=500, max_reqs=4, max_extend_tiles=tiles, max_dequant_blocks=blocks,
+                     max_partial_slots=20000)
+        f = wc.check(c, shape=shape)
+        assert tiles != 300 or torch.equal(f.out[:c.T], g.out)
+
+
+@pytest.mark.parametrize("code", wc.KINDS)
+def test_nan_in_a_piece_reaches_its_rows(code):
+    """A NaN key (int8: a NaN scale) in one piece makes the rows that see it NaN, and no
+    other row's key: split-KV items and pieces of tiles alike."""
+    for q_len, hq in ((1, 8), (40, 8), (1, 64)):
+        c = wc.WindowCase(hq=hq, hkv=2, d=128, q_lens=[q_len, q_len], seq_lens=[3000, 2900], code=code, window=2500, sinks=0, seed=3)
+        b = c.table[0, 2000 // 16]
+        if c.scaled:
+            c.ks[b] = float("nan")
+        else:
+            c.kc[b, 0] = float("nan") if code == "bf16" else 0x7F
+        g = wc.OnGpu(c)
+        out = g.run()
+        assert torch.isnan(out[:q_len]).all()
+        ref, tol = c.reference()
+        oc.assert_within(out[q_len:2 * q_len], ref[q_len:], tol[q_len:])
+
+
 @pytest.mark.parametrize("seed", range(40))
 def test_drawn_steps(seed):
     """Steps of every kind of row, windows and first tokens of any size."""

@@ -114,6 +114,27 @@ def test_fixed_shapes_with_a_window(code):
     assert binding.pa_plan_window_status(shape=dict(shape, max_tokens=0), **desc([1], [3], 64, 4, code)) == INVALID
 
 
+@pytest.mark.parametrize("code", range(4))
+def test_tiles_that_leave_sms_idle_are_cut(code):
+    """Few tiles: cut into pieces for the SMs, joined by merge rows; a shape without
+    room for the pieces keeps them whole, and so does one with a decode prefix."""
+    kw = desc([40], [5000], 4000, 20, code, max_blocks_per_req=400)      # one tile of 33 steps per kv head
+    info = binding.pa_plan_window(**kw).info()
+    assert info["num_extend_tiles"] > 8 and info["num_merge_rows"] == 40 and info["num_extend_ctas"] == info["num_extend_tiles"]
+    n, d = info["num_extend_tiles"], 500 if code else 0
+    assert binding.pa_plan_window(**{**kw, "window": 200}).info()["num_extend_tiles"] == 2
+    assert binding.pa_plan_window(**{**kw, "num_sms": 1}).info()["num_extend_tiles"] == 2
+    shape = dict(max_tokens=100, max_reqs=4, max_extend_tiles=n, max_dequant_blocks=d, max_partial_slots=5000)
+    assert binding.pa_plan_window(shape=shape, **kw).info()["num_extend_tiles"] == n
+    for small in (dict(max_extend_tiles=n - 1), dict(max_partial_slots=10), dict(decode_prefix_tokens=1)):
+        whole = binding.pa_plan_window(shape={**shape, **small}, **kw).info()
+        assert whole["num_extend_tiles"] == 2 and whole["num_merge_rows"] == 0
+    # a last round of a few tiles: 8 kv heads x 20 blocks of 64 tokens on 152 SMs
+    wide = dict(hq=32, hkv=8, max_blocks_per_req=700)
+    assert binding.pa_plan_window(**desc([1280], [9000], 8000, 0, code, **wide)).info()["num_extend_tiles"] > 160
+    assert binding.pa_plan_window(**desc([1216], [9000], 8000, 0, code, **wide)).info()["num_extend_tiles"] == 152
+
+
 def test_windowed_plans_refuse_the_wrong_calls(lib):
     """The attention calls go by the cache type, windows or not."""
     plain = binding.pa_plan_window(**desc([1], [40], code=0))

@@ -139,6 +139,8 @@ class OnGpu:
         dev = torch.device("cuda")
         self.case = case
         self.q, self.kc, self.vc, self.ks, self.vs = (t.to(dev) for t in (case.q, case.kc, case.vc, case.ks, case.vs))
+        if shape is not None:            # q and out hold a fixed shape's rows
+            self.q = torch.cat([self.q, self.q.new_zeros(shape["max_tokens"] - self.q.shape[0], *self.q.shape[1:])])
         self.table = torch.from_numpy(case.table).to(dev)
         self.out = torch.full_like(self.q, 7.0)
         self.plan = binding.pa_plan_window(shape=shape, **case.desc(**over))
