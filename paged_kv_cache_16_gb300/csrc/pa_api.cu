@@ -210,6 +210,39 @@ pa_status validate(const pa_batch_desc *d, const pa_window_desc *win = nullptr) 
     return PA_OK;
 }
 
+// Step-time model used to split the SMs between the tensor-core tiles and
+// the split-KV decode stream when a step has both (times in microseconds,
+// constants measured on GB300 at full clock).  The tiles are bound by the
+// tensor pipe of the SMs they run on, the decode stream by HBM once it has
+// enough SMs (each SM streams about 90 GB/s of bf16 blocks, 52 GB/s of E4M3
+// codes), so running the two side by side on disjoint SMs costs about
+// the longer of the two instead of their sum.
+// Side by side the two slow each other down a little (the tiles' K/V
+// re-reads and the decode stream share L2 and HBM): the side constants below
+// were measured that way.  With E4M3 caches the tile stream first makes the
+// bf16 copies of the tiles' blocks (three bytes moved per code).
+constexpr double kTileStepUs = 1.85;          // one 128-key step of a 256-row tile on one SM
+constexpr double kTileStepSideUs = 2.15;      // the same beside the bf16 decode stream
+constexpr double kTileStepSideFp8Us = 1.80;   // the same beside the E4M3 decode stream
+constexpr double kDequantUsPerBlock = 0.05;   // bf16 copy of one E4M3 block (K and V, all kv heads)
+constexpr double kHbmBytesPerUs = 7.0e6;      // decode stream at the HBM limit
+constexpr double kHbmSideBytesPerUs = 6.7e6;  // the same beside the tiles
+constexpr double kSmBf16BytesPerUs = 9.0e4;   // decode stream of one SM, bf16 caches
+constexpr double kSmFp8BytesPerUs = 5.2e4;    // decode stream of one SM, E4M3 caches
+constexpr double kSmFp8AloneBytesPerUs = 4.9e4;  // windowed rows, whole runs: E4M3 caches, up to 8 query rows
+constexpr double kSmScaledBytesPerUs = 4.5e4;  // the same, block-scaled caches
+constexpr double kSmRows16BytesPerUs = 3.6e4;  // the same, 8-bit caches and more than 8 rows
+constexpr double kMergeUs = 3.0;               // launch of the merge
+constexpr double kMergeBytesPerUs = 1.9e6;     // its partials, written and read back
+constexpr int64_t kMaxPackedSteps = 1 << 14;   // largest load of a CTA that is evened out (bounds the planning)
+constexpr double kForkUs = 5.0;               // cost of the second stream (fork, join, plain launches)
+constexpr double kHostLinkBytesPerUs = 2.0e5;  // page-locked host <-> device copy (staged inputs)
+// Share of the tiles' output copy-back counted on their path: the copy
+// overlaps the decode stream's tail, so only part of it lengthens the step
+// (mixed step from host memory to host memory: 1.018 / 0.997 / 1.059 ms
+// for 0 / 0.25 / 0.5, 1.100 ms for all of it).
+constexpr double kOutLeadWeight = 0.25;
+
 // A unit of the split-KV decode kernel: n_tok <= 16 / G consecutive query
 // tokens of one request whose G heads fill the 16 rows of one MMA tile; the
 // unit reads keys [0, key_end), key_end = one past its last token's position.
@@ -273,6 +306,67 @@ void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector
     int64_t ncta = std::min<int64_t>(cap, (total + min_pages - 1) / min_pages);
     ncta = std::max<int64_t>(ncta, 1);
     if (fixed_ncta > 0) ncta = std::min(ncta, fixed_ncta);
+    if (P->window > 0) {
+        // Windows make runs of one length: where there are enough of them, whole runs
+        // on the CTAs stream as fast as an equal cut and need no merge (window
+        // 1024, bf16: 90 requests 60.2 us instead of 62.7, 128 79.6 instead of 87.8, 128
+        // of 128 keys 15.0 instead of 20.0; but 64 of 1024 52.6 instead of 46.0).
+        std::vector<int32_t> order(runs.size());
+        for (size_t i = 0; i < order.size(); ++i) order[i] = static_cast<int32_t>(i);
+        std::stable_sort(order.begin(), order.end(),
+                         [&](int32_t a, int32_t b) { return runs[a].pe - runs[a].pb > runs[b].pe - runs[b].pb; });
+        const int64_t grid = std::min<int64_t>(cap, static_cast<int64_t>(runs.size()));
+        std::vector<std::vector<int32_t>> of(static_cast<size_t>(grid));
+        std::priority_queue<std::pair<int64_t, int64_t>, std::vector<std::pair<int64_t, int64_t>>,
+                            std::greater<std::pair<int64_t, int64_t>>> load;
+        for (int64_t c = 0; c < grid; ++c) load.push({0, c});
+        int64_t rows = 0;
+        for (int32_t i : order) {
+            const std::pair<int64_t, int64_t> least = load.top();
+            load.pop();
+            of[least.second].push_back(i);
+            load.push({least.first + runs[i].pe - runs[i].pb, least.second});
+            rows = std::max<int64_t>(rows, units[runs[i].u].n_tok);
+        }
+        const double bytes = 2.0 * kBlockSize * P->HG * P->D * (P->kv8 ? 1 : 2);   // of a block
+        const double rate = !P->kv8                            ? kSmBf16BytesPerUs
+                            : rows * P->G > kMmaRows / 2       ? kSmRows16BytesPerUs
+                            : P->scaled                        ? kSmScaledBytesPerUs
+                                                               : kSmFp8AloneBytesPerUs;
+        // whole runs: the CTAs share HBM until they end, shortest first
+        const double cta_rate = rate / cps;   // (its share of an SM's consumer warps)
+        double whole = 0;
+        int64_t done = 0, active = grid;
+        for (; !load.empty(); load.pop(), --active) {
+            whole += (load.top().first - done) * bytes / std::min(cta_rate, kHbmBytesPerUs / active);
+            done = load.top().first;
+        }
+        const double parts = static_cast<double>(std::min<int64_t>(runs.size(), ncta) + ncta);
+        const double cut = total * bytes / std::min(kHbmBytesPerUs, ncta * cta_rate) + kMergeUs +
+                           parts * rows * P->HG * P->G * P->D * sizeof(float) / kMergeBytesPerUs;
+        if (whole < cut) {
+            P->items.reserve(runs.size());
+            for (const std::vector<int32_t> &mine : of) {
+                for (int32_t i : mine) {
+                    DecodeItem it{};
+                    it.token = units[runs[i].u].t0;
+                    it.req = units[runs[i].u].r;
+                    it.page_begin = runs[i].pb;
+                    it.page_end = runs[i].pe;
+                    it.key_end = units[runs[i].u].key_end;
+                    it.head_group = runs[i].grp;
+                    it.part = pieces[static_cast<size_t>(runs[i].u) * P->n_groups + runs[i].grp]++;
+                    it.n_tok = units[runs[i].u].n_tok;
+                    P->items.push_back(it);
+                    item_unit.push_back(runs[i].u);
+                }
+                P->cta_begin.push_back(static_cast<int32_t>(P->items.size()));
+            }
+            while (static_cast<int64_t>(P->cta_begin.size()) < fixed_ncta + 1)
+                P->cta_begin.push_back(static_cast<int32_t>(P->items.size()));
+            return;
+        }
+    }
     // The cut is equal in cost, not in pages: an item costs its pages plus a
     // fixed start-up and finish (q loads, the fused row store, the epilogue),
     // so a CTA that holds the end of one run and the start of the next gets
@@ -320,34 +414,6 @@ void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector
     while (static_cast<int64_t>(P->cta_begin.size()) < fixed_ncta + 1)
         P->cta_begin.push_back(static_cast<int32_t>(P->items.size()));
 }
-
-// Step-time model used to split the SMs between the tensor-core tiles and
-// the split-KV decode stream when a step has both (times in microseconds,
-// constants measured on GB300 at full clock).  The tiles are bound by the
-// tensor pipe of the SMs they run on, the decode stream by HBM once it has
-// enough SMs (each SM streams about 90 GB/s of bf16 blocks, 52 GB/s of E4M3
-// codes), so running the two side by side on disjoint SMs costs about
-// the longer of the two instead of their sum.
-// Side by side the two slow each other down a little (the tiles' K/V
-// re-reads and the decode stream share L2 and HBM): the side constants below
-// were measured that way.  With E4M3 caches the tile stream first makes the
-// bf16 copies of the tiles' blocks (three bytes moved per code).
-constexpr double kTileStepUs = 1.85;          // one 128-key step of a 256-row tile on one SM
-constexpr double kTileStepSideUs = 2.15;      // the same beside the bf16 decode stream
-constexpr double kTileStepSideFp8Us = 1.80;   // the same beside the E4M3 decode stream
-constexpr double kDequantUsPerBlock = 0.05;   // bf16 copy of one E4M3 block (K and V, all kv heads)
-constexpr double kHbmBytesPerUs = 7.0e6;      // decode stream at the HBM limit
-constexpr double kHbmSideBytesPerUs = 6.7e6;  // the same beside the tiles
-constexpr double kSmBf16BytesPerUs = 9.0e4;   // decode stream of one SM, bf16 caches
-constexpr double kSmFp8BytesPerUs = 5.2e4;    // decode stream of one SM, E4M3 caches
-constexpr int64_t kMaxPackedSteps = 1 << 14;   // largest load of a CTA that is evened out (bounds the planning)
-constexpr double kForkUs = 5.0;               // cost of the second stream (fork, join, plain launches)
-constexpr double kHostLinkBytesPerUs = 2.0e5;  // page-locked host <-> device copy (staged inputs)
-// Share of the tiles' output copy-back counted on their path: the copy
-// overlaps the decode stream's tail, so only part of it lengthens the step
-// (mixed step from host memory to host memory: 1.018 / 0.997 / 1.059 ms
-// for 0 / 0.25 / 0.5, 1.100 ms for all of it).
-constexpr double kOutLeadWeight = 0.25;
 
 struct StepModel {
     double tile_units = 0, tile_max = 0;      // sum and largest tile cost (128-key steps + 1)

@@ -115,7 +115,8 @@ def test_drawn_steps(seed):
 
 @pytest.mark.parametrize("code", wc.KINDS)
 @pytest.mark.parametrize("window,sinks", [(2**31 - 1, 0), (2**31 - 1, 2**31 - 1), (1, 2**31 - 1), (5000, 3)])
-def test_a_window_without_effect_changes_no_bit(code, window, sinks):
+def test_a_window_without_effect(code, window, sinks):
+    """The plain rows' results; bit for bit where the work is cut alike."""
     c = wc.WindowCase(hq=8, hkv=2, d=128, q_lens=[1, 4, 90, 1], seq_lens=[300, 70, 333, 17], code=code, window=window,
                       sinks=sinks, seed=1)
     g = wc.check(c)
@@ -123,7 +124,10 @@ def test_a_window_without_effect_changes_no_bit(code, window, sinks):
     kw = c.desc()
     del kw["window"], kw["sink_tokens"]
     plain.plan = binding.pa_plan(**kw)
-    assert torch.equal(plain.run(), g.out)
+    ref, tol = c.reference()
+    oc.assert_within(plain.run(), ref, tol)
+    if plain.plan.info() == g.plan.info():
+        assert torch.equal(plain.out, g.out)
 
 
 @pytest.mark.parametrize("code", wc.KINDS)
