@@ -533,14 +533,15 @@ def pa_write_kv_fp8(key, value, slot_mapping, key_cache, value_cache, k_scale: f
 def _check_window(plan, q, key_cache, value_cache, block_table, out, *more):
     """Windowed plans: the kernels go by the plan, so tensors of another step, type or
     device would be read as what they are not, or past their ends."""
-    if plan.window is None:
-        return
     if _cuda is None:
         _use_torch()
+    # (element counts: a shape object costs as much as three other questions, and
+    # the smallest calls are bound by this thread)
     kind, rows, nb, hkv, dim, entries, width = plan._step
     dtype = key_cache.dtype
-    if _PLAIN_CACHES.get(dtype) != kind or value_cache.dtype is not dtype or key_cache.shape[1:] != (16, hkv, dim) or \
-            key_cache.shape[0] < nb or value_cache.shape != key_cache.shape or not key_cache.is_contiguous() or \
+    blocks, slots, heads, d = key_cache.shape
+    if _PLAIN_CACHES.get(dtype) != kind or value_cache.dtype is not dtype or slots != 16 or heads != hkv or d != dim or \
+            blocks < nb or value_cache.numel() != key_cache.numel() or not key_cache.is_contiguous() or \
             not value_cache.is_contiguous():
         raise ValueError(f"caches: the plan's type, contiguous [{nb}, 16, {hkv}, {dim}] wanted")
     if q.dtype is not _BF16 or out.dtype is not _BF16 or q.numel() < rows or out.numel() < rows or \
@@ -549,14 +550,11 @@ def _check_window(plan, q, key_cache, value_cache, block_table, out, *more):
     if block_table.dtype is not _I32 or not block_table.is_contiguous() or block_table.numel() < entries or \
             block_table.shape[-1] != width:
         raise ValueError(f"block_table: contiguous int32, the plan's requests and its {width} blocks each wanted")
-    _here("q, caches, block table, out, workspace", q, key_cache, value_cache, block_table, out,
-          *(t for t in more if t is not None))
+    _here("q, caches, block table, out, workspace", q, key_cache, value_cache, block_table, out, *more)
 
 
 def _check_new_rows(plan, key, value, slot_mapping):
     """The new rows of a fused call with a windowed plan."""
-    if plan.window is None:
-        return
     import torch
     _, rows, _, hkv, dim, _, _ = plan._step
     tokens = rows // (plan.heads_q * dim)
@@ -567,10 +565,13 @@ def _check_new_rows(plan, key, value, slot_mapping):
     if slot_mapping is not None and (slot_mapping.dtype is not torch.int64 or slot_mapping.numel() < tokens or
                                      not slot_mapping.is_contiguous()):
         raise ValueError("slot_mapping: contiguous int64, one per row of the plan wanted")
+    if slot_mapping is not None:
+        _here("slot_mapping", slot_mapping)
 
 
 def pa_attention(plan: Plan, q, key_cache, value_cache, block_table, out, workspace, stream=None):
-    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace)
+    if plan.window is not None:
+        _check_window(plan, q, key_cache, value_cache, block_table, out, workspace)
     nbytes = workspace.numel() * workspace.element_size()
     _check(load().pa_attention(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(block_table),
                                _ptr(out), _ptr(workspace), nbytes, _stream(stream)), "pa_attention")
@@ -607,7 +608,14 @@ def pa_upload_metadata_from(host_src, nbytes: int, workspace, stream=None):
 
 def pa_attention_launch(plan: Plan, q, key_cache, value_cache, block_table, out, workspace, stream=None):
     """The attention kernels alone (capturable in a CUDA graph; see pa.h)."""
-    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace)
+    if plan.window is not None:
+        _check_window(plan, q, key_cache, value_cache, block_table, out, workspace)
+        st = load().pa_attention_launch(plan.handle, q.data_ptr(), key_cache.data_ptr(), value_cache.data_ptr(),
+                                        block_table.data_ptr(), out.data_ptr(), workspace.data_ptr(), workspace.nbytes,
+                                        _stream(stream))
+        if st:
+            _check(st, "pa_attention_launch")
+        return
     nbytes = workspace.numel() * workspace.element_size()
     _check(load().pa_attention_launch(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache), _ptr(block_table),
                                       _ptr(out), _ptr(workspace), nbytes, _stream(stream)), "pa_attention_launch")
@@ -616,8 +624,9 @@ def pa_attention_launch(plan: Plan, q, key_cache, value_cache, block_table, out,
 def pa_attention_with_kv_update(plan: Plan, q, key, value, key_cache, value_cache, block_table, out, workspace,
                                 slot_mapping=None, stream=None):
     """Cache write + attention in one call (see pa.h)."""
-    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace, key, value, slot_mapping)
-    _check_new_rows(plan, key, value, slot_mapping)
+    if plan.window is not None:
+        _check_window(plan, q, key_cache, value_cache, block_table, out, workspace, key, value)
+        _check_new_rows(plan, key, value, slot_mapping)
     nbytes = workspace.numel() * workspace.element_size()
     _check(load().pa_attention_with_kv_update(plan.handle, _ptr(q), _ptr(key), _ptr(value), _ptr(key_cache),
                                               _ptr(value_cache), _ptr(block_table), _ptr(slot_mapping), _ptr(out),
@@ -627,8 +636,9 @@ def pa_attention_with_kv_update(plan: Plan, q, key, value, key_cache, value_cach
 
 def pa_attention_with_kv_update_launch(plan: Plan, q, key, value, key_cache, value_cache, block_table, out,
                                        workspace, slot_mapping=None, stream=None):
-    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace, key, value, slot_mapping)
-    _check_new_rows(plan, key, value, slot_mapping)
+    if plan.window is not None:
+        _check_window(plan, q, key_cache, value_cache, block_table, out, workspace, key, value)
+        _check_new_rows(plan, key, value, slot_mapping)
     nbytes = workspace.numel() * workspace.element_size()
     _check(load().pa_attention_with_kv_update_launch(plan.handle, _ptr(q), _ptr(key), _ptr(value), _ptr(key_cache),
                                                      _ptr(value_cache), _ptr(block_table), _ptr(slot_mapping),
@@ -643,8 +653,9 @@ def pa_attention_with_kv_update_launch_staged(plan: Plan, q, key, value, key_cac
     prefix on may still be written until late_rows (a torch.cuda.Event,
     already recorded) fires.  late_out_ready (a torch.cuda.Event) is recorded
     once out's rows from the prefix on are final."""
-    _check_window(plan, q, key_cache, value_cache, block_table, out, workspace, key, value, slot_mapping)
-    _check_new_rows(plan, key, value, slot_mapping)
+    if plan.window is not None:
+        _check_window(plan, q, key_cache, value_cache, block_table, out, workspace, key, value)
+        _check_new_rows(plan, key, value, slot_mapping)
     nbytes = workspace.numel() * workspace.element_size()
     if late_out_ready is not None and not late_out_ready.cuda_event:
         late_out_ready.record()   # torch creates the CUDA event at its first record
@@ -668,8 +679,9 @@ def pa_attention_no_alloc(plan: Plan, q, key_cache, value_cache, block_table, ou
                           stream=None):
     """pa_attention with the library's fixed scratch array instead of a workspace
     (for callers that cannot allocate device memory; see pa.h)."""
-    _check_window(plan, q, key_cache, value_cache, block_table, out,
-                  None if isinstance(device_error_word, int) else device_error_word)
+    if plan.window is not None:
+        more = () if device_error_word is None or isinstance(device_error_word, int) else (device_error_word,)
+        _check_window(plan, q, key_cache, value_cache, block_table, out, *more)
     _check(load().pa_attention_no_alloc(plan.handle, _ptr(q), _ptr(key_cache), _ptr(value_cache),
                                         _ptr(block_table), _ptr(out), _ptr(device_error_word), _stream(stream)),
            "pa_attention_no_alloc")
@@ -747,10 +759,13 @@ def pa_rope_create_axes(*, num_axes, axis_of_pair, rotary_dim, frequencies=PA_RO
 
 def _axis_stride(rope: Rope, positions, num_tokens: int) -> int:
     """Elements between the axes of positions (int32 [axes, tokens], tokens dense)."""
-    if positions.dtype is not _I32 or positions.shape != (rope.num_axes, num_tokens) or \
-            (num_tokens > 1 and positions.stride(1) != 1):
-        raise ValueError(f"positions: int32 [{rope.num_axes}, {num_tokens}] with dense rows wanted")
-    return num_tokens if rope.num_axes == 1 else positions.stride(0)
+    n = rope.num_axes
+    if positions.dtype is not _I32 or positions.shape != (n, num_tokens):
+        raise ValueError(f"positions: int32 [{n}, {num_tokens}] wanted")
+    apart, dense = positions.stride()
+    if num_tokens > 1 and dense != 1:
+        raise ValueError("positions: dense rows wanted")
+    return num_tokens if n == 1 else apart
 
 
 def _here(what: str, *tensors):
