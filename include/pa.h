@@ -367,11 +367,13 @@ pa_status pa_plan_fixed(const pa_batch_desc *desc, const pa_fixed_shape *shape, 
  * 0 times it).
  * Fixed shapes: window and sink_tokens count as model fields, as the kernels'
  * arguments hold them.  max_dequant_blocks counts blocks that some query sees.
- * Tiles that leave SMs idle are cut along their keys where that ends the step sooner
- * (pa_plan_info.num_extend_tiles counts the pieces; joined by the merge); a fixed shape
- * cuts them like pa_plan_window without a shape does, if its max_extend_tiles and
- * max_partial_slots have room for all pieces, else (and with decode_prefix_tokens) not
- * at all: its results then differ from the plain plan's within rounding.
+ * Where tensor-core tiles would leave SMs idle, the plan makes more of them where that
+ * ends the step sooner: tiles of half the rows, and pieces of a tile's keys, joined by
+ * the merge (pa_plan_info.num_extend_tiles counts them all; the sums' order, and so the
+ * rounding, is that of the plan).  A fixed shape does as pa_plan_window without a
+ * shape does if its max_extend_tiles and max_partial_slots have room, else (and with
+ * decode_prefix_tokens) it makes none: its results then differ from the plain plan's
+ * within rounding.
  * Errors: as pa_plan / pa_plan_fixed, plus PA_ERR_INVALID_ARGUMENT for a NULL
  * window, window <= 0 or sink_tokens < 0, and PA_ERR_UNSUPPORTED for
  * num_common_prefix_blocks > 0 (a window leaves no prefix in common).

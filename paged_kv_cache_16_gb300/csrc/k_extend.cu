@@ -58,7 +58,7 @@ struct ExtCfg {
     static_assert(REGS_CTRL * 128 + REGS_SOFTMAX * 256 <= 168 * 384, "register split exceeds the launch");
     static constexpr int TILE_SMEM = 2 * QB + (NSK + NSV) * KVB;
     // one CTA per SM: it owns all 512 tensor-memory columns
-    static constexpr int SMEM = (TILE_SMEM + 2048 < 120 * 1024) ? 120 * 1024 : TILE_SMEM + 2048;
+    static constexpr int SMEM = (TILE_SMEM + 1024 < 120 * 1024) ? 120 * 1024 : TILE_SMEM + 1024;
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, false);
     static constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true);
@@ -68,7 +68,16 @@ struct ExtCfg {
 // WIN: with a sliding window and first tokens (tiles in WindowView's numbers: key
 // tiles of 128 keys run over the blocks with first tokens and on into those of the
 // tile's first window, whose lower masks reach over the first key tiles only).
-template <int D, bool WIN>
+// SPLIT (with a window): tiles of one sub-tile of rows whose keys both sub-tiles share
+// may be among them (a variant of its own: it costs the other tiles 3%).  Sharing
+// doubles the loads per step: K and V in boxes of one block and 64 columns (2 KB) come
+// at 46 GB/s per SM (the TMA unit's time per box), which that needs twice of.  So V
+// of such tiles comes by 16-byte asynchronous copies of the two idle warps (a step of
+// two key tiles 1.7 us instead of 2.8; in the other tiles they would cost 6%, by the
+// issue slots they take).  The planner splits all tiles of a step over bf16 caches or
+// none, so that one side brings every V tile of a CTA.  COPIES: over the consecutive
+// 16-bit copies of E4M3 blocks, a key tile is one box per 64 columns.
+template <int D, bool WIN, bool COPIES, bool SPLIT>
 __global__ void __launch_bounds__(384, 1)
 extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const ExtendParams p) {
@@ -77,6 +86,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     __shared__ int abort_flag;
     __shared__ uint32_t tmem_base_slot;
     __shared__ __align__(8) uint64_t bars[NUM_BARS];
+    __shared__ float2 second[SPLIT ? kTileRows : 1];   // split tiles: sub-tile 1's maximum and sum of each row
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto q_s = [&](int t) { return base + static_cast<uint32_t>(t) * C::QB; };
@@ -90,6 +100,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const int tile_begin = p.cta_tile_begin[blockIdx.x];
     const int tile_end = p.cta_tile_begin[blockIdx.x + 1];
     if (tile_begin >= tile_end) return;
+    const bool v_warps = SPLIT && !COPIES && p.tiles[p.cta_tiles[tile_begin]].split != 0;   // warps 2 and 3 bring V
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (uniform to the compiler)
     const int lane = threadIdx.x & 31;
     const int G = p.group;
@@ -104,7 +115,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             mbar_init(bar(B_KEMPTY + s), 1);
         }
         for (int s = 0; s < C::NSV; ++s) {
-            mbar_init(bar(B_VFULL + s), 1);
+            mbar_init(bar(B_VFULL + s), v_warps ? 2 : 1);
             mbar_init(bar(B_VEMPTY + s), 1);
         }
         for (int t = 0; t < 2; ++t) {
@@ -114,6 +125,8 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             mbar_init(bar(B_ODONE + t), 1);
         }
         mbar_init(bar(B_DRAIN), 1);
+        mbar_init(bar(B_SECOND), 4);
+        mbar_init(bar(B_JOINED), 4);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -139,7 +152,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         bool ok = true;
         for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
             const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-            const TileShape sh = tile_shape(tile, tpt);
+            const TileShape sh = tile_shape<SPLIT>(tile, tpt);
             // Q of this tile, once the previous tile's QK^T no longer read Q
             if (n_q_loads > 0 && !warp_wait(bar(B_QEMPTY), (n_q_loads - 1) & 1, &abort_flag)) {
                 if (lane == 0) raise_abort(&abort_flag, p.err, kErrTimeout);
@@ -152,11 +165,44 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             __syncwarp();
             if (lane < n_q * C::NH) {
                 const int t = lane / C::NH, half = lane % C::NH;
-                tma_load_3d(q_s(t) + half * C::HALF, &tm_q, half * 64, tile.kv_head * G, tile.t0 + t * tpt,
-                            bar(B_QFULL));
+                tma_load_3d(q_s(t) + half * C::HALF, &tm_q, half * 64, tile.kv_head * G,
+                            tile.t0 + (sh.split ? 0 : t * tpt), bar(B_QFULL));
             }
             ++n_q_loads;
             const int32_t *bt = p.block_table + static_cast<int64_t>(tile.req) * p.max_blocks;
+            if constexpr (COPIES) {
+                // the copies of the head (rows of its padding are other blocks'), then
+                // those from page `head` on, counted from the tile's first page
+                const int pg_begin = tile.key_begin / kBlockSize, head = tile.head - pg_begin;
+                const int pg_end = (tile.key_end - tile.key_begin + kBlockSize - 1) / kBlockSize;
+                const int32_t dst0 = bt[tile.head + tile.skip] - head, head0 = head > 0 ? bt[0] + pg_begin : 0;
+                if (dst0 + max(head, 0) < 0 || dst0 + pg_end > p.num_blocks || head0 < 0) {   // (not from the planner)
+                    if (lane == 0) raise_abort(&abort_flag, p.err, kErrBlockRange);
+                    break;
+                }
+                for (int j = 0; j < sh.n_tiles && ok; ++j) {
+                    const int pg0 = j * (kTileKeys / kBlockSize);
+                    const int32_t at = (pg0 < head ? head0 : dst0) + pg0;
+#pragma unroll
+                    for (int tensor = 0; tensor < 2; ++tensor) {
+                        const int ns = tensor ? C::NSV : C::NSK;
+                        const int s = issued[tensor] % ns, n = issued[tensor] / ns;
+                        const int full = tensor ? B_VFULL : B_KFULL;
+                        if (n > 0 && !warp_wait(bar((tensor ? B_VEMPTY : B_KEMPTY) + s), (n & 1) ^ 1, &abort_flag)) {
+                            if (lane == 0) raise_abort(&abort_flag, p.err, kErrTimeout);
+                            ok = false;
+                            break;
+                        }
+                        if (lane == 0) mbar_arrive_expect_tx(bar(full + s), C::KVB);
+                        __syncwarp();
+                        if (lane < C::NH)
+                            tma_load_3d((tensor ? v_s(s) : k_s(s)) + lane * C::HALF, tensor ? &tm_v : &tm_k, lane * 64,
+                                        tile.kv_head, at * kBlockSize, bar(full + s));
+                        ++issued[tensor];
+                    }
+                }
+                continue;
+            }
             // block ids of 32 pages (4 key tiles) per load: the producer's
             // dependent block-table read happens once per window, not per tile
             const int pg_end = (tile.key_end + kBlockSize - 1) / kBlockSize;
@@ -188,6 +234,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 const bool mine = lane < 8 * C::NH && ((vmask >> page) & 1u);
 #pragma unroll
                 for (int tensor = 0; tensor < 2; ++tensor) {
+                    if (tensor && v_warps) continue;
                     const int ns = tensor ? C::NSV : C::NSK;
                     const int s = issued[tensor] % ns, n = issued[tensor] / ns;
                     const int empty = tensor ? B_VEMPTY : B_KEMPTY;
@@ -221,7 +268,65 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer --
-        issue_mmas<D, C>(p, smem_u32(bars), q_s(0), k_s(0), v_s(0), tmem, tile_begin, tile_end, tpt, lane, &abort_flag);
+        issue_mmas<D, C, SPLIT>(p, smem_u32(bars), q_s(0), k_s(0), v_s(0), tmem, tile_begin, tile_end, tpt, lane, &abort_flag);
+      } else if (v_warps) {
+        // ------------------------------------------------------- V copies --
+        // Each warp brings 64 rows (4 blocks) of a V tile, swizzled as a box would
+        // be, and hands them over a tile later, so that its copies are under way
+        // while it waits for the next stage.
+        constexpr int CH = D / 8;                // 16-byte chunks of a row
+        const int64_t row_elems = static_cast<int64_t>(p.num_heads_kv) * D;
+        int issued = 0;
+        bool ok = true;
+        auto hand_over = [&](int i) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(B_VFULL + i % C::NSV));
+        };
+        for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
+            const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
+            const TileShape sh = tile_shape<SPLIT>(tile, tpt);
+            const WindowView view{tile.head, tile.skip};
+            const int32_t *bt = p.block_table + static_cast<int64_t>(tile.req) * p.max_blocks;
+            const int pg_end = (tile.key_end + kBlockSize - 1) / kBlockSize;
+            int32_t win = 0;                     // block ids of 32 pages
+            int win0 = -64;
+            for (int j = 0; j < sh.n_tiles; ++j) {
+                const int pg0 = (tile.key_begin + j * kTileKeys) / kBlockSize;
+                if (pg0 + 8 > win0 + 32) {
+                    win0 = pg0;
+                    win = pg0 + lane < pg_end ? bt[view.at(pg0 + lane)] : -1;
+                }
+                const int s = issued % C::NSV, n = issued / C::NSV;
+                if (n > 0 && !warp_wait(bar(B_VEMPTY + s), (n & 1) ^ 1, &abort_flag)) {
+                    if (lane == 0) raise_abort(&abort_flag, p.err, kErrTimeout);
+                    ok = false;
+                    break;
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int page = 4 * (warp - 2) + k;
+                    const int32_t blk = __shfl_sync(0xffffffffu, win, (pg0 - win0 + page) & 31);
+                    if (pg0 + page >= pg_end || blk < 0 || blk >= p.num_blocks) continue;   // (reported with K)
+                    const uint16_t *src = p.value_cache + blk * kBlockSize * row_elems + tile.kv_head * D;
+#pragma unroll
+                    for (int i = 0; i < kBlockSize * CH / 32; ++i) {
+                        const int row = (32 * i + lane) / CH, c = (32 * i + lane) % CH;
+                        cp_async16(v_s(s) + (c / 8) * C::HALF + (page * kBlockSize + row) * 128 + (((c % 8) ^ (row & 7)) << 4),
+                                   src + row * row_elems + c * 8);
+                    }
+                }
+                cp_async_commit();
+                if (issued > 0) {
+                    cp_async_wait<1>();
+                    hand_over(issued - 1);
+                }
+                ++issued;
+            }
+        }
+        // no copy may outlive the CTA
+        cp_async_wait_all();
+        if (issued > 0) hand_over(issued - 1);
       }
     } else {
         // ------------------------------------------- softmax + epilogue --
@@ -231,12 +336,13 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const int row = quarter * 32 + lane;
         const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         int scnt = 0, ocnt = 0;                  // S tiles and outputs consumed by this sub-tile
+        int n_split = 0;                         // split tiles so far
         int vbase = 0;                           // V tiles of the previous tiles of this CTA
         bool ok = true;
         for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
             const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-            const TileShape sh = tile_shape(tile, tpt);
-            const int i = t * tpt + row / G;         // token of this row within the tile
+            const TileShape sh = tile_shape<SPLIT>(tile, tpt);
+            const int i = (sh.split ? 0 : t * tpt) + row / G;   // token of this row within the tile
             const int gq = row % G;
             // rows past tpt * G (when G does not divide 128) are padding
             const bool tok_valid = row < tpt * G && i < tile.n_tok;
@@ -246,7 +352,8 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             // windows: this row's begins at low, the tile's first one at low_min
             const int low = pos_lim - p.window, low_min = tile.pos0 + 1 - p.window;
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < n_mine; ++j) {
+            for (int i_step = 0; i_step < n_mine; ++i_step) {
+                const int j = sh.step(i_step, t);   // key tile
                 if (!warp_wait(bar(B_SFULL + t), scnt & 1, &abort_flag)) { ok = false; break; }
                 ++scnt;
                 tc_fence_after();
@@ -259,17 +366,8 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 tmem_ld32(t_row + col_s(t) + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
                 tmem_ld32(t_row + col_s(t) + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
                 tmem_wait_ld();
-                if (lim < kTileKeys) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= lim) sr[c] = __float_as_uint(-INFINITY);
-                }
-                if (WIN && kt0 < low) {   // keys behind the row's window that are not first tokens
-                    const int from = p.sinks - kt0, to = low - kt0;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= from && c < to) sr[c] = __float_as_uint(-INFINITY);
-                }
+                // keys past the row's limit, or behind its window and not first tokens
+                if (lim < kTileKeys || (WIN && kt0 < low)) hide_columns<WIN>(sr, lim, p.sinks - kt0, low - kt0);
                 // row max: 3-input max, four chains
                 float mx0 = -INFINITY, mx1 = -INFINITY, mx2 = -INFINITY, mx3 = -INFINITY;
 #pragma unroll
@@ -311,8 +409,8 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                 };
                 // the first half of P, under which its PV can begin
                 weights(0);
-                if (j >= 1 && __any_sync(0xffffffffu, need)) {
-                    // O_t holds the tiles before j (their PV completed before S_t(j) did)
+                if (i_step >= 1 && __any_sync(0xffffffffu, need)) {
+                    // O_t holds the key tiles before (their PV completed before S_t(j) did)
 #pragma unroll 1
                     for (int c = 0; c < D; c += 32) {
                         uint32_t orr[32];
@@ -369,6 +467,25 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (!warp_wait(bar(B_ODONE + t), ocnt & 1, &abort_flag)) { ok = false; break; }
             ++ocnt;
             tc_fence_after();
+            // a split tile: sub-tile 1 hands over its maximum and sum, and goes on when
+            // sub-tile 0 has read its O
+            Joined joined;
+            if (sh.split) {
+                if (t == 1) {
+                    second[row] = make_float2(m, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_SECOND));
+                    if (!warp_wait(bar(B_JOINED), n_split & 1, &abort_flag)) { ok = false; break; }
+                    ++n_split;
+                    tc_fence_after();
+                    continue;
+                }
+                if (!warp_wait(bar(B_SECOND), n_split & 1, &abort_flag)) { ok = false; break; }
+                ++n_split;
+                tc_fence_after();
+                joined.join(m, l, second[row]);
+            }
             const float inv = l > 0.f ? p.out_scale / l : 0.f;
             const int tok = tile.t0 + i;
             const int h = tile.kv_head * G + gq;
@@ -376,7 +493,13 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             if (tile.part >= 0 && tok_valid)
                 slot = static_cast<int64_t>(p.part_offset[tok * p.n_groups + tile.kv_head / p.heads_per_group]) +
                        tile.part;
-            store_output<D>(p, t_row + col_o(t), tok_valid, tile.part, tok, h, slot, inv, lane);
+            store_output<D>(p, t_row + col_o(t), t_row + col_o(1), sh.split, tok_valid, tile.part, tok, h, slot,
+                            joined.a0 * inv, joined.a1 * inv, lane, [&] {
+                                if (!sh.split) return;
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(bar(B_JOINED));
+                            });
             if (tok_valid && tile.part >= 0) p.ml_part[slot * p.num_heads_q + h] = partial_weight(m, l);
             tc_fence_before();
         }
@@ -389,11 +512,11 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
 }
 
-template <int D, bool WIN>
+template <int D, bool WIN, bool COPIES, bool SPLIT>
 cudaError_t configure() {
     static bool configured = false;  // attribute is per function, set once per process
     if (!configured) {
-        cudaError_t e = cudaFuncSetAttribute(extend_kernel<D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(extend_kernel<D, WIN, COPIES, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              ExtCfg<D>::SMEM);
         if (e != cudaSuccess) return e;
         configured = true;
@@ -401,33 +524,39 @@ cudaError_t configure() {
     return cudaSuccess;
 }
 
-template <int D, bool WIN>
+template <int D, bool WIN, bool COPIES, bool SPLIT>
 cudaError_t launch_t(int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                      const ExtendParams &p, cudaStream_t stream, bool pdl) {
     using C = ExtCfg<D>;
-    cudaError_t e = configure<D, WIN>();
+    cudaError_t e = configure<D, WIN, COPIES, SPLIT>();
     if (e != cudaSuccess) return e;
-    return launch_ex(extend_kernel<D, WIN>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, pdl, tm_q, tm_k, tm_v, p);
+    return launch_ex(extend_kernel<D, WIN, COPIES, SPLIT>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, pdl, tm_q, tm_k, tm_v, p);
 }
 
 }  // namespace
 
-cudaError_t prepare_extend(int head_dim, bool window) {
-    if (head_dim == 128) return window ? configure<128, true>() : configure<128, false>();
-    if (head_dim == 64) return window ? configure<64, true>() : configure<64, false>();
+// f<WIN, COPIES, SPLIT> of a plan's variant (E4M3 caches, whose tiles read copies, have
+// head_dim 128)
+#define PA_EXTEND_CASE(window, copies, split, f, ...)                                        \
+    if (head_dim == 128 && !(window)) return f<128, false, false, false>(__VA_ARGS__);        \
+    if (head_dim == 128 && (copies))                                                          \
+        return (split) ? f<128, true, true, true>(__VA_ARGS__) : f<128, true, true, false>(__VA_ARGS__);   \
+    if (head_dim == 128)                                                                      \
+        return (split) ? f<128, true, false, true>(__VA_ARGS__) : f<128, true, false, false>(__VA_ARGS__); \
+    if (head_dim == 64 && !(window)) return f<64, false, false, false>(__VA_ARGS__);          \
+    if (head_dim == 64)                                                                       \
+        return (split) ? f<64, true, false, true>(__VA_ARGS__) : f<64, true, false, false>(__VA_ARGS__);   \
     return cudaErrorInvalidValue;
+
+cudaError_t prepare_extend(int head_dim, bool window, bool copies, bool split) {
+    PA_EXTEND_CASE(window, copies, split, configure)
 }
 
 cudaError_t launch_extend(int head_dim, int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const ExtendParams &p, cudaStream_t stream, bool pdl) {
     if (grid <= 0) return cudaSuccess;
-    if (head_dim == 128)
-        return p.window > 0 ? launch_t<128, true>(grid, tm_q, tm_k, tm_v, p, stream, pdl)
-                            : launch_t<128, false>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
-    if (head_dim == 64)
-        return p.window > 0 ? launch_t<64, true>(grid, tm_q, tm_k, tm_v, p, stream, pdl)
-                            : launch_t<64, false>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
-    return cudaErrorInvalidValue;
+    PA_EXTEND_CASE(p.window > 0, p.value_cache == nullptr, p.split != 0, launch_t, grid, tm_q, tm_k, tm_v, p, stream, pdl)
 }
+#undef PA_EXTEND_CASE
 
 }  // namespace pa

@@ -59,7 +59,7 @@ struct ScaledExtCfg {
     static constexpr int FACTORS = NSV * (kTileKeys / kBlockSize) * 16;   // a record per block of a V stage
     static constexpr int TILE_SMEM = 2 * QB + (NSK + NSV) * KVB + FACTORS;
     // one CTA per SM: it owns all 512 tensor-memory columns
-    static constexpr int SMEM = (TILE_SMEM + 2048 < 120 * 1024) ? 120 * 1024 : TILE_SMEM + 2048;
+    static constexpr int SMEM = (TILE_SMEM + 1024 < 120 * 1024) ? 120 * 1024 : TILE_SMEM + 1024;
     static constexpr uint32_t TMEM_COLS = 512;
     static constexpr uint32_t IDESC_QK = idesc_bf16(128, 128, false, false);
     static constexpr uint32_t IDESC_PV = idesc_bf16(128, D, false, true) & ~((1u << 7) | (1u << 10));   // f16 A and B
@@ -68,8 +68,9 @@ struct ScaledExtCfg {
 
 // WIN: with a sliding window and first tokens (tiles in WindowView's numbers, the
 // head padded to whole key tiles: the copies of a head's blocks are consecutive,
-// and so are those from the window on).
-template <int D, bool WIN>
+// and so are those from the window on).  SPLIT: tiles of one sub-tile of rows whose
+// keys both sub-tiles share may be among them.
+template <int D, bool WIN, bool SPLIT>
 __global__ void __launch_bounds__(384, 1)
 scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const ScaledExtendParams sp) {
@@ -79,6 +80,7 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     __shared__ int abort_flag;
     __shared__ uint32_t tmem_base_slot;
     __shared__ __align__(8) uint64_t bars[NUM_BARS];
+    __shared__ float2 second[SPLIT ? kTileRows : 1];   // split tiles: sub-tile 1's maximum and sum of each row
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto q_s = [&](int t) { return base + static_cast<uint32_t>(t) * C::QB; };
@@ -120,6 +122,8 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             mbar_init(bar(B_ODONE + t), 1);
         }
         mbar_init(bar(B_DRAIN), 1);
+        mbar_init(bar(B_SECOND), 4);
+        mbar_init(bar(B_JOINED), 4);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -145,7 +149,7 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         bool ok = true;
         for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
             const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-            const TileShape sh = tile_shape(tile, tpt);
+            const TileShape sh = tile_shape<SPLIT>(tile, tpt);
             // Q of this tile, once the previous tile's QK^T no longer read Q
             if (n_q_loads > 0 && !warp_wait(bar(B_QEMPTY), (n_q_loads - 1) & 1, &abort_flag)) {
                 if (lane == 0) raise_abort(&abort_flag, p.err, kErrTimeout);
@@ -158,8 +162,8 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             __syncwarp();
             if (lane < n_q * C::NH) {
                 const int t = lane / C::NH, half = lane % C::NH;
-                tma_load_3d(q_s(t) + half * C::HALF, &tm_q, half * 64, tile.kv_head * G, tile.t0 + t * tpt,
-                            bar(B_QFULL));
+                tma_load_3d(q_s(t) + half * C::HALF, &tm_q, half * 64, tile.kv_head * G,
+                            tile.t0 + (sh.split ? 0 : t * tpt), bar(B_QFULL));
             }
             ++n_q_loads;
             // the copies of a request's blocks are consecutive, so a key tile is
@@ -225,7 +229,7 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer --
-        issue_mmas<D, C>(p, smem_u32(bars), q_s(0), k_s(0), v_s(0), tmem, tile_begin, tile_end, tpt, lane, &abort_flag);
+        issue_mmas<D, C, SPLIT>(p, smem_u32(bars), q_s(0), k_s(0), v_s(0), tmem, tile_begin, tile_end, tpt, lane, &abort_flag);
       }
     } else {
         // ------------------------------------------- softmax + epilogue --
@@ -235,13 +239,14 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
         const int row = quarter * 32 + lane;
         const uint32_t t_row = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
         int scnt = 0, ocnt = 0;                  // S tiles and outputs consumed by this sub-tile
+        int n_split = 0;                         // split tiles so far
         int vbase = 0;                           // V tiles of the previous tiles of this CTA
         int v_seen = 0;                          // one past the last V tile waited for
         bool ok = true;
         for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
             const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-            const TileShape sh = tile_shape(tile, tpt);
-            const int i = t * tpt + row / G;         // token of this row within the tile
+            const TileShape sh = tile_shape<SPLIT>(tile, tpt);
+            const int i = (sh.split ? 0 : t * tpt) + row / G;   // token of this row within the tile
             const int gq = row % G;
             // rows past tpt * G (when G does not divide 128) are padding
             const bool tok_valid = row < tpt * G && i < tile.n_tok;
@@ -251,15 +256,17 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             // windows: this row's begins at low, the tile's first one at low_min
             const int low = pos_lim - p.window, low_min = tile.pos0 + 1 - p.window;
             float m = -INFINITY, l = 0.f;
-            for (int j = 0; j < n_mine; ++j) {
+            for (int i_step = 0; i_step < n_mine; ++i_step) {
+                const int j = sh.step(i_step, t);   // key tile
                 const int kt0 = tile.key_begin + j * kTileKeys;
                 // Behind tiles whose empty second sub-tile passed this warpgroup by,
                 // S comes first: the parity of a V barrier tells two neighbouring
                 // phases apart only, and this warpgroup has not seen the phase
-                // before the one asked for.  S completes behind every MMA of the
-                // tiles before, so that phase is over.  (S first in every tile:
+                // before the one asked for (nor has it of a split tile, whose key tiles it
+                // sees every second of).  S completes behind every MMA of the key tiles
+                // before, so that phase is over.  (S first in every tile:
                 // 214.0 us instead of 212.8 for the two chunks above.)
-                const bool s_first = vbase + j >= v_seen + C::NSV;
+                const bool s_first = sh.split || vbase + j >= v_seen + C::NSV;
                 if (s_first && !warp_wait(bar(B_SFULL + t), scnt & 1, &abort_flag)) { ok = false; break; }
                 v_seen = vbase + j + 1;
                 // the factors of the tile's blocks, which came with its V stage,
@@ -301,22 +308,13 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                 tmem_ld32(t_row + col_s(t) + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
                 tmem_ld32(t_row + col_s(t) + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
                 tmem_wait_ld();
-                if (lim < kTileKeys) {
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= lim) sr[c] = __float_as_uint(-INFINITY);
+                // keys past the row's limit, or behind its window and not first tokens
+                if (lim < kTileKeys || (WIN && kt0 < low)) {
+                    const int from = p.sinks - kt0, to = low - kt0;
+                    hide_columns<WIN>(sr, lim, from, to);
 #pragma unroll
                     for (int b = 0; b < 8; ++b)   // none of the block: its scale, NaN even, plays no part
-                        if (kBlockSize * b >= lim) fs[b] = 1.f;
-                }
-                if (WIN && kt0 < low) {   // keys behind the row's window that are not first tokens
-                    const int from = p.sinks - kt0, to = low - kt0;
-#pragma unroll
-                    for (int c = 0; c < 128; ++c)
-                        if (c >= from && c < to) sr[c] = __float_as_uint(-INFINITY);
-#pragma unroll
-                    for (int b = 0; b < 8; ++b)
-                        if (kBlockSize * b >= from && kBlockSize * (b + 1) <= to) fs[b] = 1.f;
+                        if (kBlockSize * b >= lim || (WIN && kBlockSize * b >= from && kBlockSize * (b + 1) <= to)) fs[b] = 1.f;
                 }
                 // row max of s + log2 vs
                 float mxs = -INFINITY;
@@ -361,8 +359,8 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
                     l2 = fma_f32x2(add_f32x2(w[0], w[1]), f32x2(iv[b], iv[b]), l2);
                     if (b == 3) {   // the first half of P, under which its PV can begin
                         tmem_st32(t_row + col_s(t) + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-                        if (j >= 1 && __any_sync(0xffffffffu, need)) {
-                            // O_t holds the tiles before j (their PV completed before S_t(j) did)
+                        if (i_step >= 1 && __any_sync(0xffffffffu, need)) {
+                            // O_t holds the key tiles before (their PV completed before S_t(j) did)
 #pragma unroll 1
                             for (int c = 0; c < D; c += 32) {
                                 uint32_t orr[32];
@@ -416,6 +414,25 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (!warp_wait(bar(B_ODONE + t), ocnt & 1, &abort_flag)) { ok = false; break; }
             ++ocnt;
             tc_fence_after();
+            // a split tile: sub-tile 1 hands over its maximum and sum, and goes on when
+            // sub-tile 0 has read its O
+            Joined joined;
+            if (sh.split) {
+                if (t == 1) {
+                    second[row] = make_float2(m, l);
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(B_SECOND));
+                    if (!warp_wait(bar(B_JOINED), n_split & 1, &abort_flag)) { ok = false; break; }
+                    ++n_split;
+                    tc_fence_after();
+                    continue;
+                }
+                if (!warp_wait(bar(B_SECOND), n_split & 1, &abort_flag)) { ok = false; break; }
+                ++n_split;
+                tc_fence_after();
+                joined.join(m, l, second[row]);
+            }
             const float inv = l == 0.f ? 0.f : 1.f / l;   // no visible key: 0; a NaN stays one
             const int tok = tile.t0 + i;
             const int h = tile.kv_head * G + gq;
@@ -423,7 +440,13 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
             if (tile.part >= 0 && tok_valid)
                 slot = static_cast<int64_t>(p.part_offset[tok * p.n_groups + tile.kv_head / p.heads_per_group]) +
                        tile.part;
-            store_output<D>(p, t_row + col_o(t), tok_valid, tile.part, tok, h, slot, inv, lane);
+            store_output<D>(p, t_row + col_o(t), t_row + col_o(1), sh.split, tok_valid, tile.part, tok, h, slot,
+                            joined.a0 * inv, joined.a1 * inv, lane, [&] {
+                                if (!sh.split) return;
+                                tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) mbar_arrive(bar(B_JOINED));
+                            });
             // the partial's weight 2^m l in the merge, kept as l = 1 (L holds the
             // range of 1 / vs); a NaN takes the merge over
             if (tok_valid && tile.part >= 0)
@@ -440,37 +463,37 @@ scaled_extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_cons
     }
 }
 
-template <int D, bool WIN>
+template <int D, bool WIN, bool SPLIT>
 cudaError_t configure() {
     // the attribute is per function and device; setting it again is harmless
-    return cudaFuncSetAttribute(scaled_extend_kernel<D, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScaledExtCfg<D>::SMEM);
+    return cudaFuncSetAttribute(scaled_extend_kernel<D, WIN, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScaledExtCfg<D>::SMEM);
 }
 
-template <int D, bool WIN>
+template <int D, bool WIN, bool SPLIT>
 cudaError_t launch_t(int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                      const ScaledExtendParams &p, cudaStream_t stream, bool pdl) {
     using C = ScaledExtCfg<D>;
-    return launch_ex(scaled_extend_kernel<D, WIN>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, pdl, tm_q, tm_k, tm_v, p);
+    return launch_ex(scaled_extend_kernel<D, WIN, SPLIT>, dim3(grid), dim3(C::THREADS), C::SMEM, stream, pdl, tm_q, tm_k, tm_v, p);
 }
 
 }  // namespace
 
-cudaError_t prepare_scaled_extend(int head_dim, bool window) {
-    if (head_dim == 128) return window ? configure<128, true>() : configure<128, false>();
-    if (head_dim == 64) return window ? configure<64, true>() : configure<64, false>();
+#define PA_EXTEND_CASE(window, split, f, ...)                                                     \
+    if (head_dim == 128)                                                                          \
+        return !(window) ? f<128, false, false>(__VA_ARGS__)                                      \
+               : (split) ? f<128, true, true>(__VA_ARGS__) : f<128, true, false>(__VA_ARGS__);    \
+    if (head_dim == 64)                                                                           \
+        return !(window) ? f<64, false, false>(__VA_ARGS__)                                       \
+               : (split) ? f<64, true, true>(__VA_ARGS__) : f<64, true, false>(__VA_ARGS__);      \
     return cudaErrorInvalidValue;
-}
+
+cudaError_t prepare_scaled_extend(int head_dim, bool window, bool split) { PA_EXTEND_CASE(window, split, configure) }
 
 cudaError_t launch_scaled_extend(int head_dim, int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const ScaledExtendParams &p, cudaStream_t stream, bool pdl) {
     if (grid <= 0) return cudaSuccess;
-    if (head_dim == 128)
-        return p.base.window > 0 ? launch_t<128, true>(grid, tm_q, tm_k, tm_v, p, stream, pdl)
-                                 : launch_t<128, false>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
-    if (head_dim == 64)
-        return p.base.window > 0 ? launch_t<64, true>(grid, tm_q, tm_k, tm_v, p, stream, pdl)
-                                 : launch_t<64, false>(grid, tm_q, tm_k, tm_v, p, stream, pdl);
-    return cudaErrorInvalidValue;
+    PA_EXTEND_CASE(p.base.window > 0, p.base.split != 0, launch_t, grid, tm_q, tm_k, tm_v, p, stream, pdl)
 }
+#undef PA_EXTEND_CASE
 
 }  // namespace pa

@@ -511,25 +511,32 @@ struct TileBlock {
     int32_t steps;       // its 128-key steps
     int32_t first_steps; // those of its first sub-tile
     int32_t pieces = 1;
+    int32_t own_steps() const { return tile.split ? (steps + 1) / 2 : steps; }   // two key tiles a step where split
 };
 
-// Costs in steps (1.55 us): a tile's Q load and epilogue as the assignment to CTAs
-// counts them, one more for a piece's fp32 output, and the merge that joins pieces
-// (its launch, the partials written and read back, a row's partials one after
-// another).  Fitted: 512 tokens of 32 heads over 1024 / 2048 / 4096 keys, cut in
-// two 27.7 / 33.9 / 44.8 us, whole 19.8 / 30.5 / 53.9; one token of 32 heads over
-// 8192 keys in 17 / 33 pieces 15.1 / 18.4 us, whole 89.6.
-constexpr int kTileExtra = 2, kPieceExtra = 3;
-constexpr double kMergeLaunch = 1.5, kMergeBytesPerStep = 2.9e6, kMergePerPiece = 0.1;
+// Costs in quarters of a step (1.4 us): a step, one of a split tile, a tile's Q load
+// and epilogue as the assignment to CTAs counts them, what it takes more where the
+// epilogue joins two sub-tiles or writes a piece's fp32 output, and the merge that joins
+// pieces (its launch, the partials written and read back, a row's partials one after
+// another).  Fitted: 512 tokens of 32 heads over 1024 / 2048 / 4096 keys, whole 19.8 /
+// 30.5 / 53.9 us, halved 16.1 / 23.1 / 36.7, cut in two 27.7 / 33.9 / 44.8; one token of
+// 32 heads over 8192 keys in 17 / 33 pieces 15.1 / 18.4 us, whole 89.6.
+constexpr int kStepCost = 4, kSplitStepCost = 5, kTileCost = 8, kJoinCost = 4, kPieceCost = 4;
+constexpr double kMergeLaunch = 6, kMergeBytesPerQuarter = 0.7e6, kMergePerPiece = 0.4;
 constexpr int kMaxPieces = 32;   // (the merge kernel's lanes)
 
-// Steps of the longest CTA when tiles of the given steps (descending) go to the
-// least loaded one each.
-int64_t longest_cta(const std::vector<int32_t> &steps, int ctas) {
+int64_t tile_cost(const TileBlock &b, int64_t own_steps, int32_t pieces) {
+    return own_steps * (b.tile.split ? kSplitStepCost : kStepCost) + kTileCost + (b.tile.split ? kJoinCost : 0) +
+           (pieces > 1 ? kPieceCost : 0);
+}
+
+// Cost of the longest CTA when tiles of the given costs (descending) go to the least
+// loaded one each.
+int64_t longest_cta(const std::vector<int64_t> &costs, int ctas) {
     std::priority_queue<int64_t, std::vector<int64_t>, std::greater<int64_t>> load;
     for (int c = 0; c < ctas; ++c) load.push(0);
     int64_t most = 0;
-    for (int32_t s : steps) {
+    for (int64_t s : costs) {
         const int64_t v = load.top() + s;
         load.pop();
         load.push(v);
@@ -538,59 +545,74 @@ int64_t longest_cta(const std::vector<int32_t> &steps, int ctas) {
     return most;
 }
 
-// Cut the keys of a windowed plan's tiles where that ends the step sooner: when the
-// tiles are fewer than the CTAs (a short chunk, a single token of more than 16 heads
-// per kv head), or leave the last round of CTAs mostly empty.  Partials are
-// joined by the merge kernel; a block's tiles of all kv heads are cut alike, as the
-// merge joins all heads of a token.  row_bytes: a token's partial.
-void cut_blocks(std::vector<TileBlock> &blocks, int hkv, int64_t row_bytes, int ctas) {
+// Spread a windowed plan's tiles where that ends the step sooner: when they are fewer
+// than the CTAs (a short chunk, a single token of more than 16 heads per kv head), or
+// leave the last round of CTAs mostly empty.  Two ways, together too: tiles of half the
+// rows, whose two sub-tiles share the keys (halve), and pieces of the keys, joined by
+// the merge kernel (a block's tiles of all kv heads alike, as the merge joins all heads
+// of a token).  row_bytes: a token's partial.
+// Over bf16 caches all tiles are split or none (the kernel's V loads).
+template <typename Halve>
+void spread_blocks(std::vector<TileBlock> &blocks, Halve halve, int hkv, int64_t row_bytes, int ctas, bool bf16) {
     const int64_t n = static_cast<int64_t>(blocks.size()) * hkv;
     if (n == 0 || n > 8LL * ctas) return;   // many rounds of CTAs hide an uneven last one
-    // longest first; the first `cut` of them may be cut: all, or those of the last round
-    std::vector<int32_t> order(blocks.size());
-    for (size_t i = 0; i < order.size(); ++i) order[i] = static_cast<int32_t>(i);
-    std::stable_sort(order.begin(), order.end(), [&](int32_t a, int32_t b) { return blocks[a].steps > blocks[b].steps; });
+    auto cost = [](const TileBlock &b) { return tile_cost(b, b.own_steps(), 1); };
+    // longest first; the first `cut` of them may be spread: all, or those of the last round
+    std::stable_sort(blocks.begin(), blocks.end(), [&](const TileBlock &a, const TileBlock &b) { return cost(a) > cost(b); });
     const size_t cut = n < ctas ? blocks.size() : static_cast<size_t>((n % ctas + hkv - 1) / hkv);
-    const int32_t longest = blocks[order[0]].steps;
-    auto pieces_of = [&](size_t i, int32_t most) { return i < cut ? (blocks[order[i]].steps + most - 1) / most : 1; };
-    double best = longest + kTileExtra, best_merge = 0;
-    int32_t piece = 0;
-    for (int k = 2; k <= std::min(kMaxPieces, longest / 2) && cut > 0; ++k) {
-        const int32_t most = (longest + k - 1) / k;
-        int64_t tiles = 0, rows = 0;
+    if (cut == 0) return;
+    double best = static_cast<double>(cost(blocks[0])), best_merge = 0;
+    std::vector<TileBlock> taken;
+    enum { kAsIs, kWhole, kHalved };
+    for (const int way : {kAsIs, kWhole, kHalved}) {
+        if (way == kHalved && bf16 && cut < blocks.size()) break;
+        std::vector<TileBlock> some;   // the blocks to spread
+        int32_t longest = 0;
         for (size_t i = 0; i < cut; ++i) {
-            const int32_t j = pieces_of(i, most);
-            tiles += static_cast<int64_t>(j) * hkv;
-            if (j > 1) rows += static_cast<int64_t>(j) * blocks[order[i]].tile.n_tok;
+            if (way == kHalved) halve(blocks[i], some);
+            else some.push_back(blocks[i]);
+            if (way == kWhole) some.back().tile.split = 0;   // (pieces of one sub-tile each)
         }
-        const double merge = kMergeLaunch + rows * row_bytes / kMergeBytesPerStep + k * kMergePerPiece;
-        const double t = static_cast<double>((tiles + ctas - 1) / ctas) * (most + kPieceExtra) + merge;
-        if (t < best) {
-            best = t;
-            best_merge = merge;
-            piece = most;
-        }
-    }
-    if (piece == 0) return;
-    if (n >= ctas) {   // whole tiles beside the pieces: as they would be dealt out
-        std::vector<int32_t> before, after;
-        for (size_t i = 0; i < order.size(); ++i) {
-            const int32_t steps = blocks[order[i]].steps, k = pieces_of(i, piece);
-            for (int h = 0; h < hkv; ++h) {
-                before.push_back(steps + kTileExtra);
-                for (int32_t j = 0; j < k; ++j)
-                    after.push_back(steps * (j + 1) / k - steps * j / k + (k > 1 ? kPieceExtra : kTileExtra));
+        for (const TileBlock &b : some) longest = std::max(longest, b.own_steps());
+        for (int k = 1; k <= std::max(1, std::min(kMaxPieces, longest / 2)); ++k) {
+            const int32_t most = (longest + k - 1) / k;
+            int64_t tiles = 0, rows = 0, one = 0;
+            for (const TileBlock &b : some) {
+                const int32_t j = (b.own_steps() + most - 1) / most;
+                tiles += static_cast<int64_t>(j) * hkv;
+                if (j > 1) rows += static_cast<int64_t>(j) * b.tile.n_tok;
+                one = std::max(one, tile_cost(b, std::min(b.own_steps(), most), j));
+            }
+            const double merge = rows > 0 ? kMergeLaunch + rows * row_bytes / kMergeBytesPerQuarter + k * kMergePerPiece : 0;
+            const double t = static_cast<double>((tiles + ctas - 1) / ctas) * one + merge;
+            if (t < best) {
+                best = t;
+                best_merge = merge;
+                taken = some;
+                for (TileBlock &b : taken) b.pieces = (b.own_steps() + most - 1) / most;
             }
         }
-        std::sort(after.begin(), after.end(), std::greater<int32_t>());
-        if (longest_cta(after, ctas) + best_merge >= longest_cta(before, ctas)) return;
     }
-    for (size_t i = 0; i < cut; ++i) blocks[order[i]].pieces = pieces_of(i, piece);
+    if (taken.empty()) return;
+    taken.insert(taken.end(), blocks.begin() + static_cast<long>(cut), blocks.end());
+    if (n >= ctas) {   // whole tiles beside the others: as they would be dealt out
+        auto longest = [&](const std::vector<TileBlock> &all) {
+            std::vector<int64_t> costs;
+            for (const TileBlock &b : all)
+                for (int32_t j = 0; j < b.pieces; ++j)
+                    costs.insert(costs.end(), static_cast<size_t>(hkv),
+                                 tile_cost(b, b.own_steps() * (j + 1) / b.pieces - b.own_steps() * j / b.pieces, b.pieces));
+            std::sort(costs.begin(), costs.end(), std::greater<int64_t>());
+            return longest_cta(costs, ctas);
+        };
+        if (longest(taken) + best_merge >= longest(blocks)) return;
+    }
+    blocks.swap(taken);
 }
 
-// cut: windowed plans may cut the keys of tiles (cut_blocks)
+// spread: windowed plans may make more tiles of their blocks (spread_blocks)
 pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape *shape, const pa_window_desc *win,
-                     bool cut) {
+                     bool spread) {
     P->fixed = shape != nullptr;
     P->window = win ? win->window : 0;
     P->sinks = win ? win->sink_tokens : 0;
@@ -691,9 +713,31 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
         P->tiles.reserve(n);
     }
     std::vector<TileBlock> blocks;   // windowed
+    // n tokens of request r from its m-th on: in WindowView's numbers, the keys shared by
+    // both sub-tiles where the rows fill one at most
+    auto block_of = [&](int32_t r, int32_t m, int32_t n) {
+        ExtendTile t{};
+        t.t0 = qsl[r] + m;
+        t.n_tok = n;
+        t.req = r;
+        const int32_t p0 = d->num_computed_tokens[r] + m;
+        // (over 8-bit caches whole key tiles of consecutive copies are read: the head is
+        // padded to one)
+        const WindowView v = window_view(p0, p0 + n, P->window, P->sinks, P->kv8 ? kTileKeys / kBlockSize : 1);
+        t.head = v.head;
+        t.skip = v.skip;
+        t.pos0 = p0 - v.skip * kBlockSize;
+        t.key_end = t.pos0 + n;
+        t.part = -1;
+        t.causal = 1;
+        t.split = n <= tpt / 2 ? 1 : 0;
+        auto steps = [&](int32_t rows) { return (t.pos0 + rows + kTileKeys - 1) / kTileKeys; };
+        return TileBlock{t, steps(n), steps(std::min(n, tpt / 2))};
+    };
     for (int32_t r : extend_rows) {
         const int32_t q_len = qsl[r + 1] - qsl[r];
-        for (int h = 0; h < (win ? 1 : P->Hkv); ++h)
+        for (int32_t m0 = 0; win && m0 < q_len; m0 += tpt) blocks.push_back(block_of(r, m0, std::min(tpt, q_len - m0)));
+        for (int h = 0; !win && h < P->Hkv; ++h)
             for (int32_t m0 = 0; m0 < q_len; m0 += tpt) {
                 ExtendTile t{};
                 t.t0 = qsl[r] + m0;
@@ -702,21 +746,6 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
                 t.pos0 = d->num_computed_tokens[r] + m0;
                 t.key_begin = kb_keys;
                 t.key_end = std::min(d->seq_lens[r], t.pos0 + t.n_tok);
-                if (win) {
-                    // block-scaled tiles read whole key tiles of consecutive copies:
-                    // their head is padded to one
-                    const WindowView v = window_view(t.pos0, t.key_end, P->window, P->sinks,
-                                                     P->scaled ? kTileKeys / kBlockSize : 1);
-                    t.head = v.head;
-                    t.skip = v.skip;
-                    t.pos0 -= v.skip * kBlockSize;
-                    t.key_end -= v.skip * kBlockSize;
-                    t.part = -1;
-                    t.causal = 1;
-                    const int32_t first_end = std::min(t.key_end, t.pos0 + std::min(t.n_tok, tpt / 2));
-                    blocks.push_back({t, (t.key_end + kTileKeys - 1) / kTileKeys, (first_end + kTileKeys - 1) / kTileKeys});
-                    continue;
-                }
                 t.kv_head = h;
                 t.part = cascade ? P->prefix_splits : -1;
                 t.causal = 1;
@@ -725,9 +754,20 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
     }
     std::vector<int32_t> tile_pieces;   // windowed: of each token's tiles
     if (win) {
+        auto halve = [&](const TileBlock &b, std::vector<TileBlock> &to) {
+            const int32_t r = b.tile.req, m = b.tile.t0 - qsl[r], n = b.tile.n_tok;
+            to.push_back(block_of(r, m, std::min(n, tpt / 2)));
+            if (n > tpt / 2) to.push_back(block_of(r, m + tpt / 2, n - tpt / 2));
+        };
+        bool all = true;
+        for (const TileBlock &b : blocks) all = all && b.tile.split != 0;
+        for (TileBlock &b : blocks)
+            if (!P->kv8 && !all) b.tile.split = 0;
         // staged inputs: rows from the decode prefix on may not be merged
-        if (cut && !(P->fixed && shape->decode_prefix_tokens > 0))
-            cut_blocks(blocks, P->Hkv, static_cast<int64_t>(P->Hq) * P->D * sizeof(float), P->num_sms);
+        if (spread && !(P->fixed && shape->decode_prefix_tokens > 0))
+            spread_blocks(blocks, halve, P->Hkv, static_cast<int64_t>(P->Hq) * P->D * sizeof(float), P->num_sms, !P->kv8);
+        P->split = P->fixed;
+        for (const TileBlock &b : blocks) P->split = P->split || b.tile.split != 0;
         tile_pieces.assign(static_cast<size_t>(P->T), 0);
         for (const TileBlock &b : blocks)
             for (int h = 0; h < P->Hkv; ++h)
@@ -833,6 +873,7 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
             // between two tiles a CTA spends some steps' time (1 / 2 / 3 / 4 steps
             // in the cut: 248.4 / 244.5 / 244.2 / 244.4 us for two chunks of 2048
             // tokens on E4M3, 214.3 / 211.4 / 211.7 / 211.5 on block-scaled codes)
+            if (t.split) n_tiles = ((n_tiles + 1) / 2 * kSplitStepCost + kJoinCost) / kStepCost;   // (two at a time, and a join)
             cost.push_back({n_tiles + 2, static_cast<int32_t>(i)});
             model.tile_units += n_tiles + 1;
             model.tile_max = std::max<double>(model.tile_max, n_tiles + 1);
@@ -1155,18 +1196,18 @@ pa_status make_plan(const pa_batch_desc *desc, const pa_fixed_shape *shape, cons
     if (shape && desc->kv_cache_dtype != PA_KV_BF16 && shape->max_extend_tiles > 0 && shape->max_dequant_blocks == 0)
         return PA_ERR_INVALID_ARGUMENT;   // tiles over 8-bit caches read 16-bit copies: they need room
     pa_plan_s *P = nullptr;
-    // a fixed shape without room for the pieces of cut tiles takes them whole
-    for (const bool cut : {true, false}) {
+    // a fixed shape without room for more tiles, or for partials, takes them whole
+    for (const bool spread : {true, false}) {
         P = new (std::nothrow) pa_plan_s();
         if (!P) return PA_ERR_INVALID_ARGUMENT;
         try {
-            st = build_plan(P, desc, shape, win, cut);
+            st = build_plan(P, desc, shape, win, spread);
         } catch (const std::bad_alloc &) {   // (nothing throws across the ABI)
             st = PA_ERR_INVALID_ARGUMENT;
         }
         if (st == PA_OK) break;
         delete P;
-        if (!cut || !win || st != PA_ERR_CAPACITY) return st;
+        if (!spread || !win || st != PA_ERR_CAPACITY) return st;
     }
     *out = P;
     *workspace_bytes = P->ws_bytes;
@@ -1229,7 +1270,8 @@ pa_status prepare_plan(pa_plan_s *P) {
     if (P->ncta > 0 && (P->scaled ? prepare_scaled_decode(P->D, P->HG, P->int8, window)
                                   : prepare_decode(P->D, P->HG, P->kv8, window)) != cudaSuccess)
         return PA_ERR_CUDA;
-    if (P->cap_tiles > 0 && (P->scaled ? prepare_scaled_extend(P->D, window) : prepare_extend(P->D, window)) != cudaSuccess)
+    if (P->cap_tiles > 0 && (P->scaled ? prepare_scaled_extend(P->D, window, P->split)
+                                       : prepare_extend(P->D, window, P->kv8, P->split)) != cudaSuccess)
         return PA_ERR_CUDA;
     if (P->fork && side_stream() == nullptr) return PA_ERR_CUDA;
     P->prepared = true;
@@ -1346,8 +1388,8 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
             if (launch_dequant(std::min(P->cap_dequant, 8 * sms), qp, tile_stream, !fork) != cudaSuccess)
                 return PA_ERR_CUDA;
             const uint64_t srows = static_cast<uint64_t>(std::max(1, P->cap_dequant)) * kBlockSize;
-            // (block-scaled: a key tile's copies in one box)
-            const uint32_t box = P->scaled ? kTileKeys : kBlockSize;
+            // (block-scaled or windowed: a key tile's copies in one box)
+            const uint32_t box = P->scaled || P->window > 0 ? kTileKeys : kBlockSize;
             if (!make_map(&tm_tk, ws + P->off_kscr, P->D, P->Hkv, srows, 1, box) ||
                 !make_map(&tm_tv, ws + P->off_vscr, P->D, P->Hkv, srows, 1, box))
                 return PA_ERR_CUDA;
@@ -1376,6 +1418,9 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
         ep.out_scale = P->out_scale;
         ep.window = P->window;
         ep.sinks = P->sinks;
+        ep.value_cache = P->kv8 ? nullptr : static_cast<const uint16_t *>(value_cache);
+        ep.num_heads_kv = P->Hkv;
+        ep.split = P->split ? 1 : 0;
         if (rec(1, true, tile_stream) != cudaSuccess) return PA_ERR_CUDA;
         const ScaledExtendParams sep{ep, reinterpret_cast<const float4 *>(ws + P->off_factors)};
         if ((P->scaled ? launch_scaled_extend(P->D, P->ext_ctas, tm_q, tm_tk, tm_tv, sep, tile_stream, !fork)

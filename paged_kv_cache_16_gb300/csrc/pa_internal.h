@@ -120,7 +120,8 @@ struct ExtendTile {
     // windowed plans: pos0, key_begin and key_end are in WindowView's numbers
     int32_t head;        // its fields
     int32_t skip;
-    int32_t pad;
+    int32_t split;       // 1: at most one sub-tile of rows, whose keys both sub-tiles share:
+                         // key tiles go to them in turn, and their results are joined
 };
 
 // The query heads [hq_begin, hq_begin + hq_count) of one token whose output
@@ -196,6 +197,9 @@ struct ExtendParams {
     float scale_log2;           // softmax_scale * k_scale * log2(e)
     float out_scale;            // v_scale (1 for bf16 caches)
     int32_t window, sinks;      // window > 0: see WindowView
+    const uint16_t *value_cache;    // windowed, bf16 caches (null: the tiles read consecutive copies)
+    int32_t num_heads_kv;
+    int32_t split;              // windowed: split tiles may be among them
 };
 
 // The same over block-scaled 8-bit caches (base.out_scale is unused): the K
@@ -416,7 +420,7 @@ cudaError_t launch_zero_blocks(const int32_t *ids, int32_t num_ids, int32_t num_
 // kernels a plan launches, so that later launches can be captured.
 cudaError_t prepare_decode(int head_dim, int hg, bool kv8, bool window);
 cudaError_t prepare_scaled_decode(int head_dim, int hg, bool int8, bool window);
-cudaError_t prepare_extend(int head_dim, bool window);
-cudaError_t prepare_scaled_extend(int head_dim, bool window);
+cudaError_t prepare_extend(int head_dim, bool window, bool copies, bool split);
+cudaError_t prepare_scaled_extend(int head_dim, bool window, bool split);
 
 }  // namespace pa

@@ -35,14 +35,19 @@ enum : int {
     B_PFULL = 14,   // +sub-tile: keys 0..63 of P; +2: keys 64..127
     B_ODONE = 18,   // +sub-tile
     B_DRAIN = 20,
-    NUM_BARS = 21
+    B_SECOND = 21,  // split tiles: sub-tile 1's O, maximum and sum are there
+    B_JOINED = 22,  // and have been read
+    NUM_BARS = 23
 };
 
 // key tiles each sub-tile of a CTA tile needs (0 for an empty sub-tile)
 struct TileShape {
     int n_sub[2];
     int n_tiles;
+    bool split;   // key tile j belongs to sub-tile j % 2
+    __device__ __forceinline__ int step(int i, int t) const { return split ? 2 * i + t : i; }   // i-th key tile of sub-tile t
 };
+template <bool SPLIT>
 __device__ __forceinline__ TileShape tile_shape(const ExtendTile &tile, int tpt) {
     TileShape sh;
 #pragma unroll
@@ -57,14 +62,36 @@ __device__ __forceinline__ TileShape tile_shape(const ExtendTile &tile, int tpt)
         sh.n_sub[t] = (kend - tile.key_begin + kTileKeys - 1) / kTileKeys;
     }
     sh.n_tiles = max(sh.n_sub[0], sh.n_sub[1]);
+    sh.split = SPLIT && tile.split != 0 && sh.n_tiles >= 2;
+    if (sh.split) {
+        sh.n_sub[0] = (sh.n_tiles + 1) / 2;
+        sh.n_sub[1] = sh.n_tiles / 2;
+    }
     return sh;
+}
+
+// Hide the columns of an S row that a query does not see: from `lim` on, and
+// [from, to) with a window.  A bit per column, so that a column costs little more
+// than its select (two compares each: 4.7 us of the 71.4 that two chunks of 2048
+// tokens take over a window of 1024).
+template <bool WIN>
+__device__ __forceinline__ void hide_columns(uint32_t (&sr)[128], int lim, int from, int to) {
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        auto below = [&](int n) { return n <= 32 * w ? 0u : n >= 32 * w + 32 ? ~0u : (1u << (n - 32 * w)) - 1u; };
+        uint32_t seen = below(lim);
+        if (WIN) seen &= ~(below(to) & ~below(from));
+#pragma unroll
+        for (int c = 0; c < 32; ++c)
+            if (!(seen >> c & 1u)) sr[32 * w + c] = __float_as_uint(-INFINITY);
+    }
 }
 
 // The warp that issues the MMAs, over the CTA's tiles.  C: the kernel's
 // configuration (stages, tile bytes, instruction descriptors); q_s, k_s, v_s: its
 // shared memory.  P comes in two halves, so that PV begins under the second half's
 // exponentials.
-template <int D, typename C>
+template <int D, typename C, bool SPLIT>
 __device__ __forceinline__ void issue_mmas(const ExtendParams &p, uint32_t bars, uint32_t q_s, uint32_t k_s, uint32_t v_s,
                                            uint32_t tmem, int tile_begin, int tile_end, int tpt, int lane, int *abort_flag) {
     auto bar = [&](int i) { return bars + 8u * i; };
@@ -144,13 +171,43 @@ __device__ __forceinline__ void issue_mmas(const ExtendParams &p, uint32_t bars,
     const int ti_end = __shfl_sync(0xffffffffu, tile_end, 0);
     for (int ti = __shfl_sync(0xffffffffu, tile_begin, 0); ti < ti_end && ok; ++ti) {
         const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-        const TileShape sh = tile_shape(tile, tpt);
+        const TileShape sh = tile_shape<SPLIT>(tile, tpt);
         const int n0 = __shfl_sync(0xffffffffu, sh.n_sub[0], 0), n1 = __shfl_sync(0xffffffffu, sh.n_sub[1], 0);
         const int n = max(n0, n1), n_both = min(n0, n1);
         ok = warp_wait_spin(bar(B_QFULL), n_q & 1, abort_flag);
         ++n_q;
         if (!ok || n == 0) {
             if (ok) tc_commit_if(lead, bar(B_QEMPTY));
+            continue;
+        }
+        if (SPLIT && __shfl_sync(0xffffffffu, sh.split ? 1 : 0, 0)) {
+            // a key tile for one sub-tile, the next for the other
+            auto next_qk = [&](int t, bool last) -> bool {
+                if (!need(k_ready, k_bar, k_par)) return false;
+                tc_fence_after();
+                qk(t, nothing);
+                tc_commit_if(lead, k_bar + kEmptyK);
+                next_k();
+                if (last) tc_commit_if(lead, bar(B_QEMPTY));
+                return true;
+            };
+            ok = next_qk(0, false) && next_qk(1, n0 + n1 == 2);
+            for (int i = 0; i < n0 && ok; ++i) {
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int nt = t ? n1 : n0;
+                    if (!ok || i >= nt) continue;
+                    ok = need(v_ready, v_bar, v_par) && need(p_ready[t], pfull[t], p_par[t]);
+                    if (!ok) break;
+                    tc_fence_after();
+                    ok = pv(t, i > 0 ? 1u : 0u, nothing);
+                    if (!ok) break;
+                    tc_commit_if(lead, v_bar + kEmptyV);
+                    next_v();
+                    if (i + 1 < nt) ok = next_qk(t, 2 * (i + 1) + t + 1 == n0 + n1);
+                    else tc_commit_if(lead, bar(B_ODONE + t));
+                }
+            }
             continue;
         }
         if (!need(k_ready, k_bar, k_par)) { ok = false; break; }
@@ -229,11 +286,33 @@ __device__ __forceinline__ void issue_mmas(const ExtendParams &p, uint32_t bars,
     __syncwarp();
 }
 
-// A row's output of a finished tile: O (tensor memory at o_at, this warp's lanes)
-// times `inv`, as bf16 into its row of out, or as fp32 into its partial.
-template <int D>
-__device__ __forceinline__ void store_output(const ExtendParams &p, uint32_t o_at, bool tok_valid, int part, int tok, int h,
-                                             int64_t slot, float inv, int lane) {
+// N columns of a row's O (tensor memory at o_at, this warp's lanes) times `inv`; with a
+// second sub-tile's O at `other`, that one times `inv2` added.
+template <int N>
+__device__ __forceinline__ void load_output(uint32_t (&x)[N], uint32_t o_at, uint32_t other, bool two, float inv, float inv2) {
+#pragma unroll
+    for (int c = 0; c < N; c += 32) tmem_ld32(o_at + c, *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < N; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * inv);
+    if (two) {
+#pragma unroll
+        for (int c = 0; c < N; c += 32) {
+            uint32_t y[32];
+            tmem_ld32(other + c, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+                x[c + e] = __float_as_uint(fmaf(__uint_as_float(y[e]), inv2, __uint_as_float(x[c + e])));
+        }
+    }
+}
+
+// A row's output of a finished tile: O times `inv` (and the second sub-tile's), as bf16
+// into its row of out, or as fp32 into its partial.  read() runs once O has been read.
+template <int D, typename Read>
+__device__ __forceinline__ void store_output(const ExtendParams &p, uint32_t o_at, uint32_t other, bool two, bool tok_valid,
+                                             int part, int tok, int h, int64_t slot, float inv, float inv2, int lane, Read read) {
     if (part < 0) {
         // Four neighbouring lanes hold four rows; their 32-byte pieces are
         // exchanged so that a store writes 128 consecutive bytes of 8 rows
@@ -247,12 +326,10 @@ __device__ __forceinline__ void store_output(const ExtendParams &p, uint32_t o_a
 #pragma unroll 1
         for (int c = 0; c < D; c += 64) {
             uint32_t orr[64], w[32];
-            tmem_ld32(o_at + c, *reinterpret_cast<uint32_t(*)[32]>(&orr[0]));
-            tmem_ld32(o_at + c + 32, *reinterpret_cast<uint32_t(*)[32]>(&orr[32]));
-            tmem_wait_ld();
+            load_output<64>(orr, o_at + c, other + c, two, inv, inv2);
+            if (c + 64 >= D) read();
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(orr[2 * e]) * inv, __uint_as_float(orr[2 * e + 1]) * inv);
+            for (int e = 0; e < 32; ++e) w[e] = pack_bf16x2(__uint_as_float(orr[2 * e]), __uint_as_float(orr[2 * e + 1]));
 #pragma unroll
             for (int bit = 1; bit <= 2; bit *= 2) {
                 const bool up = lane & bit;
@@ -278,23 +355,30 @@ __device__ __forceinline__ void store_output(const ExtendParams &p, uint32_t o_a
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
             uint32_t orr[32];
-            tmem_ld32(o_at + c, orr);
-            tmem_wait_ld();
+            load_output<32>(orr, o_at + c, other + c, two, inv, inv2);
+            if (c + 32 >= D) read();
             if (!tok_valid) continue;
             float *dst = p.o_part + (slot * p.num_heads_q + h) * D + c;
 #pragma unroll
             for (int q8 = 0; q8 < 4; ++q8)
-                st_global_v8(dst + q8 * 8, __float_as_uint(__uint_as_float(orr[q8 * 8 + 0]) * inv),
-                             __float_as_uint(__uint_as_float(orr[q8 * 8 + 1]) * inv),
-                             __float_as_uint(__uint_as_float(orr[q8 * 8 + 2]) * inv),
-                             __float_as_uint(__uint_as_float(orr[q8 * 8 + 3]) * inv),
-                             __float_as_uint(__uint_as_float(orr[q8 * 8 + 4]) * inv),
-                             __float_as_uint(__uint_as_float(orr[q8 * 8 + 5]) * inv),
-                             __float_as_uint(__uint_as_float(orr[q8 * 8 + 6]) * inv),
-                             __float_as_uint(__uint_as_float(orr[q8 * 8 + 7]) * inv));
+                st_global_v8(dst + q8 * 8, orr[q8 * 8 + 0], orr[q8 * 8 + 1], orr[q8 * 8 + 2], orr[q8 * 8 + 3],
+                             orr[q8 * 8 + 4], orr[q8 * 8 + 5], orr[q8 * 8 + 6], orr[q8 * 8 + 7]);
         }
     }
 }
+
+// The joint result of a split tile's sub-tiles, for the warpgroup of sub-tile 0: m and l
+// become those of all keys, and a0, a1 what each sub-tile's O counts in it.
+struct Joined {
+    float a0 = 1.f, a1 = 0.f;
+    __device__ __forceinline__ void join(float &m, float &l, float2 second) {
+        const float top = fmaxf(m, second.x);
+        a0 = m == -INFINITY ? 0.f : ex2(m - top);
+        a1 = second.x == -INFINITY ? 0.f : ex2(second.x - top);
+        m = top;
+        l = l * a0 + second.y * a1;
+    }
+};
 
 }  // namespace tiles
 }  // namespace pa
