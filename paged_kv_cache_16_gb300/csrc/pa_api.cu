@@ -307,58 +307,79 @@ void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector
     ncta = std::max<int64_t>(ncta, 1);
     if (fixed_ncta > 0) ncta = std::min(ncta, fixed_ncta);
     if (P->window > 0) {
-        // Windows make runs of one length: where there are enough of them, whole runs
-        // on the CTAs stream as fast as an equal cut and need no merge (window
-        // 1024, bf16: 90 requests 60.2 us instead of 62.7, 128 79.6 instead of 87.8, 128
-        // of 128 keys 15.0 instead of 20.0; but 64 of 1024 52.6 instead of 46.0).
-        std::vector<int32_t> order(runs.size());
-        for (size_t i = 0; i < order.size(); ++i) order[i] = static_cast<int32_t>(i);
-        std::stable_sort(order.begin(), order.end(),
-                         [&](int32_t a, int32_t b) { return runs[a].pe - runs[a].pb > runs[b].pe - runs[b].pb; });
-        const int64_t grid = std::min<int64_t>(cap, static_cast<int64_t>(runs.size()));
-        std::vector<std::vector<int32_t>> of(static_cast<size_t>(grid));
-        std::priority_queue<std::pair<int64_t, int64_t>, std::vector<std::pair<int64_t, int64_t>>,
-                            std::greater<std::pair<int64_t, int64_t>>> load;
-        for (int64_t c = 0; c < grid; ++c) load.push({0, c});
+        // Windows make runs of one length: dealt out whole, or in as many equal pieces
+        // as give every CTA one, they stream as fast as an equal cut, with fewer items
+        // and fewer partials to merge, or none (window 1024, bf16: 90 requests 60.2 us
+        // instead of 62.7, 128 79.6 instead of 87.8, 128 of 128 keys 15.0 instead of 20.0;
+        // but 64 of 1024 whole 52.6 instead of 46.0).
+        struct Piece { int32_t run, pb, pe; };
         int64_t rows = 0;
-        for (int32_t i : order) {
-            const std::pair<int64_t, int64_t> least = load.top();
-            load.pop();
-            of[least.second].push_back(i);
-            load.push({least.first + runs[i].pe - runs[i].pb, least.second});
-            rows = std::max<int64_t>(rows, units[runs[i].u].n_tok);
-        }
+        for (const Run &r : runs) rows = std::max<int64_t>(rows, units[r.u].n_tok);
         const double bytes = 2.0 * kBlockSize * P->HG * P->D * (P->kv8 ? 1 : 2);   // of a block
         const double rate = !P->kv8                            ? kSmBf16BytesPerUs
                             : rows * P->G > kMmaRows / 2       ? kSmRows16BytesPerUs
                             : P->scaled                        ? kSmScaledBytesPerUs
                                                                : kSmFp8AloneBytesPerUs;
-        // whole runs: the CTAs share HBM until they end, shortest first
         const double cta_rate = rate / cps;   // (its share of an SM's consumer warps)
-        double whole = 0;
-        int64_t done = 0, active = grid;
-        for (; !load.empty(); load.pop(), --active) {
-            whole += (load.top().first - done) * bytes / std::min(cta_rate, kHbmBytesPerUs / active);
-            done = load.top().first;
+        auto merge_us = [&](double parts) {
+            return kMergeUs + parts * rows * P->HG * P->G * P->D * sizeof(float) / kMergeBytesPerUs;
+        };
+        double best = total * bytes / std::min(kHbmBytesPerUs, ncta * cta_rate) +
+                      merge_us(static_cast<double>(std::min<int64_t>(runs.size(), ncta) + ncta));
+        std::vector<std::vector<Piece>> dealt;
+        const int64_t each = cap / static_cast<int64_t>(runs.size());
+        for (const int64_t k : {int64_t{1}, each}) {
+            if (k < 1 || (k > 1 && total / (k * static_cast<int64_t>(runs.size())) < min_pages)) continue;
+            std::vector<Piece> some;
+            some.reserve(runs.size() * static_cast<size_t>(k));
+            for (size_t i = 0; i < runs.size(); ++i) {
+                const int64_t n = runs[i].pe - runs[i].pb;
+                for (int64_t j = 0; j < k; ++j) {
+                    const int32_t from = static_cast<int32_t>(n * j / k), to = static_cast<int32_t>(n * (j + 1) / k);
+                    if (to > from) some.push_back({static_cast<int32_t>(i), runs[i].pb + from, runs[i].pb + to});
+                }
+            }
+            const double merge = k > 1 ? merge_us(static_cast<double>(some.size())) : 0;
+            std::stable_sort(some.begin(), some.end(), [](const Piece &x, const Piece &y) { return x.pe - x.pb > y.pe - y.pb; });
+            // to the least loaded CTA each; the CTAs share HBM until they end, shortest
+            // first
+            const int64_t grid = std::min<int64_t>(cap, static_cast<int64_t>(some.size()));
+            std::vector<std::vector<Piece>> of(static_cast<size_t>(grid));
+            std::priority_queue<std::pair<int64_t, int64_t>, std::vector<std::pair<int64_t, int64_t>>,
+                                std::greater<std::pair<int64_t, int64_t>>> load;
+            for (int64_t c = 0; c < grid; ++c) load.push({0, c});
+            for (const Piece &x : some) {
+                const std::pair<int64_t, int64_t> least = load.top();
+                load.pop();
+                of[least.second].push_back(x);
+                load.push({least.first + x.pe - x.pb, least.second});
+            }
+            double t = merge;
+            int64_t done = 0, active = grid;
+            for (; !load.empty(); load.pop(), --active) {
+                t += (load.top().first - done) * bytes / std::min(cta_rate, kHbmBytesPerUs / active);
+                done = load.top().first;
+            }
+            if (t < best) {
+                best = t;
+                dealt.swap(of);
+            }
         }
-        const double parts = static_cast<double>(std::min<int64_t>(runs.size(), ncta) + ncta);
-        const double cut = total * bytes / std::min(kHbmBytesPerUs, ncta * cta_rate) + kMergeUs +
-                           parts * rows * P->HG * P->G * P->D * sizeof(float) / kMergeBytesPerUs;
-        if (whole < cut) {
-            P->items.reserve(runs.size());
-            for (const std::vector<int32_t> &mine : of) {
-                for (int32_t i : mine) {
+        if (!dealt.empty()) {
+            for (const std::vector<Piece> &mine : dealt) {
+                for (const Piece &x : mine) {
+                    const Run &r = runs[x.run];
                     DecodeItem it{};
-                    it.token = units[runs[i].u].t0;
-                    it.req = units[runs[i].u].r;
-                    it.page_begin = runs[i].pb;
-                    it.page_end = runs[i].pe;
-                    it.key_end = units[runs[i].u].key_end;
-                    it.head_group = runs[i].grp;
-                    it.part = pieces[static_cast<size_t>(runs[i].u) * P->n_groups + runs[i].grp]++;
-                    it.n_tok = units[runs[i].u].n_tok;
+                    it.token = units[r.u].t0;
+                    it.req = units[r.u].r;
+                    it.page_begin = x.pb;
+                    it.page_end = x.pe;
+                    it.key_end = units[r.u].key_end;
+                    it.head_group = r.grp;
+                    it.part = pieces[static_cast<size_t>(r.u) * P->n_groups + r.grp]++;
+                    it.n_tok = units[r.u].n_tok;
                     P->items.push_back(it);
-                    item_unit.push_back(runs[i].u);
+                    item_unit.push_back(r.u);
                 }
                 P->cta_begin.push_back(static_cast<int32_t>(P->items.size()));
             }
