@@ -355,7 +355,8 @@ pa_status pa_plan_fixed(const pa_batch_desc *desc, const pa_fixed_shape *shape, 
  * (window 1: itself alone; one that reaches past position 0 hides nothing).  The
  * attention calls take the plan as they take others, by its kv_cache_dtype: the
  * window is a model field of the plan, and a layer with another window wants
- * another plan (and another upload into its workspace).  Rows, slots and
+ * another plan, with a workspace of its own or an upload before each launch: a launch
+ * reads the metadata of the plan it is given.  Rows, slots and
  * block_table are those of the whole context, with any blocks that no query of the
  * step sees given back: of request r the blocks from
  * ceil(min(sink_tokens, seq_lens[r]) / 16) up to
@@ -376,7 +377,8 @@ pa_status pa_plan_fixed(const pa_batch_desc *desc, const pa_fixed_shape *shape, 
  * within rounding.
  * Errors: as pa_plan / pa_plan_fixed, plus PA_ERR_INVALID_ARGUMENT for a NULL
  * window, window <= 0 or sink_tokens < 0, and PA_ERR_UNSUPPORTED for
- * num_common_prefix_blocks > 0 (a window leaves no prefix in common).
+ * num_common_prefix_blocks > 0 (a window leaves no prefix in common) or a context
+ * above 2^31 - 257 tokens.  (pa_graph_create makes plans without a window.)
  */
 typedef struct {
     int32_t window;              /* > 0                                               */

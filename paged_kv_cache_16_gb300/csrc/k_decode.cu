@@ -25,6 +25,7 @@
 //    E4M3 caches: codes converted in registers to f16 MMA operands; items of
 //    at most 8 query rows compute the transposed products (keys as MMA rows),
 //    which halves their MMAs.
+#include <atomic>
 #include <type_traits>
 
 #include "dev.cuh"
@@ -150,7 +151,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             for (int pg = item.page_begin; pg < item.page_end; ++pg) {
                 if (pg - window >= 32) {
                     window = pg;
-                    blk_lane = pg + lane < item.page_end ? bt[view.at(pg + lane)] : 0;
+                    blk_lane = pg + lane < item.page_end ? bt[WIN ? min(view.at(pg + lane), p.max_blocks - 1) : pg + lane] : 0;
                 }
                 const int s = issued % C::NS;
                 const int n = issued / C::NS;
@@ -887,12 +888,15 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 
 template <int D, int HG, bool KV8, bool FUSED, bool WIN>
 cudaError_t configure() {
-    static bool configured = false;  // attribute is per function, set once per process
-    if (!configured) {
+    // the attribute is per function and device: set once for each
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!(configured.load(std::memory_order_relaxed) >> dev & 1)) {
         cudaError_t e = cudaFuncSetAttribute(decode_kernel<D, HG, KV8, FUSED, WIN>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, DecodeCfg<D, HG, KV8>::SMEM);
         if (e != cudaSuccess) return e;
-        configured = true;
+        configured.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
     }
     return cudaSuccess;
 }

@@ -437,7 +437,7 @@ scaled_decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_cons
             for (int pg = item.page_begin; pg < item.page_end; ++pg) {
                 if (pg - window >= 32) {
                     window = pg;
-                    blk_lane = pg + lane < item.page_end ? bt[view.at(pg + lane)] : 0;
+                    blk_lane = pg + lane < item.page_end ? bt[WIN ? min(view.at(pg + lane), p.max_blocks - 1) : pg + lane] : 0;
                 }
                 const int s = issued % C::NS;
                 const int n = issued / C::NS;

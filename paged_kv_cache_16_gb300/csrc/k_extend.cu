@@ -33,6 +33,8 @@
 // (P_t in the first 64 columns of S_t), O_0 [256,256+D), O_1 [384,384+D).
 // Shared memory tiles are 128-byte-swizzled [rows][64 elements] halves:
 // Q_t (A, K-major), K (B, K-major), V (B, MN-major).
+#include <atomic>
+
 #include "tiles.cuh"
 
 namespace pa {
@@ -514,12 +516,15 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 
 template <int D, bool WIN, bool COPIES, bool SPLIT>
 cudaError_t configure() {
-    static bool configured = false;  // attribute is per function, set once per process
-    if (!configured) {
+    // the attribute is per function and device: set once for each
+    static std::atomic<uint64_t> configured{0};
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!(configured.load(std::memory_order_relaxed) >> dev & 1)) {
         cudaError_t e = cudaFuncSetAttribute(extend_kernel<D, WIN, COPIES, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              ExtCfg<D>::SMEM);
         if (e != cudaSuccess) return e;
-        configured = true;
+        configured.fetch_or(uint64_t{1} << dev, std::memory_order_relaxed);
     }
     return cudaSuccess;
 }

@@ -3,6 +3,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <exception>
 #include <mutex>
 #include <queue>
 #include <new>
@@ -1213,7 +1214,12 @@ pa_status make_plan(const pa_batch_desc *desc, const pa_fixed_shape *shape, cons
         return PA_ERR_INVALID_ARGUMENT;
     pa_status st = validate(desc, win);
     if (st != PA_OK) return st;
-    if (win && desc->num_common_prefix_blocks > 0) return PA_ERR_UNSUPPORTED;
+    if (win) {
+        if (desc->num_common_prefix_blocks > 0) return PA_ERR_UNSUPPORTED;
+        // (positions rounded up to key tiles stay in 32 bits)
+        for (int32_t r = 0; r < desc->num_reqs; ++r)
+            if (desc->seq_lens[r] > INT32_MAX - 2 * kTileKeys) return PA_ERR_UNSUPPORTED;
+    }
     if (shape && desc->kv_cache_dtype != PA_KV_BF16 && shape->max_extend_tiles > 0 && shape->max_dequant_blocks == 0)
         return PA_ERR_INVALID_ARGUMENT;   // tiles over 8-bit caches read 16-bit copies: they need room
     pa_plan_s *P = nullptr;
@@ -1223,7 +1229,7 @@ pa_status make_plan(const pa_batch_desc *desc, const pa_fixed_shape *shape, cons
         if (!P) return PA_ERR_INVALID_ARGUMENT;
         try {
             st = build_plan(P, desc, shape, win, spread);
-        } catch (const std::bad_alloc &) {   // (nothing throws across the ABI)
+        } catch (const std::exception &) {   // (nothing throws across the ABI)
             st = PA_ERR_INVALID_ARGUMENT;
         }
         if (st == PA_OK) break;

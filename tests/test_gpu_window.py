@@ -245,6 +245,89 @@ def test_two_streams_at_once(code):
         oc.assert_within(g.out, ref, tol)
 
 
+@pytest.mark.parametrize("q_lens,seq", [([1, 1], [500, 70]), ([20, 1, 100], [900, 33, 260])])
+def test_staged_inputs(q_lens, seq):
+    """Rows from the decode prefix on behind an event: the unstaged results."""
+    order = np.argsort([q > 1 for q in q_lens], kind="stable")      # decode rows first
+    q_lens, seq = [q_lens[i] for i in order], [seq[i] for i in order]
+    c = wc.WindowCase(hq=8, hkv=2, d=128, q_lens=q_lens, seq_lens=seq, code="bf16", window=90, sinks=5, seed=4, hidden=False)
+    P = sum(q for q in q_lens if q == 1)
+    shape = dict(max_tokens=200, max_reqs=4, max_extend_tiles=8, decode_prefix_tokens=P)
+    g = torch.Generator().manual_seed(9)
+    key, value = (torch.randn(200, 2, 128, generator=g).to(torch.bfloat16).to(DEV) for _ in range(2))
+    a, b = wc.OnGpu(c, shape=shape, num_sms=40), wc.OnGpu(c, shape=shape, num_sms=40)
+    for x in (a, b):
+        binding.pa_upload_metadata(x.plan, x.ws)
+    binding.pa_attention_with_kv_update_launch(a.plan, a.q, key, value, a.kc, a.vc, a.table, a.out, a.ws)
+    late, ready = torch.cuda.Event(), torch.cuda.Event()
+    late.record()
+    binding.pa_attention_with_kv_update_launch_staged(b.plan, b.q, key, value, b.kc, b.vc, b.table, b.out, b.ws, late,
+                                                      late_out_ready=ready)
+    torch.cuda.synchronize()
+    for x, y in ((a.out, b.out), (a.kc, b.kc), (a.vc, b.vc)):
+        assert torch.equal(x, y)
+    c.kc, c.vc = a.kc.cpu(), a.vc.cpu()
+    ref, tol = c.reference()
+    oc.assert_within(a.out[:c.T], ref, tol)
+
+
+@pytest.mark.parametrize("code", wc.KINDS)
+@pytest.mark.parametrize("q_len", [1, 5, 30, 200])
+def test_cache_offsets_past_32_bits(code, q_len):
+    """Blocks whose elements lie beyond 2^32: a pool of 9 GB (bf16) for K and for V."""
+    c = wc.WindowCase(hq=16, hkv=8, d=128, q_lens=[q_len], seq_lens=[700], code=code, window=300, sinks=20, seed=q_len, spare=0)
+    nb, base = 2**32 // (16 * 8 * 128) + 1000, 2**32 // (16 * 8 * 128) + 500
+    big = [torch.empty((nb,) + tuple(t.shape[1:]), dtype=t.dtype, device=DEV) for t in (c.kc, c.vc)]
+    for t, src in zip(big, (c.kc, c.vc)):
+        t[base:base + c.nb].copy_(src)
+    g = wc.OnGpu(c)
+    g.kc, g.vc = big
+    if c.scaled:
+        g.ks, g.vs = (torch.ones(nb, 8, device=DEV) for _ in range(2))
+        g.ks[base:base + c.nb], g.vs[base:base + c.nb] = c.ks.to(DEV), c.vs.to(DEV)
+    table = np.where(c.table >= 0, c.table + base, c.table).astype(np.int32)
+    g.table = torch.from_numpy(table).to(DEV)
+    g.plan = binding.pa_plan_window(**c.desc(num_blocks=nb, block_table_host=table))
+    g.ws = torch.zeros(g.plan.workspace_bytes, dtype=torch.uint8, device=DEV)
+    out = g.run()
+    ref, tol = c.reference()
+    oc.assert_within(out[:c.T], ref[:c.T], tol[:c.T])
+
+
+@pytest.mark.parametrize("code", wc.KINDS)
+def test_physical_blocks_do_not_matter_and_runs_repeat(code):
+    """The same logical contents elsewhere in the pool, and the same call again: the
+    same bits."""
+    kw = dict(hq=8, hkv=2, d=128, q_lens=[1, 4, 30, 1, 150], seq_lens=[900, 300, 1500, 40, 700], code=code, window=600, sinks=40)
+    c = wc.WindowCase(seed=1, spare=30, **kw)
+    g = wc.OnGpu(c)
+    first = g.run().clone()
+    assert torch.equal(g.run(), first)
+    perm = np.random.default_rng(7).permutation(c.nb)
+    p = torch.from_numpy(perm).to(DEV)
+    for name in ("kc", "vc", "ks", "vs"):
+        t = getattr(g, name)
+        moved = torch.empty_like(t)
+        moved[p] = t
+        setattr(g, name, moved)
+    g.table = torch.from_numpy(np.where(c.table >= 0, perm[c.table], c.table).astype(np.int32)).to(DEV)
+    assert torch.equal(g.run(), first)
+
+
+@pytest.mark.parametrize("code", wc.KINDS)
+def test_outputs_at_16_bytes(code):
+    """An output that starts 16 bytes past a 32-byte boundary."""
+    c = wc.WindowCase(hq=8, hkv=2, d=128, q_lens=[1, 30, 3, 150], seq_lens=[300, 500, 99, 700], code=code, window=200, sinks=4)
+    g = wc.OnGpu(c)
+    want = g.run().clone()
+    buf = torch.zeros(want.numel() + 64, dtype=torch.bfloat16, device=DEV)
+    at = 8 if buf.data_ptr() % 32 == 0 else 0
+    g.out = buf[at:at + want.numel()].view(want.shape)
+    assert g.out.data_ptr() % 32 == 16
+    assert torch.equal(g.run(), want)
+    assert not buf[:at].any() and not buf[at + want.numel():].any()
+
+
 @pytest.mark.parametrize("code", wc.KINDS)
 def test_bad_block_is_reported(code):
     """A block id out of range that the host did not see, in the window or among the

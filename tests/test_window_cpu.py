@@ -40,6 +40,16 @@ def test_window_arguments(over, status, q_len):
     assert binding.pa_plan_window_status(**{**desc([q_len], [900]), **over}) == status
 
 
+def test_contexts_longer_than_the_pool():
+    """A context may outgrow the pool, and 32 bits of rounded positions are kept."""
+    for n, status in ((2**31 - 257, OK), (2**31 - 256, UNSUPPORTED), (2**31 - 1, UNSUPPORTED)):
+        for q in (1, 4, 300):
+            kw = desc([q], [n], 512, 20, max_blocks_per_req=2**27)
+            assert binding.pa_plan_window_status(**kw) == status, (n, q)
+    info = binding.pa_plan_window(**desc([1], [2**31 - 257], 512, 20, max_blocks_per_req=2**27)).info()
+    assert info["decode_kv_bytes"] == (512 + 20) * 2 * 2 * 128 * 2
+
+
 def test_window_null_arguments(lib):
     d, _keep = binding.make_desc(**{k: v for k, v in desc([1], [9]).items() if k not in ("window", "sink_tokens")})
     w, p, n = binding.WindowDesc(4, 0), ctypes.c_void_p(), ctypes.c_size_t()
