@@ -70,8 +70,9 @@ struct ExtCfg {
 // WIN: with a sliding window and first tokens (tiles in WindowView's numbers: key
 // tiles of 128 keys run over the blocks with first tokens and on into those of the
 // tile's first window, whose lower masks reach over the first key tiles only).
-// SPLIT (with a window): tiles of one sub-tile of rows whose keys both sub-tiles share
-// may be among them (a variant of its own: it costs the other tiles 3%).  Sharing
+// SPLIT (with a window): some or all of the tiles are of one sub-tile of rows whose keys
+// both sub-tiles share (variants of their own: kSomeSplit costs the other tiles 3%, and
+// 512 tokens over 4096 keys 41.1 us instead of kAllSplit's 37.1).  Sharing
 // doubles the loads per step: K and V in boxes of one block and 64 columns (2 KB) come
 // at 46 GB/s per SM (the TMA unit's time per box), which that needs twice of.  So V
 // of such tiles comes by 16-byte asynchronous copies of the two idle warps (a step of
@@ -79,7 +80,7 @@ struct ExtCfg {
 // issue slots they take).  The planner splits all tiles of a step over bf16 caches or
 // none, so that one side brings every V tile of a CTA.  COPIES: over the consecutive
 // 16-bit copies of E4M3 blocks, a key tile is one box per 64 columns.
-template <int D, bool WIN, bool COPIES, bool SPLIT>
+template <int D, bool WIN, bool COPIES, int SPLIT>
 __global__ void __launch_bounds__(384, 1)
 extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v, const ExtendParams p) {
@@ -88,7 +89,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     __shared__ int abort_flag;
     __shared__ uint32_t tmem_base_slot;
     __shared__ __align__(8) uint64_t bars[NUM_BARS];
-    __shared__ float2 second[SPLIT ? kTileRows : 1];   // split tiles: sub-tile 1's maximum and sum of each row
+    __shared__ float2 second[SPLIT != 0 ? kTileRows : 1];   // split tiles: sub-tile 1's maximum and sum of each row
 
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     auto q_s = [&](int t) { return base + static_cast<uint32_t>(t) * C::QB; };
@@ -102,7 +103,8 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const int tile_begin = p.cta_tile_begin[blockIdx.x];
     const int tile_end = p.cta_tile_begin[blockIdx.x + 1];
     if (tile_begin >= tile_end) return;
-    const bool v_warps = SPLIT && !COPIES && p.tiles[p.cta_tiles[tile_begin]].split != 0;   // warps 2 and 3 bring V
+    // warps 2 and 3 bring V
+    const bool v_warps = !COPIES && (SPLIT == kAllSplit || (SPLIT == kSomeSplit && p.tiles[p.cta_tiles[tile_begin]].split != 0));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (uniform to the compiler)
     const int lane = threadIdx.x & 31;
     const int G = p.group;
@@ -154,7 +156,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         bool ok = true;
         for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
             const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-            const TileShape sh = tile_shape<SPLIT>(tile, tpt);
+            const TileShape sh = tile_shape<SPLIT != 0>(tile, tpt);
             // Q of this tile, once the previous tile's QK^T no longer read Q
             if (n_q_loads > 0 && !warp_wait(bar(B_QEMPTY), (n_q_loads - 1) & 1, &abort_flag)) {
                 if (lane == 0) raise_abort(&abort_flag, p.err, kErrTimeout);
@@ -270,7 +272,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issuer --
-        issue_mmas<D, C, SPLIT>(p, smem_u32(bars), q_s(0), k_s(0), v_s(0), tmem, tile_begin, tile_end, tpt, lane, &abort_flag);
+        issue_mmas<D, C, SPLIT != 0>(p, smem_u32(bars), q_s(0), k_s(0), v_s(0), tmem, tile_begin, tile_end, tpt, lane, &abort_flag);
       } else if (v_warps) {
         // ------------------------------------------------------- V copies --
         // Each warp brings 64 rows (4 blocks) of a V tile, swizzled as a box would
@@ -287,7 +289,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         };
         for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
             const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-            const TileShape sh = tile_shape<SPLIT>(tile, tpt);
+            const TileShape sh = tile_shape<SPLIT != 0>(tile, tpt);
             const WindowView view{tile.head, tile.skip};
             const int32_t *bt = p.block_table + static_cast<int64_t>(tile.req) * p.max_blocks;
             const int pg_end = (tile.key_end + kBlockSize - 1) / kBlockSize;
@@ -343,7 +345,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         bool ok = true;
         for (int ti = tile_begin; ti < tile_end && ok; ++ti) {
             const ExtendTile tile = p.tiles[p.cta_tiles[ti]];
-            const TileShape sh = tile_shape<SPLIT>(tile, tpt);
+            const TileShape sh = tile_shape<SPLIT != 0>(tile, tpt);
             const int i = (sh.split ? 0 : t * tpt) + row / G;   // token of this row within the tile
             const int gq = row % G;
             // rows past tpt * G (when G does not divide 128) are padding
@@ -514,7 +516,7 @@ extend_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
 }
 
-template <int D, bool WIN, bool COPIES, bool SPLIT>
+template <int D, bool WIN, bool COPIES, int SPLIT>
 cudaError_t configure() {
     // the attribute is per function and device: set once for each
     static std::atomic<uint64_t> configured{0};
@@ -529,7 +531,7 @@ cudaError_t configure() {
     return cudaSuccess;
 }
 
-template <int D, bool WIN, bool COPIES, bool SPLIT>
+template <int D, bool WIN, bool COPIES, int SPLIT>
 cudaError_t launch_t(int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k, const CUtensorMap &tm_v,
                      const ExtendParams &p, cudaStream_t stream, bool pdl) {
     using C = ExtCfg<D>;
@@ -540,28 +542,30 @@ cudaError_t launch_t(int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
 
 }  // namespace
 
-// f<WIN, COPIES, SPLIT> of a plan's variant (E4M3 caches, whose tiles read copies, have
+// f<D, WIN, COPIES, SPLIT> of a plan's variant (E4M3 caches, whose tiles read copies, have
 // head_dim 128)
-#define PA_EXTEND_CASE(window, copies, split, f, ...)                                        \
-    if (head_dim == 128 && !(window)) return f<128, false, false, false>(__VA_ARGS__);        \
-    if (head_dim == 128 && (copies))                                                          \
-        return (split) ? f<128, true, true, true>(__VA_ARGS__) : f<128, true, true, false>(__VA_ARGS__);   \
-    if (head_dim == 128)                                                                      \
-        return (split) ? f<128, true, false, true>(__VA_ARGS__) : f<128, true, false, false>(__VA_ARGS__); \
-    if (head_dim == 64 && !(window)) return f<64, false, false, false>(__VA_ARGS__);          \
-    if (head_dim == 64)                                                                       \
-        return (split) ? f<64, true, false, true>(__VA_ARGS__) : f<64, true, false, false>(__VA_ARGS__);   \
+#define PA_EXTEND_SPLIT(d, copies, split, f, ...)                                 \
+    return (split) == kNoSplit     ? f<d, true, copies, kNoSplit>(__VA_ARGS__)    \
+           : copies || (split) == kSomeSplit ? f<d, true, copies, kSomeSplit>(__VA_ARGS__) \
+                                   : f<d, true, copies, copies ? kSomeSplit : kAllSplit>(__VA_ARGS__);
+#define PA_EXTEND_CASE(window, copies, split, f, ...)                                  \
+    if (head_dim == 128 && !(window)) return f<128, false, false, kNoSplit>(__VA_ARGS__); \
+    if (head_dim == 64 && !(window)) return f<64, false, false, kNoSplit>(__VA_ARGS__);   \
+    if (head_dim == 128 && (copies)) PA_EXTEND_SPLIT(128, true, split, f, __VA_ARGS__)    \
+    if (head_dim == 128) PA_EXTEND_SPLIT(128, false, split, f, __VA_ARGS__)               \
+    if (head_dim == 64) PA_EXTEND_SPLIT(64, false, split, f, __VA_ARGS__)                 \
     return cudaErrorInvalidValue;
 
-cudaError_t prepare_extend(int head_dim, bool window, bool copies, bool split) {
+cudaError_t prepare_extend(int head_dim, bool window, bool copies, int split) {
     PA_EXTEND_CASE(window, copies, split, configure)
 }
 
 cudaError_t launch_extend(int head_dim, int grid, const CUtensorMap &tm_q, const CUtensorMap &tm_k,
                           const CUtensorMap &tm_v, const ExtendParams &p, cudaStream_t stream, bool pdl) {
     if (grid <= 0) return cudaSuccess;
-    PA_EXTEND_CASE(p.window > 0, p.value_cache == nullptr, p.split != 0, launch_t, grid, tm_q, tm_k, tm_v, p, stream, pdl)
+    PA_EXTEND_CASE(p.window > 0, p.value_cache == nullptr, p.split, launch_t, grid, tm_q, tm_k, tm_v, p, stream, pdl)
 }
 #undef PA_EXTEND_CASE
+#undef PA_EXTEND_SPLIT
 
 }  // namespace pa

@@ -788,8 +788,9 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
         // staged inputs: rows from the decode prefix on may not be merged
         if (spread && !(P->fixed && shape->decode_prefix_tokens > 0))
             spread_blocks(blocks, halve, P->Hkv, static_cast<int64_t>(P->Hq) * P->D * sizeof(float), P->num_sms, !P->kv8);
-        P->split = P->fixed;
-        for (const TileBlock &b : blocks) P->split = P->split || b.tile.split != 0;
+        size_t n_split = 0;
+        for (const TileBlock &b : blocks) n_split += b.tile.split != 0 ? 1 : 0;
+        P->split = P->fixed || (n_split > 0 && n_split < blocks.size()) ? kSomeSplit : n_split > 0 ? kAllSplit : kNoSplit;
         tile_pieces.assign(static_cast<size_t>(P->T), 0);
         for (const TileBlock &b : blocks)
             for (int h = 0; h < P->Hkv; ++h)
@@ -1297,7 +1298,7 @@ pa_status prepare_plan(pa_plan_s *P) {
     if (P->ncta > 0 && (P->scaled ? prepare_scaled_decode(P->D, P->HG, P->int8, window)
                                   : prepare_decode(P->D, P->HG, P->kv8, window)) != cudaSuccess)
         return PA_ERR_CUDA;
-    if (P->cap_tiles > 0 && (P->scaled ? prepare_scaled_extend(P->D, window, P->split)
+    if (P->cap_tiles > 0 && (P->scaled ? prepare_scaled_extend(P->D, window, P->split != kNoSplit)
                                        : prepare_extend(P->D, window, P->kv8, P->split)) != cudaSuccess)
         return PA_ERR_CUDA;
     if (P->fork && side_stream() == nullptr) return PA_ERR_CUDA;
@@ -1447,7 +1448,7 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
         ep.sinks = P->sinks;
         ep.value_cache = P->kv8 ? nullptr : static_cast<const uint16_t *>(value_cache);
         ep.num_heads_kv = P->Hkv;
-        ep.split = P->split ? 1 : 0;
+        ep.split = P->split;
         if (rec(1, true, tile_stream) != cudaSuccess) return PA_ERR_CUDA;
         const ScaledExtendParams sep{ep, reinterpret_cast<const float4 *>(ws + P->off_factors)};
         if ((P->scaled ? launch_scaled_extend(P->D, P->ext_ctas, tm_q, tm_tk, tm_tv, sep, tile_stream, !fork)

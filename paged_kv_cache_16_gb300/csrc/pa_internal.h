@@ -124,6 +124,9 @@ struct ExtendTile {
                          // key tiles go to them in turn, and their results are joined
 };
 
+// Which of a plan's tiles are split (a fixed shape's: some).
+enum TileSplit : int { kNoSplit = 0, kSomeSplit = 1, kAllSplit = 2 };
+
 // The query heads [hq_begin, hq_begin + hq_count) of one token whose output
 // is the merge of `count` partial results starting at partial slot `slot0`.
 struct MergeRow {
@@ -199,7 +202,7 @@ struct ExtendParams {
     int32_t window, sinks;      // window > 0: see WindowView
     const uint16_t *value_cache;    // windowed, bf16 caches (null: the tiles read consecutive copies)
     int32_t num_heads_kv;
-    int32_t split;              // windowed: split tiles may be among them
+    int32_t split;              // windowed: which tiles are split (TileSplit)
 };
 
 // The same over block-scaled 8-bit caches (base.out_scale is unused): the K
@@ -420,7 +423,7 @@ cudaError_t launch_zero_blocks(const int32_t *ids, int32_t num_ids, int32_t num_
 // kernels a plan launches, so that later launches can be captured.
 cudaError_t prepare_decode(int head_dim, int hg, bool kv8, bool window);
 cudaError_t prepare_scaled_decode(int head_dim, int hg, bool int8, bool window);
-cudaError_t prepare_extend(int head_dim, bool window, bool copies, bool split);
+cudaError_t prepare_extend(int head_dim, bool window, bool copies, int split);
 cudaError_t prepare_scaled_extend(int head_dim, bool window, bool split);
 
 }  // namespace pa

@@ -15,7 +15,7 @@ struct pa_plan_s {
     int32_t prefix_req = -1;      // block-table row of the shared prefix
     int32_t prefix_splits = 0;
     int32_t window = 0, sinks = 0;   // sliding window (0: none) and first tokens that stay visible
-    bool split = false;         // windowed: the tile kernel takes split tiles (a fixed shape's always does)
+    int32_t split = pa::kNoSplit;   // windowed: which tiles are split
     float scale_log2 = 0.f;     // softmax_scale * k_scale * log2(e)
     bool kv8 = false;           // 8-bit caches (E4M3, or block-scaled)
     bool scaled = false;        // block-scaled: the attention calls with scales take it
