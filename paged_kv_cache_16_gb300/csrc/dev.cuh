@@ -454,7 +454,7 @@ __device__ __forceinline__ uint32_t sw128(uint32_t base, uint32_t row, uint32_t 
 //   m = max m_r,  w_r = 2^(m_r - m) l_r,  out = sum w_r o_r / sum w_r.
 // Partials are read in slot order, so the result does not depend on which
 // CTA or kernel performs the merge.
-template <int D>
+template <int D, int KPRE>
 __device__ __forceinline__ void merge_head(uint16_t *out_row, const float *o_part, const float2 *ml_part,
                                            int64_t slot0, int count, int num_heads_q, int h, int lane) {
     constexpr int V = D / 32;
@@ -464,7 +464,6 @@ __device__ __forceinline__ void merge_head(uint16_t *out_row, const float *o_par
     // whose l is 0 was never written and its o is skipped (not multiplied
     // by 0: it may hold anything).  L2 loads: partials written by other SMs
     // in this same launch must not be served from a stale L1 line.
-    constexpr int KPRE = 8;
     using VecT = typename std::conditional<V == 4, float4, float2>::type;
     auto o_at = [&](int j) {
         return reinterpret_cast<const VecT *>(o_part + ((slot0 + j) * num_heads_q + h) * D + lane * V);

@@ -1069,6 +1069,8 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
         }
     }
     if (slots > INT32_MAX) return PA_ERR_UNSUPPORTED;
+    P->few_partials = win && !P->fixed && !P->merges.empty();
+    for (const MergeRow &m : P->merges) P->few_partials = P->few_partials && m.count <= 3;
     P->num_slots = static_cast<int32_t>(slots);
 
     // ------------------------------------------------- launch shape
@@ -1506,6 +1508,7 @@ pa_status enqueue_attention(pa_plan_s *P, const void *q, const void *key_cache, 
         mp.counts = counts;
         mp.num_heads_q = P->Hq;
         mp.max_heads = P->HG * P->G;
+        mp.few = P->few_partials ? 1 : 0;
         const int64_t warps = static_cast<int64_t>(P->cap_merges) * mp.max_heads;   // 8 warps per CTA
         const int grid = static_cast<int>(std::min<int64_t>((warps + 7) / 8, 16 * sms));
         if (rec(2, true, stream) != cudaSuccess) return PA_ERR_CUDA;

@@ -248,6 +248,7 @@ struct MergeParams {
     const int32_t *counts;      // device work counts (MetaCounts)
     int32_t num_heads_q;
     int32_t max_heads;          // largest hq_count of any row
+    int32_t few;                // no row has more than three partials
 };
 
 // Work counts at the head of the uploaded metadata: kernels launched on a
