@@ -221,7 +221,9 @@ pa_status validate(const pa_batch_desc *d, const pa_window_desc *win = nullptr) 
 // Side by side the two slow each other down a little (the tiles' K/V
 // re-reads and the decode stream share L2 and HBM): the side constants below
 // were measured that way.  With E4M3 caches the tile stream first makes the
-// bf16 copies of the tiles' blocks (three bytes moved per code).
+// bf16 copies of the tiles' blocks (three bytes moved per code).  (The tiles' step
+// times are those of the kernel's first schedule, 1.55 us on one SM by now: another
+// split of a mixed step would round differently and has not been fitted.)
 constexpr double kTileStepUs = 1.85;          // one 128-key step of a 256-row tile on one SM
 constexpr double kTileStepSideUs = 2.15;      // the same beside the bf16 decode stream
 constexpr double kTileStepSideFp8Us = 1.80;   // the same beside the E4M3 decode stream
@@ -280,6 +282,43 @@ int decode_ctas_per_sm(const pa_plan_s *P) {
                                  : decode_ctas_per_sm_static(P->D, P->HG, P->kv8));
 }
 
+// Blocks [pb, pe) of a run, as one item.
+struct Piece {
+    int32_t run, pb, pe;
+};
+
+// Deal pieces out, longest first (they are sorted), each to the least loaded of at
+// most `cap` CTAs; the time until the last one has streamed its own, when a CTA streams
+// `cta` blocks a microsecond and all of them `hbm` at most.
+double deal_pieces(std::vector<Piece> &pieces, int64_t cap, double hbm, double cta, std::vector<int32_t> &cta_of) {
+    auto longer = [](const Piece &x, const Piece &y) { return x.pe - x.pb > y.pe - y.pb; };
+    if (!std::is_sorted(pieces.begin(), pieces.end(), longer)) std::stable_sort(pieces.begin(), pieces.end(), longer);
+    const size_t n = pieces.size(), grid = static_cast<size_t>(std::min<int64_t>(cap, static_cast<int64_t>(n)));
+    cta_of.resize(n);
+    std::vector<uint64_t> load(grid);   // blocks << 32 | CTA: a min-heap once every CTA has one
+    for (size_t i = 0; i < grid; ++i) {
+        cta_of[i] = static_cast<int32_t>(i);
+        load[i] = static_cast<uint64_t>(pieces[i].pe - pieces[i].pb) << 32 | i;
+    }
+    if (n > grid) {
+        std::make_heap(load.begin(), load.end(), std::greater<uint64_t>());
+        for (size_t i = grid; i < n; ++i) {
+            std::pop_heap(load.begin(), load.end(), std::greater<uint64_t>());
+            cta_of[i] = static_cast<int32_t>(load.back() & 0xFFFFFFFFu);
+            load.back() += static_cast<uint64_t>(pieces[i].pe - pieces[i].pb) << 32;
+            std::push_heap(load.begin(), load.end(), std::greater<uint64_t>());
+        }
+    }
+    std::sort(load.begin(), load.end());
+    double t = 0;
+    uint64_t done = 0;
+    for (size_t i = 0; i < grid; ++i) {   // they share HBM until they end, shortest first
+        t += static_cast<double>((load[i] >> 32) - done) / std::min(cta, hbm / static_cast<double>(grid - i));
+        done = load[i] >> 32;
+    }
+    return t;
+}
+
 void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector<int32_t> &pieces,
                  std::vector<int32_t> &item_unit, int64_t work_ctas, int64_t fixed_ncta) {
     struct Run { int32_t u, grp, pb, pe; };
@@ -313,7 +352,6 @@ void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector
         // and fewer partials to merge, or none (window 1024, bf16: 90 requests 60.2 us
         // instead of 62.7, 128 79.6 instead of 87.8, 128 of 128 keys 15.0 instead of 20.0;
         // but 64 of 1024 whole 52.6 instead of 46.0).
-        struct Piece { int32_t run, pb, pe; };
         int64_t rows = 0;
         for (const Run &r : runs) rows = std::max<int64_t>(rows, units[r.u].n_tok);
         const double bytes = 2.0 * kBlockSize * P->HG * P->D * (P->kv8 ? 1 : 2);   // of a block
@@ -327,11 +365,12 @@ void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector
         };
         double best = total * bytes / std::min(kHbmBytesPerUs, ncta * cta_rate) +
                       merge_us(static_cast<double>(std::min<int64_t>(runs.size(), ncta) + ncta));
-        std::vector<std::vector<Piece>> dealt;
+        std::vector<Piece> some, taken;
+        std::vector<int32_t> cta_of, taken_cta;
         const int64_t each = cap / static_cast<int64_t>(runs.size());
-        for (const int64_t k : {int64_t{1}, each}) {
-            if (k < 1 || (k > 1 && total / (k * static_cast<int64_t>(runs.size())) < min_pages)) continue;
-            std::vector<Piece> some;
+        for (int64_t k = 1; k == 1 || k == each; k = k == 1 && each > 1 ? each : 0) {
+            if (k > 1 && total / (k * static_cast<int64_t>(runs.size())) < min_pages) break;
+            some.clear();
             some.reserve(runs.size() * static_cast<size_t>(k));
             for (size_t i = 0; i < runs.size(); ++i) {
                 const int64_t n = runs[i].pe - runs[i].pb;
@@ -340,49 +379,38 @@ void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector
                     if (to > from) some.push_back({static_cast<int32_t>(i), runs[i].pb + from, runs[i].pb + to});
                 }
             }
-            const double merge = k > 1 ? merge_us(static_cast<double>(some.size())) : 0;
-            std::stable_sort(some.begin(), some.end(), [](const Piece &x, const Piece &y) { return x.pe - x.pb > y.pe - y.pb; });
-            // to the least loaded CTA each; the CTAs share HBM until they end, shortest
-            // first
-            const int64_t grid = std::min<int64_t>(cap, static_cast<int64_t>(some.size()));
-            std::vector<std::vector<Piece>> of(static_cast<size_t>(grid));
-            std::priority_queue<std::pair<int64_t, int64_t>, std::vector<std::pair<int64_t, int64_t>>,
-                                std::greater<std::pair<int64_t, int64_t>>> load;
-            for (int64_t c = 0; c < grid; ++c) load.push({0, c});
-            for (const Piece &x : some) {
-                const std::pair<int64_t, int64_t> least = load.top();
-                load.pop();
-                of[least.second].push_back(x);
-                load.push({least.first + x.pe - x.pb, least.second});
-            }
-            double t = merge;
-            int64_t done = 0, active = grid;
-            for (; !load.empty(); load.pop(), --active) {
-                t += (load.top().first - done) * bytes / std::min(cta_rate, kHbmBytesPerUs / active);
-                done = load.top().first;
-            }
+            const double t = (k > 1 ? merge_us(static_cast<double>(some.size())) : 0) +
+                             deal_pieces(some, cap, kHbmBytesPerUs / bytes, cta_rate / bytes, cta_of);
             if (t < best) {
                 best = t;
-                dealt.swap(of);
+                taken.swap(some);
+                taken_cta.swap(cta_of);
             }
         }
-        if (!dealt.empty()) {
-            for (const std::vector<Piece> &mine : dealt) {
-                for (const Piece &x : mine) {
-                    const Run &r = runs[x.run];
-                    DecodeItem it{};
-                    it.token = units[r.u].t0;
-                    it.req = units[r.u].r;
-                    it.page_begin = x.pb;
-                    it.page_end = x.pe;
-                    it.key_end = units[r.u].key_end;
-                    it.head_group = r.grp;
-                    it.part = pieces[static_cast<size_t>(r.u) * P->n_groups + r.grp]++;
-                    it.n_tok = units[r.u].n_tok;
-                    P->items.push_back(it);
-                    item_unit.push_back(r.u);
-                }
-                P->cta_begin.push_back(static_cast<int32_t>(P->items.size()));
+        if (!taken.empty()) {
+            const int64_t grid = std::min<int64_t>(cap, static_cast<int64_t>(taken.size()));
+            // by CTA, in the order they were dealt out
+            std::vector<int32_t> begin(static_cast<size_t>(grid) + 1, 0), at(taken.size());
+            for (int32_t c : taken_cta) ++begin[static_cast<size_t>(c) + 1];
+            for (size_t c = 1; c < begin.size(); ++c) begin[c] += begin[c - 1];
+            P->cta_begin.assign(begin.begin(), begin.end());
+            for (size_t i = 0; i < taken.size(); ++i) at[static_cast<size_t>(begin[taken_cta[i]]++)] = static_cast<int32_t>(i);
+            P->items.reserve(taken.size());
+            item_unit.reserve(taken.size());
+            for (int32_t i : at) {
+                const Piece &x = taken[i];
+                const Run &r = runs[x.run];
+                DecodeItem it{};
+                it.token = units[r.u].t0;
+                it.req = units[r.u].r;
+                it.page_begin = x.pb;
+                it.page_end = x.pe;
+                it.key_end = units[r.u].key_end;
+                it.head_group = r.grp;
+                it.part = pieces[static_cast<size_t>(r.u) * P->n_groups + r.grp]++;
+                it.n_tok = units[r.u].n_tok;
+                P->items.push_back(it);
+                item_unit.push_back(r.u);
             }
             while (static_cast<int64_t>(P->cta_begin.size()) < fixed_ncta + 1)
                 P->cta_begin.push_back(static_cast<int32_t>(P->items.size()));
