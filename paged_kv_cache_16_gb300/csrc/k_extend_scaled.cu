@@ -33,6 +33,11 @@
 // the next tile's first QK^T in a tile's last step +2%, one loop body for full and
 // last steps +23%; stages given back by a softmax warp, tile descriptions in shared
 // memory, three K and two V stages: no change.
+//
+// 4096 tokens over 12288, a window of 4096 with 64 first tokens: 210 us beside the
+// 8 of the expansion (tensor pipe 55% active): 456 whole tiles of 34 steps in three
+// rounds, the last 56 halved; all 512 whole in four rounds 247 with the expansion, the
+// last ones' keys cut in two and merged 234.
 #include "tiles.cuh"
 
 namespace pa {
