@@ -85,22 +85,20 @@ PER_CONFIG = [("tiny-1A", "tiny-1A", "bf16"), ("tiny-1B", "tiny", "bf16"), ("dec
 # kernel from one ncu capture, valid only while the kernel source is
 # unchanged (sha256 prefix of the file); the summaries are under profiles/.
 TRAFFIC = {
-    # profiles/decode_kernel_decode-workload.md, profiles/decode_kernel_e4m3_decode-workload.md,
-    # profiles/step_launches_mixed-workload.md, profiles/extend_kernel_prefill-workload.md
-    ("decode", "decode", "bf16", "d98510bbbb11bb79"): 643_372_032,
-    ("decode", "decode", "fp8", "d98510bbbb11bb79"): 323_800_832,
-    ("decode", "mixed", "bf16", "d98510bbbb11bb79"): 4_686_585_600,
-    ("extend", "prefill", "bf16", "7f3cc3b83e5acc2f"): 75_693_056,
     # profiles/dram_traffic_decode-and-extend_per-workload.md
-    ("decode", "long", "bf16", "d98510bbbb11bb79"): 4_299_878_400,
-    ("decode", "long", "fp8", "d98510bbbb11bb79"): 2_150_972_416,
-    ("decode", "cascade", "bf16", "d98510bbbb11bb79"): 316_145_408,
-    ("extend", "cascade", "bf16", "7f3cc3b83e5acc2f"): 17_897_216,
-    ("decode", "cascade-off", "bf16", "d98510bbbb11bb79"): 334_178_560,
-    ("decode", "verify", "bf16", "d98510bbbb11bb79"): 674_436_608,
-    ("decode", "verify", "fp8", "d98510bbbb11bb79"): 341_064_704,
-    ("decode", "mixed", "fp8", "d98510bbbb11bb79"): 2_336_910_080,
-    ("extend", "mixed", "bf16", "7f3cc3b83e5acc2f"): 78_407_936,
+    ("decode", "decode", "bf16", "1050896b2c0b0931"): 643_047_680,
+    ("decode", "decode", "fp8", "1050896b2c0b0931"): 323_490_816,
+    ("decode", "mixed", "bf16", "1050896b2c0b0931"): 4_682_118_912,
+    ("extend", "prefill", "bf16", "3f18040844f97345"): 75_079_168,
+    ("decode", "long", "bf16", "1050896b2c0b0931"): 4_300_052_224,
+    ("decode", "long", "fp8", "1050896b2c0b0931"): 2_151_263_488,
+    ("decode", "cascade", "bf16", "1050896b2c0b0931"): 316_059_648,
+    ("extend", "cascade", "bf16", "3f18040844f97345"): 17_910_016,
+    ("decode", "cascade-off", "bf16", "1050896b2c0b0931"): 333_857_536,
+    ("decode", "verify", "bf16", "1050896b2c0b0931"): 674_432_256,
+    ("decode", "verify", "fp8", "1050896b2c0b0931"): 340_763_904,
+    ("decode", "mixed", "fp8", "1050896b2c0b0931"): 2_336_486_144,
+    ("extend", "mixed", "bf16", "3f18040844f97345"): 77_526_784,
 }
 KERNEL_SOURCES = {"decode": "paged_kv_cache_16_gb300/csrc/k_decode.cu",
                   "extend": "paged_kv_cache_16_gb300/csrc/k_extend.cu"}
