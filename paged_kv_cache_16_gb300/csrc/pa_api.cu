@@ -368,15 +368,17 @@ void plan_decode(pa_plan_s *P, const std::vector<DecodeUnit> &units, std::vector
         std::vector<Piece> some, taken;
         std::vector<int32_t> cta_of, taken_cta;
         const int64_t each = cap / static_cast<int64_t>(runs.size());
-        for (int64_t k = 1; k == 1 || k == each; k = k == 1 && each > 1 ? each : 0) {
+        const int64_t tries[2] = {1, each};   // pieces of a run
+        for (int i = 0; i < (each > 1 ? 2 : 1); ++i) {
+            const int64_t k = tries[i];
             if (k > 1 && total / (k * static_cast<int64_t>(runs.size())) < min_pages) break;
             some.clear();
             some.reserve(runs.size() * static_cast<size_t>(k));
-            for (size_t i = 0; i < runs.size(); ++i) {
-                const int64_t n = runs[i].pe - runs[i].pb;
+            for (size_t r = 0; r < runs.size(); ++r) {
+                const int64_t n = runs[r].pe - runs[r].pb;
                 for (int64_t j = 0; j < k; ++j) {
                     const int32_t from = static_cast<int32_t>(n * j / k), to = static_cast<int32_t>(n * (j + 1) / k);
-                    if (to > from) some.push_back({static_cast<int32_t>(i), runs[i].pb + from, runs[i].pb + to});
+                    if (to > from) some.push_back({static_cast<int32_t>(r), runs[r].pb + from, runs[r].pb + to});
                 }
             }
             const double t = (k > 1 ? merge_us(static_cast<double>(some.size())) : 0) +

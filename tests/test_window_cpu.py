@@ -145,6 +145,20 @@ def test_tiles_that_leave_sms_idle_are_cut(code):
     assert binding.pa_plan_window(**desc([1216], [9000], 8000, 0, code, **wide)).info()["num_extend_tiles"] == 152
 
 
+@pytest.mark.parametrize("num_sms", [1, 3, 20, 152])
+@pytest.mark.parametrize("code", range(4))
+def test_more_runs_than_ctas_and_fewer(num_sms, code):
+    """Every block of every row once, however many rows a CTA gets."""
+    for n in (1, 2, 7, 40, 500):
+        for d, hkv in ((128, 2), (128, 3)):
+            kw = desc([1] * n, [100 + 3 * i for i in range(n)], 64, 4, code, hq=4 * hkv, hkv=hkv, d=d, num_sms=num_sms)
+            info = binding.pa_plan_window(**kw).info()
+            assert info["num_decode_rows"] == n and info["num_decode_items"] >= n
+            assert binding.pa_plan_window(**{**kw, "window": 1}).info()["num_decode_items"] >= n
+            shape = dict(max_tokens=600, max_reqs=600)
+            assert binding.pa_plan_window(shape=shape, **kw).info()["num_decode_items"] == info["num_decode_items"]
+
+
 def test_windowed_plans_refuse_the_wrong_calls(lib):
     """The attention calls go by the cache type, windows or not."""
     plain = binding.pa_plan_window(**desc([1], [40], code=0))
