@@ -603,7 +603,8 @@ int64_t longest_cta(const std::vector<int64_t> &costs, int ctas) {
 // rows, whose two sub-tiles share the keys (halve), and pieces of the keys, joined by
 // the merge kernel (a block's tiles of all kv heads alike, as the merge joins all heads
 // of a token).  row_bytes: a token's partial.
-// Over bf16 caches all tiles are split or none (the kernel's V loads).
+// Over bf16 caches all tiles are split or none (the kernel's V loads), so that blocks of
+// the last round alone keep what the others have.
 template <typename Halve>
 void spread_blocks(std::vector<TileBlock> &blocks, Halve halve, int hkv, int64_t row_bytes, int ctas, bool bf16) {
     const int64_t n = static_cast<int64_t>(blocks.size()) * hkv;
@@ -617,7 +618,7 @@ void spread_blocks(std::vector<TileBlock> &blocks, Halve halve, int hkv, int64_t
     std::vector<TileBlock> taken;
     enum { kAsIs, kWhole, kHalved };
     for (const int way : {kAsIs, kWhole, kHalved}) {
-        if (way == kHalved && bf16 && cut < blocks.size()) break;
+        if (way != kAsIs && bf16 && cut < blocks.size()) break;
         std::vector<TileBlock> some;   // the blocks to spread
         int32_t longest = 0;
         for (size_t i = 0; i < cut; ++i) {
