@@ -465,16 +465,24 @@ def pa_plan_fixed_status(*, max_tokens, max_reqs, max_extend_tiles=0, max_dequan
     return st
 
 
+def _int32(n) -> int:
+    """For a 32-bit field that holds no negative number: one that it does not hold is
+    refused like those (ctypes would wrap it)."""
+    n = int(n)
+    return n if -2**31 <= n < 2**31 else -1
+
+
 def _plan_window(window, sink_tokens, shape, kw):
+    window, sink_tokens = _int32(window), _int32(sink_tokens)
     d, keep = make_desc(**kw)
     fs = _fixed_shape(**shape) if shape else None
     handle = ctypes.c_void_p()
     ws = ctypes.c_size_t()
-    st = load().pa_plan_window(ctypes.byref(d), ctypes.byref(WindowDesc(int(window), int(sink_tokens))),
+    st = load().pa_plan_window(ctypes.byref(d), ctypes.byref(WindowDesc(window, sink_tokens)),
                                ctypes.byref(fs) if fs is not None else None, ctypes.byref(handle), ctypes.byref(ws))
     rows = fs.max_tokens if fs is not None else int(keep[0][-1]) if len(keep[0]) else 0
-    return st, handle.value, lambda: Plan(handle.value, ws.value, keep, _step_of(d, rows), (int(window), int(sink_tokens)),
-                                     d.num_heads_q)
+    return st, handle.value, lambda: Plan(handle.value, ws.value, keep, _step_of(d, rows), (window, sink_tokens),
+                                          d.num_heads_q)
 
 
 def pa_plan_window(*, window, sink_tokens=0, shape: dict | None = None, **kw) -> Plan:
@@ -740,10 +748,12 @@ def pa_rope_status(*, rotary_dim, layout=PA_ROPE_HALF, base=10000.0, scaling=PA_
 
 
 def _axes_desc(rotary_dim, num_axes, axis_of_pair, frequencies):
-    axis = np.ascontiguousarray(axis_of_pair, dtype=np.int32)
-    if axis.ndim != 1 or 2 * axis.size != rotary_dim:
+    given = np.asarray(axis_of_pair)
+    with np.errstate(invalid="ignore"):   # (a number that 32 bits do not hold comes out as another)
+        axis = np.ascontiguousarray(given.astype(np.int32))
+    if axis.ndim != 1 or 2 * axis.size != rotary_dim or (axis != given).any():
         raise ValueError("axis_of_pair: an axis for each of the rotary_dim / 2 pairs wanted")
-    return RopeAxesDesc(int(num_axes), int(frequencies), axis.ctypes.data), axis
+    return RopeAxesDesc(_int32(num_axes), _int32(frequencies), axis.ctypes.data), axis
 
 
 def pa_rope_create_axes(*, num_axes, axis_of_pair, rotary_dim, frequencies=PA_ROPE_AXES_SHARED, layout=PA_ROPE_HALF,
