@@ -371,8 +371,7 @@ pa_status pa_plan_fixed(const pa_batch_desc *desc, const pa_fixed_shape *shape, 
  * Where tensor-core tiles would leave SMs idle, the plan makes more of them where that
  * ends the step sooner: tiles of half the rows, and pieces of a tile's keys, joined by
  * the merge (pa_plan_info.num_extend_tiles counts them all; the sums' order, and so the
- * rounding, is that of the plan).  The pieces' partials never take a step past
- * PA_NO_ALLOC_SCRATCH_BYTES that would stay below it without them.  A fixed shape does as pa_plan_window without a
+ * rounding, is that of the plan).  A fixed shape does as pa_plan_window without a
  * shape does if its max_extend_tiles and max_partial_slots have room, else (and with
  * decode_prefix_tokens) it makes none: its results then differ from the plain plan's
  * within rounding.

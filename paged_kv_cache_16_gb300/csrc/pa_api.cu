@@ -602,13 +602,11 @@ int64_t longest_cta(const std::vector<int64_t> &costs, int ctas) {
 // leave the last round of CTAs mostly empty.  Two ways, together too: tiles of half the
 // rows, whose two sub-tiles share the keys (halve), and pieces of the keys, joined by
 // the merge kernel (a block's tiles of all kv heads alike, as the merge joins all heads
-// of a token), as many as make at most max_pieces partials of a token.  row_bytes: of
-// one of those.
+// of a token).  row_bytes: a token's partial.
 // Over bf16 caches all tiles are split or none (the kernel's V loads), so that blocks of
 // the last round alone keep what the others have.
 template <typename Halve>
-void spread_blocks(std::vector<TileBlock> &blocks, Halve halve, int hkv, int64_t row_bytes, int64_t max_pieces, int ctas,
-                   bool bf16) {
+void spread_blocks(std::vector<TileBlock> &blocks, Halve halve, int hkv, int64_t row_bytes, int ctas, bool bf16) {
     const int64_t n = static_cast<int64_t>(blocks.size()) * hkv;
     if (n == 0 || n > 8LL * ctas) return;   // many rounds of CTAs hide an uneven last one
     auto cost = [](const TileBlock &b) { return tile_cost(b, b.own_steps(), 1); };
@@ -638,7 +636,6 @@ void spread_blocks(std::vector<TileBlock> &blocks, Halve halve, int hkv, int64_t
                 if (j > 1) rows += static_cast<int64_t>(j) * b.tile.n_tok;
                 one = std::max(one, tile_cost(b, std::min(b.own_steps(), most), j));
             }
-            if (rows > max_pieces) break;   // (more pieces, more rows)
             const double merge = rows > 0 ? kMergeLaunch + rows * row_bytes / kMergeBytesPerQuarter + k * kMergePerPiece : 0;
             const double t = static_cast<double>((tiles + ctas - 1) / ctas) * one + merge;
             if (t < best) {
@@ -666,16 +663,9 @@ void spread_blocks(std::vector<TileBlock> &blocks, Halve halve, int hkv, int64_t
     blocks.swap(taken);
 }
 
-// Partials of a token that pieces of tiles may make (spread_blocks): as many as they
-// like; kNoSpread: every block as one tile.
-constexpr int64_t kAnyPieces = INT64_MAX, kNoSpread = -1;
-
-// Bytes of workspace that a partial of a token and one group of kv heads takes.
-size_t partial_bytes(const pa_plan_s *P) { return static_cast<size_t>(P->Hq) * (P->D * sizeof(float) + sizeof(float2)); }
-
-// max_pieces: how far a windowed plan may spread its tiles
+// spread: windowed plans may make more tiles of their blocks (spread_blocks)
 pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape *shape, const pa_window_desc *win,
-                     int64_t max_pieces) {
+                     bool spread) {
     P->fixed = shape != nullptr;
     P->window = win ? win->window : 0;
     P->sinks = win ? win->sink_tokens : 0;
@@ -827,9 +817,8 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
         for (TileBlock &b : blocks)
             if (!P->kv8 && !all) b.tile.split = 0;
         // staged inputs: rows from the decode prefix on may not be merged
-        if (max_pieces != kNoSpread && !(P->fixed && shape->decode_prefix_tokens > 0))
-            spread_blocks(blocks, halve, P->Hkv, static_cast<int64_t>(P->Hq) * P->D * sizeof(float), max_pieces, P->num_sms,
-                          !P->kv8);
+        if (spread && !(P->fixed && shape->decode_prefix_tokens > 0))
+            spread_blocks(blocks, halve, P->Hkv, static_cast<int64_t>(P->Hq) * P->D * sizeof(float), P->num_sms, !P->kv8);
         size_t n_split = 0;
         for (const TileBlock &b : blocks) n_split += b.tile.split != 0 ? 1 : 0;
         P->split = P->fixed || (n_split > 0 && n_split < blocks.size()) ? kSomeSplit : n_split > 0 ? kAllSplit : kNoSplit;
@@ -1077,11 +1066,9 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
                 count[static_cast<size_t>(t) * P->n_groups + grp] = cascade ? P->prefix_splits + k : (k > 1 ? k : 0);
         }
     if (win)
-        for (size_t t = 0; t < tile_pieces.size(); ++t) {
-            P->tile_partials += tile_pieces[t];
+        for (size_t t = 0; t < tile_pieces.size(); ++t)
             for (int grp = 0; grp < P->n_groups && tile_pieces[t] > 0; ++grp)
                 count[t * P->n_groups + grp] = tile_pieces[t];
-        }
     if (cascade)
         for (int32_t r : extend_rows)
             for (int32_t t = qsl[r]; t < qsl[r + 1]; ++t)
@@ -1269,43 +1256,19 @@ pa_status make_plan(const pa_batch_desc *desc, const pa_fixed_shape *shape, cons
     }
     if (shape && desc->kv_cache_dtype != PA_KV_BF16 && shape->max_extend_tiles > 0 && shape->max_dequant_blocks == 0)
         return PA_ERR_INVALID_ARGUMENT;   // tiles over 8-bit caches read 16-bit copies: they need room
-    auto build = [&](int64_t max_pieces, pa_plan_s **plan) {
-        *plan = new (std::nothrow) pa_plan_s();
-        if (!*plan) return PA_ERR_INVALID_ARGUMENT;
-        pa_status made;
-        try {
-            made = build_plan(*plan, desc, shape, win, max_pieces);
-        } catch (const std::exception &) {   // (nothing throws across the ABI)
-            made = PA_ERR_INVALID_ARGUMENT;
-        }
-        if (made != PA_OK) {
-            delete *plan;
-            *plan = nullptr;
-        }
-        return made;
-    };
     pa_plan_s *P = nullptr;
-    st = build(kAnyPieces, &P);
     // a fixed shape without room for more tiles, or for partials, takes them whole
-    if (st == PA_ERR_CAPACITY && win) st = build(kNoSpread, &P);
-    if (st != PA_OK) return st;
-    // Pieces' partials are all that a plain plan has without a bound.  Where they take a
-    // step past the library's scratch, fewer pieces, or none: every step whose whole tiles
-    // go without a workspace does.
-    const size_t scratch = PA_NO_ALLOC_SCRATCH_BYTES, each = partial_bytes(P) * P->n_groups;
-    const size_t other = P->ws_bytes - static_cast<size_t>(P->tile_partials) * each;
-    if (!P->fixed && !P->scaled && P->tile_partials > 0 && P->ws_bytes > scratch && other - P->blob_bytes <= scratch) {
-        for (const int64_t pieces : {static_cast<int64_t>(scratch > other ? (scratch - other) / each : 0), kNoSpread}) {
-            pa_plan_s *fewer = nullptr;
-            if (build(pieces, &fewer) != PA_OK) continue;
-            if (fewer->ws_bytes > scratch) {
-                delete fewer;
-                continue;
-            }
-            delete P;
-            P = fewer;
-            break;
+    for (const bool spread : {true, false}) {
+        P = new (std::nothrow) pa_plan_s();
+        if (!P) return PA_ERR_INVALID_ARGUMENT;
+        try {
+            st = build_plan(P, desc, shape, win, spread);
+        } catch (const std::exception &) {   // (nothing throws across the ABI)
+            st = PA_ERR_INVALID_ARGUMENT;
         }
+        if (st == PA_OK) break;
+        delete P;
+        if (!spread || !win || st != PA_ERR_CAPACITY) return st;
     }
     *out = P;
     *workspace_bytes = P->ws_bytes;

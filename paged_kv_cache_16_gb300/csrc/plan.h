@@ -16,7 +16,6 @@ struct pa_plan_s {
     int32_t prefix_splits = 0;
     int32_t window = 0, sinks = 0;   // sliding window (0: none) and first tokens that stay visible
     int32_t split = pa::kNoSplit;   // windowed: which tiles are split
-    int64_t tile_partials = 0;      // windowed: partials of a token that pieces of tiles make
     bool few_partials = false;      // windowed, plain plans: three at most for any row
     float scale_log2 = 0.f;     // softmax_scale * k_scale * log2(e)
     bool kv8 = false;           // 8-bit caches (E4M3, or block-scaled)

@@ -5,7 +5,6 @@ import torch
 
 import window_common as wc
 from gpu_common import ensure_library
-from paged_kv_cache_16_gb300 import binding
 
 pytestmark = pytest.mark.gpu
 
@@ -28,20 +27,3 @@ def test_short_tiles_in_more_rounds_than_one(code, n, q, seq, window, sinks, lay
     lens = [seq + i % 7 for i in range(n)]
     wc.check(wc.WindowCase(hq=hq, hkv=hkv, d=128 if code == "e4m3" else d, q_lens=[q] * n, seq_lens=lens, code=code,
                            window=window, sinks=sinks, seed=n), num_sms=num_sms)
-
-
-@pytest.mark.parametrize("q_len", [128, 256])
-def test_long_windows_without_a_workspace(q_len):
-    """Chunks whose pieces would outgrow the library's scratch: the call without a
-    workspace takes them, with the bits of the call with one."""
-    c = wc.WindowCase(hq=32, hkv=8, d=128, q_lens=[q_len], seq_lens=[9000], code="bf16", window=8192, sinks=0, seed=q_len)
-    g = wc.OnGpu(c)
-    out = g.run().clone()
-    assert g.plan.info()["num_merge_rows"] == q_len
-    again = torch.zeros_like(out)
-    word = torch.zeros(1, dtype=torch.int32, device="cuda")
-    binding.pa_attention_no_alloc(g.plan, g.q, g.kc, g.vc, g.table, again, word)
-    assert torch.equal(again, out) and int(word) == 0
-    whole = wc.OnGpu(c, num_sms=1)
-    # the weights round alike but for their references (2^-8 of sum p |v|, |v| < 6, and two roundings of out)
-    assert (whole.run().float() - out.float()).abs().max() <= 6 * 2 * 2.0 ** -8

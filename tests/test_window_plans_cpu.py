@@ -128,29 +128,3 @@ def test_drawn_steps_are_read_once(seed, code):
         seq = [x + int(2 ** rng.uniform(0, 13)) - 1 for x in q]
         check_plan(desc(q, seq, int(2 ** rng.uniform(0, 13)), int(rng.choice([0, 1, 4, 17, 130, 900])), code, hq=hq, hkv=hkv,
                         max_blocks_per_req=600, num_sms=rng.choice([1, 3, 20, 152, 152])))
-
-
-@pytest.mark.parametrize("code", [0, 1])
-@pytest.mark.parametrize("hq,hkv", [(32, 8), (64, 8), (32, 1), (48, 16)])
-@pytest.mark.parametrize("rows", [[128], [256], [1300], [600], [60, 60], [9] * 5, [200, 1, 1, 2], [30]])
-@pytest.mark.parametrize("window", [1500, 4096, 8192])
-def test_pieces_stay_inside_the_librarys_scratch(code, hq, hkv, rows, window):
-    """pa_attention_no_alloc takes every windowed step whose whole tiles it takes."""
-    n = len(rows)
-    kw = desc(rows, [9000 - 7 * i for i in range(n)], window, 4, code, hq=hq, hkv=hkv, max_blocks_per_req=600)
-    spread = binding.pa_plan_window(**kw)
-    # (a window of the whole context on one SM: no pieces of tiles; the copies of 8-bit blocks are those of the window)
-    one = binding.pa_plan_window(**{**kw, "num_sms": 1})
-    assert one.info()["num_dequant_blocks"] == spread.info()["num_dequant_blocks"]
-    whole = one.workspace_bytes + 152 * 2 * hkv * hq * 130 * 4 * (1 in rows)
-    if whole <= binding.NO_ALLOC_SCRATCH_BYTES:
-        assert spread.workspace_bytes <= binding.NO_ALLOC_SCRATCH_BYTES
-    if (hq, window) == (32, 8192):
-        check_plan(kw)
-
-
-def test_a_chunk_is_still_cut_where_its_pieces_fit():
-    """128 tokens of 32 heads: in pieces that the scratch holds, not in none."""
-    kw = desc([128], [9000], 8192, 0, hq=32, hkv=8, max_blocks_per_req=600)
-    info = binding.pa_plan_window(**kw).info()
-    assert info["num_merge_rows"] == 128 and info["num_extend_tiles"] > 100
