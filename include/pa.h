@@ -784,7 +784,10 @@ pa_status pa_plan_kernel_times(pa_plan_t *plan, double ms_total[4], int32_t laun
  *   stream             cudaStream_t
  * Returns PA_ERR_WORKSPACE_TOO_SMALL, before enqueueing anything, when the
  * plan's workspace_bytes exceeds PA_NO_ALLOC_SCRATCH_BYTES; otherwise as
- * pa_attention.
+ * pa_attention.  A windowed plan (pa_plan_window without a shape) whose pieces of
+ * tiles alone take it past that size goes with fewer of them, or none, planned by the
+ * plan's first such call and kept with it; the result then differs from
+ * pa_attention's within rounding.
  *
  * The first call on a device (made with that device current) looks up the
  * array's device address; make that first call before any stream capture.

@@ -13,7 +13,8 @@
 // process exits.  Its device address is looked up once per device (on the
 // first call made with that device current) and passed to the same kernels
 // pa_attention launches.  Nothing here allocates: no cudaMalloc, no
-// cudaMallocHost, no cudaFree, no event creation.
+// cudaMallocHost, no cudaFree, no event creation (host memory, once for a
+// plan whose step scratch_plan plans anew).
 #include <cstring>
 #include <mutex>
 
@@ -67,7 +68,8 @@ extern "C" pa_status pa_attention_no_alloc(const pa_plan_t *plan, const void *q,
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(key_cache, 16) || !aligned(value_cache, 16) ||
         !aligned(block_table, 4) || (device_error_word && !aligned(device_error_word, 4)))
         return PA_ERR_INVALID_ARGUMENT;
-    if (P->ws_bytes > kScratchBytes) return PA_ERR_WORKSPACE_TOO_SMALL;  // plan needs more than the array
+    P = scratch_plan(P);
+    if (!P) return PA_ERR_WORKSPACE_TOO_SMALL;  // the step needs more than the array
     cudaStream_t stream = static_cast<cudaStream_t>(stream_);
     void *scratch = nullptr;
     pa_status st = scratch_address(&scratch);

@@ -1,6 +1,7 @@
 // The plan object behind the opaque pa_plan_t of pa.h (host only), and the
 // host helpers the entry points share.
 #pragma once
+#include <memory>
 #include <mutex>
 #include <vector>
 
@@ -59,6 +60,16 @@ struct pa_plan_s {
     size_t pinned_cap = 0;
     cudaEvent_t upload_evt = nullptr;   // recorded after each upload from `pinned`
     pa_plan_info info{};
+    // windowed plans that pieces of tiles take past the library's scratch: their step, and
+    // its plan for that scratch once asked for (scratch_plan)
+    struct Step {
+        pa_batch_desc desc;
+        pa_window_desc window;
+        std::vector<int32_t> qsl, seq_lens, num_computed;
+    };
+    int64_t tile_partials = 0;          // partials of a token that pieces of tiles make
+    std::unique_ptr<Step> step;
+    std::unique_ptr<pa_plan_s> for_scratch;
     // timing
     bool timing = false;
     std::vector<cudaEvent_t> ev_start[4], ev_stop[4];
@@ -113,6 +124,10 @@ struct SideStream {
     cudaEvent_t fork = nullptr, join = nullptr;
 };
 SideStream *side_stream();
+
+// The plan by which the step runs in the library's scratch: P, or one with fewer pieces
+// of tiles that P keeps; null where the step does not fit.
+pa_plan_s *scratch_plan(pa_plan_s *P);
 
 // Set the kernel attributes the plan's launches need (once per plan).
 pa_status prepare_plan(pa_plan_s *P);

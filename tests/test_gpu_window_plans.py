@@ -5,6 +5,7 @@ import torch
 
 import window_common as wc
 from gpu_common import ensure_library
+from paged_kv_cache_16_gb300 import binding
 
 pytestmark = pytest.mark.gpu
 
@@ -27,3 +28,23 @@ def test_short_tiles_in_more_rounds_than_one(code, n, q, seq, window, sinks, lay
     lens = [seq + i % 7 for i in range(n)]
     wc.check(wc.WindowCase(hq=hq, hkv=hkv, d=128 if code == "e4m3" else d, q_lens=[q] * n, seq_lens=lens, code=code,
                            window=window, sinks=sinks, seed=n), num_sms=num_sms)
+
+
+@pytest.mark.parametrize("q_len", [128, 256])
+def test_long_windows_without_a_workspace(q_len):
+    """Chunks whose pieces outgrow the library's scratch: the call without a workspace
+    takes them, and gives the same bits each time."""
+    c = wc.WindowCase(hq=32, hkv=8, d=128, q_lens=[q_len], seq_lens=[9000], code="bf16", window=8192, sinks=0, seed=q_len)
+    g = wc.OnGpu(c)
+    out = g.run().clone()
+    assert g.plan.workspace_bytes > binding.NO_ALLOC_SCRATCH_BYTES
+    word = torch.zeros(1, dtype=torch.int32, device="cuda")
+    again = [torch.zeros_like(out) for _ in range(2)]
+    for x in again:
+        binding.pa_attention_no_alloc(g.plan, g.q, g.kc, g.vc, g.table, x, word)
+        assert int(word) == 0
+    assert torch.equal(*again)
+    # both round each weight to 2^-8 of it, relative to other maxima: out by 2^-8 of sum p |v| each (|v| < 6), and half a
+    # step of out each
+    assert (again[0].float() - out.float()).abs().max() <= 6 * 4 * 2.0 ** -8
+    assert torch.equal(g.run(), out)

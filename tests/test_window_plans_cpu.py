@@ -2,10 +2,11 @@
 import random
 
 import pytest
+import torch
 
 import plan_image as pi
 from paged_kv_cache_16_gb300 import binding, build
-from test_window_cpu import desc
+from test_window_cpu import FAKE, desc
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -128,3 +129,28 @@ def test_drawn_steps_are_read_once(seed, code):
         seq = [x + int(2 ** rng.uniform(0, 13)) - 1 for x in q]
         check_plan(desc(q, seq, int(2 ** rng.uniform(0, 13)), int(rng.choice([0, 1, 4, 17, 130, 900])), code, hq=hq, hkv=hkv,
                         max_blocks_per_req=600, num_sms=rng.choice([1, 3, 20, 152, 152])))
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the pointers lead nowhere")
+@pytest.mark.parametrize("code", [0, 1])
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (64, 8), (32, 1), (48, 16)])
+@pytest.mark.parametrize("rows", [[128], [256], [1300], [600], [60, 60], [9] * 5, [200, 1, 1, 2], [30], [3000]])
+@pytest.mark.parametrize("window", [1500, 4096, 8192])
+def test_pieces_of_tiles_do_not_outgrow_the_librarys_scratch(lib, code, hq, hkv, rows, window):
+    """pa_attention_no_alloc takes every windowed step whose whole tiles fit its scratch
+    (here it ends where it asks for a device), and refuses the others."""
+    n, scratch = len(rows), binding.NO_ALLOC_SCRATCH_BYTES
+    kw = desc(rows, [9000 - 7 * i for i in range(n)], window, 4, code, hq=hq, hkv=hkv, max_blocks_per_req=600)
+    plan, whole = binding.pa_plan_window(**kw), binding.pa_plan_window(**{**kw, "num_sms": 1})
+    decode = 2 * 152 * (-(-hkv // 8)) * hq * 130 * 4 * (1 in rows)      # more partials of split-KV rows on more SMs
+    statuses = set()
+    for _ in range(2):
+        statuses.add(lib.pa_attention_no_alloc(plan.handle, FAKE, FAKE, FAKE, FAKE, FAKE, None, None))
+    assert len(statuses) == 1
+    status = statuses.pop()
+    if whole.workspace_bytes + decode <= scratch:
+        assert status == binding.PA_ERR_CUDA
+    elif whole.workspace_bytes > scratch:
+        assert status == binding.PA_ERR_WORKSPACE_TOO_SMALL
+    else:
+        assert status in (binding.PA_ERR_CUDA, binding.PA_ERR_WORKSPACE_TOO_SMALL)
