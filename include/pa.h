@@ -277,7 +277,10 @@ pa_status pa_write_kv_fp8(const void *key, const void *value, const int64_t *slo
  * request's last block are never used (their contents may be anything,
  * including NaN).  A NaN or infinity among the values of a step's own rows may
  * reach rows of the same request that stand up to 255 tokens before it in the step
- * (a weight of 0 times it).  Returns PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_INVALID_ARGUMENT
+ * (a weight of 0 times it).  What is rounded beside the output: softmax weights, to
+ * bf16, over E4M3 caches in decode and verify rows to f16; there queries too, to f16
+ * with their row's power of two (exact down to 2^-17 of the row's largest magnitude,
+ * or of 1 where that is within [1, 2^16)).  Returns PA_ERR_WORKSPACE_TOO_SMALL, PA_ERR_INVALID_ARGUMENT
  * (NULL or misaligned pointer) or PA_ERR_CUDA (launch failure).  Equivalent to
  * pa_upload_metadata then pa_attention_launch, plus the optional timing events.
  *

@@ -49,8 +49,35 @@ struct DecodeCfg {
     static constexpr int SMEM = decode_smem_bytes(D, HG, KV8);
 };
 
-// bf16 pair -> f16 pair (saturating at the largest finite f16)
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) { return pack_f16x2_sat(bf16_lo(w), bf16_hi(w)); }
+// E4M3 caches take queries as f16, whose range bf16 outgrows at both ends: a row whose
+// largest magnitude lies outside [1, 2^16) is taken times a power of two that puts it
+// into [1, 2) (the largest of bf16: below 4), and the factor returns with its scores.
+// Exact for elements down to 2^-17 (of that power, where the row is scaled); smaller
+// ones are at most 2^-25 off.  (0.1 to 0.9% of a step's time, by the maximum at each
+// item's start: single tokens of 64 requests 51.5 us instead of 51.4, 4 tokens each 64.3
+// instead of 63.9; four chains for the maximum 64.4, queries converted before it 64.5.)
+struct QueryFactor {
+    float down, up;
+    __device__ __forceinline__ explicit QueryFactor(float amax) : down(1.f), up(1.f) {
+        int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127;
+        if ((e >= 0 && e <= 15) || amax == 0.f) return;
+        e = min(max(e, -126), 126);
+        down = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        up = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+    }
+    // (times 1 is left out where it is all rows' of the warp: verify rows take 0.8 to 1.5% otherwise)
+    template <bool SCALED>
+    __device__ __forceinline__ uint32_t f16x2(uint32_t w) const {
+        return SCALED ? pack_f16x2(bf16_lo(w) * down, bf16_hi(w) * down) : pack_f16x2(bf16_lo(w), bf16_hi(w));
+    }
+    // factor of a score (above 0, or a masked one would become NaN)
+    __device__ __forceinline__ float score(float scale_log2) const { return fmaxf(scale_log2 * up, 1.17549435e-38f); }
+};
+// largest magnitude of a row, from a quad's lanes
+__device__ __forceinline__ float quad_max(float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+}
 
 // Fused cache update of one decode row (pa_attention_with_kv_update; the
 // fused dispatch of "vLLM 推理流程分析" §6.1, the write of §6.3): the item
@@ -224,7 +251,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const uint32_t k_lane = g * 128u + 4u * t4;   // key g at +0, key g + 8 at +1024
         const uint32_t va_lane = 256u * t4 + 16u * (g >> 2) + 4u * (g & 3);             // key 2t
         const uint32_t vb_lane = 256u * t4 + 128u + 16u * ((g >> 2) ^ 1) + 4u * (g & 3);  // key 2t + 1
-        const float sl2 = p.scale_log2;  // > 0: the maximum of raw scores scales
         int consumed = 0;
         bool ok = true;
         for (int it = item_begin; it < item_end && ok; ++it) {
@@ -251,12 +277,27 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 const uint16_t *qg =
                     p.q + (static_cast<int64_t>(item.token + g / G) * p.num_heads_q + kvh * G + g % G) * D;
                 uint32_t qt[D / 16][2];
+                float amax = 0.f;
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const int c = kk * 16 + 4 * t4;
-                    qt[kk][0] = g < nrow ? bf16x2_to_f16x2(__ldg(reinterpret_cast<const uint32_t *>(qg + c))) : 0u;
-                    qt[kk][1] = g < nrow ? bf16x2_to_f16x2(__ldg(reinterpret_cast<const uint32_t *>(qg + c + 2))) : 0u;
-                }
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t w = g < nrow ? __ldg(reinterpret_cast<const uint32_t *>(qg + kk * 16 + 4 * t4 + 2 * e)) : 0u;
+                        qt[kk][e] = w;
+                        amax = max3(amax, fabsf(bf16_lo(w)), fabsf(bf16_hi(w)));
+                    }
+                const QueryFactor factor(quad_max(amax));
+                auto convert = [&](auto scaled) {
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) qt[kk][e] = factor.template f16x2<decltype(scaled)::value>(qt[kk][e]);
+                };
+                if (__any_sync(0xffffffffu, factor.up != 1.f)) convert(std::true_type{});
+                else convert(std::false_type{});
+                // of scores of rows n0 and n1 (> 0: the maximum of raw scores scales)
+                const float up = factor.score(p.scale_log2);
+                const float sla = __shfl_sync(0xffffffffu, up, 4 * n0), slb = __shfl_sync(0xffffffffu, up, 4 * n1);
                 float ot[D / 16][4];
 #pragma unroll
                 for (int j = 0; j < D / 16; ++j) ot[j][0] = ot[j][1] = ot[j][2] = ot[j][3] = 0.f;
@@ -373,8 +414,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, o));
                         mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, o));
                     }
-                    mx0 *= sl2;
-                    mx1 *= sl2;
+                    mx0 *= sla;
+                    mx1 *= slb;
                     // rescale only when the running maximum grows by more than 2^8
                     const bool need0 = mx0 > ma + 8.f;
                     const bool need1 = mx1 > mb + 8.f;
@@ -393,8 +434,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                     // P^T of a block as B fragments: the packed weights of keys
                     // g (and g + 8) x rows (n0, n1), transposed 8x8
                     auto weights = [&](const float (&s)[4], uint32_t &b0, uint32_t &b1) {
-                        b0 = movmatrix_trans(pack_f16x2(ex2(fmaf(s[0], sl2, -ra)), ex2(fmaf(s[1], sl2, -rb))));
-                        b1 = movmatrix_trans(pack_f16x2(ex2(fmaf(s[2], sl2, -ra)), ex2(fmaf(s[3], sl2, -rb))));
+                        b0 = movmatrix_trans(pack_f16x2(ex2(fmaf(s[0], sla, -ra)), ex2(fmaf(s[1], slb, -rb))));
+                        b1 = movmatrix_trans(pack_f16x2(ex2(fmaf(s[2], sla, -ra)), ex2(fmaf(s[3], slb, -rb))));
                     };
                     uint32_t pa0, pa1;
                     weights(sa, pa0, pa1);
@@ -483,18 +524,31 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             const int lim0 = min(item.key_end, item.key_end - (item.n_tok - 1 - tok0));
             const int lim1 = min(item.key_end, item.key_end - (item.n_tok - 1 - tok1));
             const int lim_min = item.key_end - (item.n_tok - 1);
-            uint32_t qf[D / 16][4];
+            uint32_t qf[D / 16][4];   // rows g and g + 8 in turn
+            float amax[2] = {0.f, 0.f};
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                const int c = kk * 16 + 4 * t4;
-                auto ld = [&](const uint16_t *row, int col) {
-                    return bf16x2_to_f16x2(__ldg(reinterpret_cast<const uint32_t *>(row + col)));
-                };
-                qf[kk][0] = g < nrow ? ld(q0, c) : 0u;
-                qf[kk][1] = g + 8 < nrow ? ld(q1, c) : 0u;
-                qf[kk][2] = g < nrow ? ld(q0, c + 2) : 0u;
-                qf[kk][3] = g + 8 < nrow ? ld(q1, c + 2) : 0u;
-            }
+            for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint16_t *row = e & 1 ? q1 : q0;
+                    const uint32_t w = g + 8 * (e & 1) < nrow
+                                           ? __ldg(reinterpret_cast<const uint32_t *>(row + kk * 16 + 4 * t4 + (e & 2)))
+                                           : 0u;
+                    qf[kk][e] = w;
+                    amax[e & 1] = max3(amax[e & 1], fabsf(bf16_lo(w)), fabsf(bf16_hi(w)));
+                }
+            const QueryFactor f0(quad_max(amax[0])), f1(quad_max(amax[1]));
+            auto convert = [&](auto scaled) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        qf[kk][e] = (e & 1 ? f1 : f0).template f16x2<decltype(scaled)::value>(qf[kk][e]);
+            };
+            if (__any_sync(0xffffffffu, f0.up != 1.f || f1.up != 1.f)) convert(std::true_type{});
+            else convert(std::false_type{});
+            // of their scores (> 0: the maximum of raw scores scales)
+            const float sl0 = f0.score(p.scale_log2), sl1 = f1.score(p.scale_log2);
             float o[D / 8][4];
 #pragma unroll
             for (int j = 0; j < D / 8; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
@@ -598,8 +652,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 }
                 mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 1));
                 mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 1));
-                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2)) * sl2;
-                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2)) * sl2;
+                mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, 2)) * sl0;
+                mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, 2)) * sl1;
                 // rescale only when the running maximum grows by more than 2^8
                 const bool need0 = mx0 > m0 + 8.f;
                 const bool need1 = mx1 > m1 + 8.f;
@@ -618,10 +672,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 uint32_t pa[2][4];
 #pragma unroll
                 for (int b = 0; b < NT / 2; ++b) {
-                    pa[b][0] = pack_f16x2(ex2(fmaf(sc[2 * b][0], sl2, -r0)), ex2(fmaf(sc[2 * b][1], sl2, -r0)));
-                    pa[b][1] = pack_f16x2(ex2(fmaf(sc[2 * b][2], sl2, -r1)), ex2(fmaf(sc[2 * b][3], sl2, -r1)));
-                    pa[b][2] = pack_f16x2(ex2(fmaf(sc[2 * b + 1][0], sl2, -r0)), ex2(fmaf(sc[2 * b + 1][1], sl2, -r0)));
-                    pa[b][3] = pack_f16x2(ex2(fmaf(sc[2 * b + 1][2], sl2, -r1)), ex2(fmaf(sc[2 * b + 1][3], sl2, -r1)));
+                    pa[b][0] = pack_f16x2(ex2(fmaf(sc[2 * b][0], sl0, -r0)), ex2(fmaf(sc[2 * b][1], sl0, -r0)));
+                    pa[b][1] = pack_f16x2(ex2(fmaf(sc[2 * b][2], sl1, -r1)), ex2(fmaf(sc[2 * b][3], sl1, -r1)));
+                    pa[b][2] = pack_f16x2(ex2(fmaf(sc[2 * b + 1][0], sl0, -r0)), ex2(fmaf(sc[2 * b + 1][1], sl0, -r0)));
+                    pa[b][3] = pack_f16x2(ex2(fmaf(sc[2 * b + 1][2], sl1, -r1)), ex2(fmaf(sc[2 * b + 1][3], sl1, -r1)));
                 }
                 const uint32_t vb0 = stage(s0) + C::TSTAGE + warp * C::BOX;
                 const LiveRows<WIN> live0(key0, item.key_end, p.sinks, low_min);
