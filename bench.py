@@ -12,7 +12,9 @@ Beside the main workload the run also measures the other configurations
 cascade route and on the plain route (their time ratio), the prefill half of
 the mixed step alone and the mixed step over E4M3 caches.
 
-Prints ONE JSON line (rank 0).  ``--impl reference`` times the fp64 CPU
+Prints ONE JSON line (rank 0), short enough to survive a log that keeps a few
+kilobytes; ``--details FILE`` writes the whole record, every configuration's
+kernels, rooflines and plans in it.  ``--impl reference`` times the fp64 CPU
 oracle on the host cores instead (bounded samples of the same workload).
 
   python bench.py [--gpus N] [--steps K] [--warmup W] [--workload NAME]
@@ -649,6 +651,38 @@ def per_config_entry(name, wl, kv, args, dev, peaks):
     return entry
 
 
+def short(x):
+    """Numbers to six digits, throughout."""
+    if isinstance(x, dict):
+        return {k: short(v) for k, v in x.items()}
+    if isinstance(x, list):
+        return [short(v) for v in x]
+    return float(f"{x:.6g}") if isinstance(x, float) else x
+
+
+def short_line(record: dict) -> dict:
+    """The line that is printed: the record's contract keys whole (the metric's values
+    unrounded), of the rest what a reader compares first."""
+    def of(d, *keys):
+        return {k: d[k] for k in keys if k in d} if d else None
+
+    roof = ("bound", "achieved", "peak", "unit", "frac", "traffic", "kernel", "launch_ms", "sms")
+    line = of(record, "metric", "value", "unit", "n_gpus", "steps", "warmup", "ms_per_step", "higher_is_better", "scaling",
+              "vs_baseline", "dtype", "data")
+    line["config"] = short(of(record["config"], "workload", "name", "tokens_per_step", "seed", "kv_cache_dtype", "l2", "write",
+                              "launch", "side_by_side", "parallelism"))
+    line["config"]["eager_ms_per_step"] = short(record["config"]["modes"]["eager"]["ms_per_step"])
+    line["roofline"], line["roofline_extend"] = (short(of(record[k], *roof)) for k in ("roofline", "roofline_extend"))
+    line["cpu_baseline"] = short(of(record["cpu_baseline"], "value", "unit", "cores", "kind", "sample"))
+    line["e2e"] = of(record["e2e"], "value", "unit", "h2d_bytes_per_step", "d2h_bytes_per_step", "ms_per_step")
+    line.update(of(record, "gpu_launches", "device_error_bits"))
+    line["clocks"] = short(of(record["clocks"], "sm_mhz", "sm_max_mhz", "reasons", "samples"))
+    if record["per_config"]:   # ms per step, and the dominant kernel's fraction of its measured peak
+        line["per_config"] = {k: [round(c["ms_per_step"], 4), round(c["roofline"]["frac"], 3) if c["roofline"] else None]
+                              for k, c in record["per_config"].items()}
+    return line
+
+
 def run_ours(args, world, rank, local):
     if not torch.cuda.is_available():
         raise SystemExit("bench.py needs a CUDA device (the CUDA library has no CPU path)")
@@ -730,7 +764,10 @@ def run_ours(args, world, rank, local):
                                           "num_prefix_tiles", "num_merge_rows", "kernels_per_call", "side_by_side")},
             "per_config": per_config or None,
         }
-        print(json.dumps(line))
+        if args.details:
+            with open(args.details, "w", encoding="utf-8") as fh:
+                json.dump(line, fh, indent=1)
+        print(json.dumps(short_line(line)))
     return 0
 
 
@@ -753,6 +790,7 @@ def main():
                     help="seconds of oracle time for each per_config entry's cpu_baseline")
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-per-config", action="store_true", help="measure the main workload only")
+    ap.add_argument("--details", metavar="FILE", help="write the whole record there (JSON)")
     args = ap.parse_args()
     if args.warmup < 3:
         ap.error("--warmup must be >= 3")
