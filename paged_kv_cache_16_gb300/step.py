@@ -329,8 +329,9 @@ class GraphStep:
         """Copy a step's request metadata and new rows (and their positions on several
         axes) into the static buffers."""
         if positions is not None:
-            if self.positions is None or positions.shape != (self.positions.shape[0], batch.num_tokens):
-                raise ValueError("positions: [axes, tokens] of a rope of several axes wanted")
+            if self.positions is None or positions.shape != (self.positions.shape[0], batch.num_tokens) or \
+                    positions.dtype not in (torch.int32, torch.int64):   # (copied into int32)
+                raise ValueError("positions: integers [axes, tokens] of a rope of several axes wanted")
             self.positions[:, :batch.num_tokens].copy_(positions)
         _fill({"q": self.q, "key": self.key, "value": self.value, "qsl": self.qsl,
                "num_computed": self.num_computed, "block_table": self.block_table}, batch, q, key, value)

@@ -46,3 +46,21 @@ def test_axes_that_are_no_numbers_of_axes():
     for axes in ([0.5] * 32, [0, 1] * 15):
         with pytest.raises(ValueError, match="axis_of_pair"):
             binding.pa_rope_create_axes(num_axes=2, axis_of_pair=axes, rotary_dim=64)
+
+
+@pytest.mark.parametrize("dtype", [torch.int32, torch.int64, torch.float32, torch.bool])
+def test_graph_steps_take_whole_positions(dtype):
+    """The static buffer of positions takes integers as they are, nothing that a cast would round."""
+    from paged_kv_cache_16_gb300 import workloads
+    from paged_kv_cache_16_gb300.step import GraphStep
+    batch = workloads.tiny("1B", seed=0)
+    rope = binding.pa_rope_create_axes(num_axes=2, axis_of_pair=[0, 1] * 16, rotary_dim=64)
+    gs = GraphStep(num_heads_q=4, num_heads_kv=2, head_dim=64, num_blocks=64, max_blocks_per_req=8, softmax_scale=0.125,
+                   max_tokens=64, max_reqs=8, max_extend_tiles=8, device="cpu", rope=rope)
+    pos = torch.arange(2 * batch.num_tokens).reshape(2, -1)
+    if dtype in (torch.int32, torch.int64):
+        gs.stage(batch, positions=pos.to(dtype))
+        assert torch.equal(gs.positions[:, :batch.num_tokens], pos.int())
+    else:
+        with pytest.raises(ValueError, match="positions"):
+            gs.stage(batch, positions=pos.to(dtype))
