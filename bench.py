@@ -26,6 +26,7 @@ import ctypes
 import hashlib
 import json
 import os
+import re
 import statistics
 import subprocess
 import sys
@@ -84,31 +85,48 @@ PER_CONFIG = [("tiny-1A", "tiny-1A", "bf16"), ("tiny-1B", "tiny", "bf16"), ("dec
               ("long-e4m3", "long", "fp8"), ("verify", "verify", "bf16"), ("verify-e4m3", "verify", "fp8")]
 
 # Per-launch DRAM traffic (dram__bytes_read.sum + dram__bytes_write.sum) of a
-# kernel from one ncu capture, valid only while the kernel source is
-# unchanged (sha256 prefix of the file); the summaries are under profiles/.
+# kernel from one ncu capture, valid only while the kernel's source is
+# unchanged (sha256 prefix of its file and the headers that it includes); the
+# summaries are under profiles/.
 TRAFFIC = {
     # profiles/dram_traffic_decode-and-extend_per-workload.md
-    ("decode", "decode", "bf16", "1050896b2c0b0931"): 643_047_680,
-    ("decode", "decode", "fp8", "1050896b2c0b0931"): 323_490_816,
-    ("decode", "mixed", "bf16", "1050896b2c0b0931"): 4_682_118_912,
-    ("extend", "prefill", "bf16", "3f18040844f97345"): 75_079_168,
-    ("decode", "long", "bf16", "1050896b2c0b0931"): 4_300_052_224,
-    ("decode", "long", "fp8", "1050896b2c0b0931"): 2_151_263_488,
-    ("decode", "cascade", "bf16", "1050896b2c0b0931"): 316_059_648,
-    ("extend", "cascade", "bf16", "3f18040844f97345"): 17_910_016,
-    ("decode", "cascade-off", "bf16", "1050896b2c0b0931"): 333_857_536,
-    ("decode", "verify", "bf16", "1050896b2c0b0931"): 674_432_256,
-    ("decode", "verify", "fp8", "1050896b2c0b0931"): 340_763_904,
-    ("decode", "mixed", "fp8", "1050896b2c0b0931"): 2_336_486_144,
-    ("extend", "mixed", "bf16", "3f18040844f97345"): 77_526_784,
+    ("decode", "decode", "bf16", "5b977f286003672c"): 643_130_112,
+    ("decode", "decode", "fp8", "5b977f286003672c"): 323_657_728,
+    ("decode", "mixed", "bf16", "5b977f286003672c"): 4_680_832_000,
+    ("extend", "prefill", "bf16", "2fb04a385bd989d8"): 75_019_520,
+    ("decode", "long", "bf16", "5b977f286003672c"): 4_300_001_280,
+    ("decode", "long", "fp8", "5b977f286003672c"): 2_150_987_520,
+    ("decode", "cascade", "bf16", "5b977f286003672c"): 316_089_344,
+    ("extend", "cascade", "bf16", "2fb04a385bd989d8"): 17_910_528,
+    ("decode", "cascade-off", "bf16", "5b977f286003672c"): 334_034_944,
+    ("decode", "verify", "bf16", "5b977f286003672c"): 674_532_864,
+    ("decode", "verify", "fp8", "5b977f286003672c"): 341_201_664,
+    ("decode", "mixed", "fp8", "5b977f286003672c"): 2_335_929_088,
+    ("extend", "mixed", "bf16", "2fb04a385bd989d8"): 77_167_104,
 }
 KERNEL_SOURCES = {"decode": "paged_kv_cache_16_gb300/csrc/k_decode.cu",
                   "extend": "paged_kv_cache_16_gb300/csrc/k_extend.cu"}
 
 
+def kernel_files(kind: str) -> list:
+    """The kernel's source and every header that it includes, one through another."""
+    todo, files = [os.path.join(ROOT, KERNEL_SOURCES[kind])], []
+    while todo:
+        path = os.path.normpath(todo.pop())
+        if path in files:
+            continue
+        files.append(path)
+        with open(path, encoding="utf-8") as fh:
+            todo += [os.path.join(os.path.dirname(path), h) for h in re.findall(r'^#include "(.+)"', fh.read(), re.M)]
+    return sorted(files)
+
+
 def source_sha(kind: str) -> str:
-    with open(os.path.join(ROOT, KERNEL_SOURCES[kind]), "rb") as fh:
-        return hashlib.sha256(fh.read()).hexdigest()[:16]
+    sha = hashlib.sha256()
+    for path in kernel_files(kind):
+        with open(path, "rb") as fh:
+            sha.update(fh.read())
+    return sha.hexdigest()[:16]
 
 
 def measured_peaks():

@@ -120,7 +120,7 @@ __device__ __forceinline__ void store_new_row(const DecodeParams &p, const Decod
 // token's window).  Bound by HBM where items have up to 8 rows: 64 requests x 1028 bf16
 // keys (Hkv 8, D 128) 44.5 us with the merge, 5.9 TB/s around the ring's fill and the
 // merge (4 us); 128 requests 79.5, 6.8 TB/s.  128 x 4 tokens over 2051 E4M3 keys (16 rows)
-// 106.5 us, 4.9 TB/s: bound by the consumers' latency (issue slots 33% used, tensor pipe
+// 106.8 us, 4.9 TB/s: bound by the consumers' latency (issue slots 33% used, tensor pipe
 // 27%); two warps per kv head with 8 rows each took 126.5 (every code converted twice,
 // 96 registers).
 template <int D, int HG, bool KV8, bool FUSED, bool WIN>

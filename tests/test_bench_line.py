@@ -1,5 +1,6 @@
-"""What bench.py prints (CPU)."""
+"""What bench.py prints and what its traffic figures are keyed by (CPU)."""
 import json
+import os
 
 import bench
 
@@ -57,3 +58,24 @@ def test_the_printed_line_without_the_optional_parts():
     full = {**record(), "roofline_extend": None, "cpu_baseline": None, "per_config": None}
     line = bench.short_line(full)
     assert line["roofline_extend"] is None and line["cpu_baseline"] is None and "per_config" not in line
+
+
+def test_traffic_figures_are_keyed_by_the_kernels_headers_too():
+    names = {kind: {os.path.basename(f) for f in bench.kernel_files(kind)} for kind in bench.KERNEL_SOURCES}
+    assert {"k_decode.cu", "dev.cuh", "pa_internal.h"} <= names["decode"]
+    assert {"k_extend.cu", "tiles.cuh", "dev.cuh", "pa_internal.h"} <= names["extend"]
+    keys = {(k[0], k[3]) for k in bench.TRAFFIC}
+    assert {kind for kind, _ in keys} == set(bench.KERNEL_SOURCES) and len(keys) == 2   # one source each
+
+
+def test_a_changed_header_changes_the_key(tmp_path, monkeypatch):
+    (tmp_path / "k.cu").write_text('#include "a.cuh"\n#include <cstdio>\n')
+    (tmp_path / "a.cuh").write_text('#include "sub/b.h"\n')
+    (tmp_path / "sub").mkdir()
+    (tmp_path / "sub" / "b.h").write_text('#include "../a.cuh"\n// 1\n')
+    monkeypatch.setattr(bench, "ROOT", str(tmp_path))
+    monkeypatch.setitem(bench.KERNEL_SOURCES, "k", "k.cu")
+    before = bench.source_sha("k")
+    assert [os.path.basename(f) for f in bench.kernel_files("k")] == ["a.cuh", "k.cu", "b.h"]
+    (tmp_path / "sub" / "b.h").write_text('#include "../a.cuh"\n// 2\n')
+    assert bench.source_sha("k") != before
