@@ -934,8 +934,9 @@ pa_status build_plan(pa_plan_s *P, const pa_batch_desc *d, const pa_fixed_shape 
                 n_tiles = std::max(n_tiles, (kend - t.key_begin + kTileKeys - 1) / kTileKeys);
             }
             // between two tiles a CTA spends some steps' time (1 / 2 / 3 / 4 steps
-            // in the cut: 248.4 / 244.5 / 244.2 / 244.4 us for two chunks of 2048
-            // tokens on E4M3, 214.3 / 211.4 / 211.7 / 211.5 on block-scaled codes)
+            // in the cut: 192.8 / 192.4 / 194.3 / 194.4 us for two chunks of 2048
+            // tokens on E4M3, 200.6 / 200.0 / 200.7 / 200.7 on block-scaled codes,
+            // 195.4 / 194.9 / 196.6 / 196.6 on bf16)
             if (t.split) n_tiles = ((n_tiles + 1) / 2 * kSplitStepCost + kJoinCost) / kStepCost;   // (two at a time, and a join)
             cost.push_back({n_tiles + 2, static_cast<int32_t>(i)});
             model.tile_units += n_tiles + 1;
